@@ -35,3 +35,15 @@ from .layer import (  # noqa: F401
     stream_moe,
     workspace_bytes,
 )
+from .block import (  # noqa: F401
+    RouterConfig,
+    expert_ffn_decode_workspace_bytes,
+    moe_dispatch_quantized,
+    moe_expert_ffn_decode,
+    moe_rmsnorm,
+    moe_rmsnorm_backward,
+    moe_router_topk,
+    moe_router_topk_backward,
+    quantized_scales,
+    rmsnorm_backward_workspace_bytes,
+)

@@ -1,4 +1,4 @@
-"""ctypes view of libmoe355.so (include/moe355.h). Marshalling only."""
+"""ctypes view of libmoe355.so (include/moe355.h, include/moe355_block.h). Marshalling only."""
 from __future__ import annotations
 
 import ctypes
@@ -16,6 +16,11 @@ MOE_ERR_TIMEOUT = 4
 MOE_BF16 = 0
 MOE_FP8_E4M3_G128 = 1
 MOE_MXFP4 = 2
+
+MOE_F32 = 16                  # the norm's weight and the router's logits (moe355_block.h)
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_MFMA_TILED = 1
@@ -66,7 +71,18 @@ class TileConfig(ctypes.Structure):
     ]
 
 
-# (name, restype, argtypes) of every exported function
+class RouterConfigT(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("normalize", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+# (name, restype, argtypes) of every function of moe355.h
 _I32, _U32, _SZ, _VP = ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_void_p
 _PP = ctypes.POINTER(PlanT)
 SIGNATURES = [
@@ -100,6 +116,22 @@ SIGNATURES = [
     ("moe_device_cu_count", ctypes.c_int, []),
 ]
 
+# the same for moe355_block.h, the operators around the layer
+_RP = ctypes.POINTER(RouterConfigT)
+BLOCK_SIGNATURES = [
+    ("moe_rmsnorm", ctypes.c_int,
+     [_VP, _VP, _VP, _I32, _I32, _I32, ctypes.c_double, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
+    ("moe_rmsnorm_backward_workspace_bytes", _SZ, [_I32, _I32]),
+    ("moe_rmsnorm_backward", ctypes.c_int, [_VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _SZ, _VP]),
+    ("moe_router_topk", ctypes.c_int, [_VP, _I32, _VP, _I32, _I32, _I32, _RP, _VP, _VP, _VP]),
+    ("moe_router_topk_backward", ctypes.c_int, [_VP, _VP, _I32, _VP, _I32, _I32, _I32, _RP, _VP, _VP]),
+    ("moe_dispatch_quantized", ctypes.c_int,
+     [_VP, _VP, _I32, _I32, _PP, _I32, _VP, _VP, _U32, _VP, _SZ, _VP]),
+    ("moe_expert_ffn_decode_workspace_bytes", _SZ, [_I32, _I32, _I32]),
+    ("moe_expert_ffn_decode", ctypes.c_int,
+     [_VP, _VP, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP]),
+]
+
 _lib = None
 
 
@@ -111,7 +143,7 @@ def load() -> ctypes.CDLL:
             raise ImportError(
                 f"{LIB_PATH} is missing: build it with `python -m combine_moe_dispatch_02_amd.build`")
         lib = ctypes.CDLL(LIB_PATH)
-        for name, res, args in SIGNATURES:
+        for name, res, args in SIGNATURES + BLOCK_SIGNATURES:
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

@@ -27,7 +27,8 @@
 namespace moe {
 
 struct DispatchArgs {
-  const uint16_t* x;
+  const uint16_t* x;           // FMT 3: the rows' codes
+  const uint32_t* x_s;         // FMT 3: the rows' scale words, row-major [T][ceil(H / 128)]
   int32_t T, K, H;
   int32_t tile, tile_shift;
   const int32_t* pos;
@@ -53,11 +54,39 @@ __device__ inline float quad_max(float v) {
 }
 
 // One token's row: read once, stored to each of its local pairs' rows.
-// FMT: 0 bf16 copy, 1 fp8 1x128 groups, 2 MXFP8 1x32 blocks.
+// FMT: 0 bf16 copy, 1 fp8 1x128 groups, 2 MXFP8 1x32 blocks, 3 rows that are codes with
+// scale words already (either format: both move H bytes and a word for 128 columns).
 template <int CPL, int FMT>
 __device__ inline void dispatch_token(const DispatchArgs& a, int t, int p, uint64_t dest, int lane) {
   constexpr bool FP8 = FMT != 0;
   const int H = a.H;
+  if constexpr (FMT == 3) {
+    const int nch = H >> 4;   // 16-byte chunks of 16 codes
+    const int words = (H + 127) >> 7;
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(reinterpret_cast<const uint8_t*>(a.x) + (int64_t)t * H, (uint32_t)H);
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.x_s + (int64_t)t * words, (uint32_t)words * 4u);
+    for (int c0 = 0; c0 < nch; c0 += kWave * CPL) {
+      u32x4 v[CPL];
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) v[i] = buf_load16_nt(xr, (uint32_t)(c0 + i * kWave + lane) * 16u);
+      for (int k = 0; k < a.K; ++k) {
+        if (!((dest >> k) & 1ull)) continue;
+        const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.pool + (int64_t)readlane(p, k) * H, (uint32_t)H);
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) buf_store16(v[i], pr, (uint32_t)(c0 + i * kWave + lane) * 16u);
+      }
+    }
+    for (int g0 = 0; g0 < words; g0 += kWave) {
+      const int g = g0 + lane;
+      const uint32_t w = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr, (uint32_t)g * 4u, 0, 2);
+      for (int k = 0; k < a.K; ++k) {
+        if (!((dest >> k) & 1ull)) continue;
+        uint32_t* srow = static_cast<uint32_t*>(a.pool_s) + scale_word(readlane(p, k), 0, words, a.tile_shift);
+        if (g < words) srow[(int64_t)g << a.tile_shift] = w;
+      }
+    }
+    return;
+  }
   const int nch = H >> 3;  // 16-byte chunks of 8 bf16 in a row
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + (int64_t)t * H, (uint32_t)H * 2u);
   const int64_t out_row_bytes = FP8 ? H : (int64_t)H * 2;
@@ -215,11 +244,12 @@ static void launch_wpb(int wpb, int cpl, int waves, hipStream_t s, const Dispatc
   }
 }
 
-int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
+int launch_dispatch(const void* x, const void* x_s, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
                     void* pool, void* pool_s, uint32_t epoch, const WsLayout& L, char* ws,
                     hipStream_t stream) {
   DispatchArgs a;
   a.x = static_cast<const uint16_t*>(x);
+  a.x_s = static_cast<const uint32_t*>(x_s);
   a.T = p.T;
   a.K = p.K;
   a.H = H;
@@ -237,7 +267,7 @@ int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p
   a.tiles_done = reinterpret_cast<uint32_t*>(ws + L.tiles_done);
   a.epoch = epoch;
   a.err = reinterpret_cast<uint32_t*>(ws + L.err);
-  const int nch = H / 8;
+  const int nch = H / (x_s ? 16 : 8);
   const int cpl = nch <= 64 ? 1 : nch <= 128 ? 2 : nch <= 256 ? 4 : 8;
   const int cus = std::max(1, device_cu_count());
   // tokens per wave: up to 64/K (one pos load per wave and token run), fewer when that
@@ -248,7 +278,9 @@ int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p
   // waves per block: the largest power of two up to 16 that leaves a block per CU
   int wpb = 1;
   while (wpb < 16 && waves / (2 * wpb) >= cus) wpb *= 2;
-  if (dtype == MOE_FP8_E4M3_G128)
+  if (x_s)
+    launch_wpb<3>(wpb, cpl, waves, stream, a);
+  else if (dtype == MOE_FP8_E4M3_G128)
     launch_wpb<1>(wpb, cpl, waves, stream, a);
   else if (dtype == MOE_MXFP4)
     launch_wpb<2>(wpb, cpl, waves, stream, a);

@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include "../../include/moe355_block.h"
 #include "common.h"
 
 namespace moe {
@@ -13,7 +14,8 @@ int check_plan(const moe_plan_t* p);
 int launch_plan(const int32_t* topk_idx, const moe_plan_t& p, const WsLayout& L, char* ws,
                 hipStream_t stream);
 
-int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
+// x_s null: x is bf16; else x holds codes of format dtype and x_s their row-major scale words
+int launch_dispatch(const void* x, const void* x_s, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
                     void* pool, void* pool_s, uint32_t epoch, const WsLayout& L, char* ws,
                     hipStream_t stream);
 
@@ -117,6 +119,26 @@ int launch_pack_weights_t(const void* w, int32_t E, int32_t rows, int32_t K, voi
 int launch_pack_mx_scales(const void* s, int32_t E, int32_t rows, int32_t K, void* out, hipStream_t stream);
 
 int device_cu_count();
+
+// norm.hip
+int launch_rmsnorm(const void* x, const void* res, const void* weight, bool w_f32, int32_t T, int32_t H, double eps,
+                   void* s_out, void* y, float* rstd, int32_t q_dtype, void* q, void* q_s, hipStream_t stream);
+int32_t rmsnorm_backward_blocks(int32_t T);
+int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, bool w_f32, const float* rstd,
+                            const void* d_res, int32_t T, int32_t H, void* dx, float* dweight, void* ws,
+                            hipStream_t stream);
+
+// router.hip
+int launch_router_topk(const void* logits, bool bf16, const float* bias, int32_t T, int32_t E, int32_t K,
+                       const moe_router_config& c, int32_t* idx, float* weights, hipStream_t stream);
+int launch_router_topk_backward(const float* d_weights, const void* logits, bool bf16, const int32_t* idx, int32_t T,
+                                int32_t E, int32_t K, const moe_router_config& c, void* d_logits, hipStream_t stream);
+
+// decode.hip
+size_t decode_ws_bytes(int32_t T, int32_t K, int32_t I);
+int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t H, int32_t I, int32_t K, int32_t begin,
+                             int32_t E, const int32_t* idx, const float* weights, const void* w1, const void* w1_s,
+                             const void* w2, const void* w2_s, void* ws, void* out, hipStream_t stream);
 
 // calib.hip
 int launch_calibrate_mfma(int32_t iters, float* sink, int32_t workgroups, hipStream_t stream);

@@ -393,6 +393,11 @@ class StreamMoE:
             self.pool_s = torch.empty(rows, (H + 127) // 128 * 4, dtype=torch.uint8, device=device)
         self.y_pool = torch.empty(rows, H, dtype=torch.bfloat16, device=device)
         self.out = torch.empty(T, H, dtype=torch.bfloat16, device=device)
+        # decode(): a few tokens straight from the routing
+        self.decode_ws = None
+        if self.dtype == "mxfp4":
+            n = load().moe_expert_ffn_decode_workspace_bytes(min(T, 64), K, I)
+            self.decode_ws = torch.empty(n, dtype=torch.uint8, device=device)
         self.epoch = 0
         # training: G kept by the forward (replaced by dG in backward), and the backward's buffers
         self.train = train
@@ -477,9 +482,42 @@ class StreamMoE:
         self.epoch = (self.epoch % 0xFFFFFFFF) + 1      # 1 .. 2^32-1; 0 is never a valid epoch
         return self.epoch
 
+    def _dispatch(self, x, epoch, stream) -> None:
+        """moe_dispatch of bf16 rows, or moe_dispatch_quantized of (codes, scales)."""
+        if isinstance(x, tuple):
+            from .block import moe_dispatch_quantized
+
+            moe_dispatch_quantized(x[0], x[1], self.plan, self.pool, self.pool_s, epoch, self.ws, self.dtype, stream)
+        else:
+            moe_dispatch(x, self.plan, self.pool, self.pool_s, epoch, self.ws, self.dtype, stream)
+
+    def decode(self, x, topk_idx, topk_weights, w1, w2, w1_scale, w2_scale) -> torch.Tensor:
+        """forward() of a few tokens (mxfp4): any number of rows up to min(T, 64), bf16 or (codes,
+        scales) as moe_rmsnorm quantises them, through the same prepared weights but without plan and
+        pool (moe_expert_ffn_decode), on the current stream. y is not rounded to bf16 before
+        combine, so the results differ from forward()'s by that rounding. Returns the first rows
+        of the layer's ``out``."""
+        from .block import moe_expert_ffn_decode
+
+        if self.dtype != "mxfp4":
+            raise MoeError("StreamMoE.decode", _abi.MOE_ERR_UNSUPPORTED)
+        x, x_s = x if isinstance(x, tuple) else (x, None)
+        if x.shape[0] > self.T:
+            raise ValueError(f"{x.shape[0]} rows, the layer was built for {self.T}")
+        if topk_idx.dtype != torch.int32:
+            topk_idx = topk_idx.to(torch.int32)
+        if topk_idx.shape[1:] != (self.K,) or w1.shape[0] != self.E_local:
+            raise ValueError("topk_idx [rows, K] / w1 [E_local, 2I, H/2] do not match the layer")
+        out = self.out[:x.shape[0]]
+        moe_expert_ffn_decode(x, x_s, topk_idx, topk_weights, w1, w1_scale, w2, w2_scale, self.decode_ws, out,
+                              self.expert_begin)
+        return out
+
     def forward(self, x, topk_idx, topk_weights, w1, w2, w1_scale=None, w2_scale=None,
                 streams=None) -> torch.Tensor:
-        """One layer. Weights and scales come from prepare_weights(). ``streams=(compute, comm)`` runs
+        """One layer. x is bf16 [T, H] or, in fp8 and mxfp4 mode, rows that are quantised already:
+        (codes [T, H], scales) as moe_rmsnorm writes them. Weights and scales come from
+        prepare_weights(). ``streams=(compute, comm)`` runs
         plan/dispatch/combine on comm and the FFN on compute, ordered by events, with GEMM A
         claiming pool tiles as dispatch raises their flags (its grid then leaves CUs free for
         dispatch); None runs everything on the current stream. Asynchronous: device errors are
@@ -490,7 +528,7 @@ class StreamMoE:
         if streams is None:
             s = torch.cuda.current_stream()
             moe_plan(topk_idx, self.plan, self.ws, s)
-            moe_dispatch(x, self.plan, self.pool, self.pool_s, epoch, self.ws, self.dtype, s)
+            self._dispatch(x, epoch, s)
             if self.combine_on_completion:
                 moe_expert_ffn_combine(self.plan, self.pool, self.pool_s, w1, w1_scale, w2, w2_scale, epoch,
                                        self.ws, self.y_pool, topk_weights, self.out, self.dtype, self.cfg, s)
@@ -509,7 +547,7 @@ class StreamMoE:
         moe_plan(topk_idx, self.plan, self.ws, comm)
         planned = torch.cuda.Event()
         planned.record(comm)
-        moe_dispatch(x, self.plan, self.pool, self.pool_s, epoch, self.ws, self.dtype, comm)
+        self._dispatch(x, epoch, comm)
         compute.wait_event(planned)
         ccfg = self._concurrent_cfg()
         if self.combine_on_completion:
