@@ -16,7 +16,7 @@ import torch
 
 from . import _abi
 from ._abi import MOE_BF16, MOE_F32, MOE_FP8_E4M3_G128, MOE_MXFP4, check, load
-from .layer import Plan, Workspace, _dtype_code, _need_cuda, _vp
+from .layer import Plan, Workspace, _dtype_code, _need_cuda
 
 __all__ = [
     "RouterConfig", "moe_rmsnorm", "moe_rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "moe_router_topk",
@@ -25,51 +25,68 @@ __all__ = [
 ]
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _launch(name: str, tensors, stream, *args) -> None:
-    """Call entry point ``name`` on the tensors' device, the stream as its last argument."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name}: tensors are on {dev} and {t.device}")
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device index of a call's first tensor."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return d
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dev: int, shape, dtype) -> Optional[int]:
+    """The address of a checked tensor (None for None): on device ``dev``, dense, of shape and dtype
+    (a dtype or a tuple of them). One line of cheap tests, since a token's call is all launch."""
+    if t is None:
+        return None
+    if (t.get_device() == dev and t.is_contiguous() and t.shape == shape
+            and (t.dtype is dtype or (dtype.__class__ is tuple and t.dtype in dtype))):
+        return t.data_ptr()
+    _need_cuda(t, name, dtype)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the call's first tensor on {dev}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _bytes(t: Optional[torch.Tensor], name: str, dev: int):
+    """(address, bytes) of a workspace; (None, 0) for None."""
+    return (None, 0) if t is None else (_ptr(t, name, dev, t.shape, _U8), t.numel())
+
+
+def _launch(name: str, dev: int, stream, *args) -> None:
+    """Call entry point ``name`` on device ``dev``, the stream as its last argument."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != dev:
-            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on {dev}")
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != dev:
+            raise ValueError(f"{name}: the stream is on {stream.device}, the tensors are on device {dev}")
         stream = stream.cuda_stream
     fn = getattr(load(), name)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, ctypes.c_void_p(int(stream)))
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, ctypes.c_void_p(int(stream)))
-    check(name, status)
-
-
-def _shaped(t: torch.Tensor, name: str, shape, dtype) -> None:
-    _need_cuda(t, name, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+            status = fn(*args, stream)
+    if status:
+        check(name, status)
 
 
 def _real_dtype(t: torch.Tensor, name: str) -> int:
-    _need_cuda(t, name, (torch.bfloat16, torch.float32))
-    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+    if t.dtype is _F32:
+        return MOE_F32
+    if t.dtype is _BF16:
+        return MOE_BF16
+    raise ValueError(f"{name} has dtype {t.dtype}, expected bf16 or fp32")
 
 
-def _scale_words(q_s: torch.Tensor, name: str, T: int, H: int, code: int) -> None:
+def _scales(q_s: Optional[torch.Tensor], name: str, dev: int, T: int, H: int, code: int) -> Optional[int]:
     """Row-major scale words: fp32 [T, ceil(H/128)] (fp8) or bytes [T, 4 ceil(H/128)] (mxfp4)."""
     words = (H + 127) // 128
     if code == MOE_FP8_E4M3_G128:
-        _shaped(q_s, name, (T, words), torch.float32)
-    else:
-        _shaped(q_s, name, (T, 4 * words), torch.uint8)
+        return _ptr(q_s, name, dev, (T, words), _F32)
+    return _ptr(q_s, name, dev, (T, 4 * words), _U8)
 
 
 def quantized_scales(T: int, H: int, dtype, device="cuda") -> torch.Tensor:
@@ -87,26 +104,19 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: Optional[t
     """y = rms_norm(s) * weight with s = x + res (s goes to ``res_out``), and its copy (q, q_s) in
     the activation format ``dtype`` ("fp8" or "mxfp4"); rstd for the backward pass. x, res, res_out, y:
     bf16 [T, H]; weight: bf16 or fp32 [H]; q: codes [T, H]; q_s: see quantized_scales()."""
-    _need_cuda(x, "x", torch.bfloat16)
+    dev = _device(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    code = _dtype_code(dtype)
+    shape = x.shape
+    T, H = shape
+    code = MOE_BF16 if dtype == "bf16" else _dtype_code(dtype)
     wcode = _real_dtype(weight, "weight")
-    if weight.shape != (H,):
-        raise ValueError("weight must be [H]")
-    for t, n in ((res, "res"), (res_out, "res_out"), (y, "y")):
-        if t is not None:
-            _shaped(t, n, (T, H), torch.bfloat16)
-    if rstd is not None:
-        _shaped(rstd, "rstd", (T,), torch.float32)
-    if q is not None:
-        _shaped(q, "q", (T, H), _CODES)
-    if q_s is not None:
-        _scale_words(q_s, "q_s", T, H, code)
-    _launch("moe_rmsnorm", (x, res, weight, res_out, y, rstd, q, q_s), stream,
-            _vp(x), _vp(res), _vp(weight), wcode, T, H, float(eps), _vp(res_out), _vp(y), _vp(rstd), code, _vp(q),
-            _vp(q_s))
+    _launch("moe_rmsnorm", dev, stream,
+            _ptr(x, "x", dev, shape, _BF16), _ptr(res, "res", dev, shape, _BF16),
+            _ptr(weight, "weight", dev, (H,), weight.dtype), wcode, T, H, eps,
+            _ptr(res_out, "res_out", dev, shape, _BF16), _ptr(y, "y", dev, shape, _BF16),
+            _ptr(rstd, "rstd", dev, (T,), _F32), code, _ptr(q, "q", dev, shape, _CODES),
+            _scales(q_s, "q_s", dev, T, H, code))
 
 
 def rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
@@ -119,24 +129,18 @@ def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
     """Gradients of moe_rmsnorm: dx (of x and of res) with the stream's own gradient d_res added, and
     dweight fp32 [H] (written, not added to), for which ws is a byte tensor of
     rmsnorm_backward_workspace_bytes(T, H). s is res_out of the forward (x where there was no residual)."""
-    _need_cuda(dy, "dy", torch.bfloat16)
+    dev = _device(dy, "dy")
     if dy.dim() != 2:
         raise ValueError("dy must be [T, H]")
-    T, H = dy.shape
+    shape = dy.shape
+    T, H = shape
     wcode = _real_dtype(weight, "weight")
-    if weight.shape != (H,):
-        raise ValueError("weight must be [H]")
-    for t, n in ((s, "s"), (dx, "dx"), (d_res, "d_res")):
-        if t is not None:
-            _shaped(t, n, (T, H), torch.bfloat16)
-    _shaped(rstd, "rstd", (T,), torch.float32)
-    if dweight is not None:
-        _shaped(dweight, "dweight", (H,), torch.float32)
-    if ws is not None:
-        _need_cuda(ws, "ws", torch.uint8)
-    _launch("moe_rmsnorm_backward", (dy, s, weight, rstd, d_res, dx, dweight, ws), stream,
-            _vp(dy), _vp(s), _vp(weight), wcode, _vp(rstd), _vp(d_res), T, H, _vp(dx), _vp(dweight), _vp(ws),
-            0 if ws is None else ws.numel())
+    ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
+    _launch("moe_rmsnorm_backward", dev, stream,
+            _ptr(dy, "dy", dev, shape, _BF16), _ptr(s, "s", dev, shape, _BF16),
+            _ptr(weight, "weight", dev, (H,), weight.dtype), wcode, _ptr(rstd, "rstd", dev, (T,), _F32),
+            _ptr(d_res, "d_res", dev, shape, _BF16), T, H, _ptr(dx, "dx", dev, shape, _BF16),
+            _ptr(dweight, "dweight", dev, (H,), _F32), ws_ptr, ws_bytes)
 
 
 @dataclass(frozen=True)
@@ -151,6 +155,7 @@ class RouterConfig:
     scale: float = 1.0         # factor of the weights
 
     def c(self) -> _abi.RouterConfigT:
+        """The C struct, made once (the fields cannot change)."""
         got = self.__dict__.get("_c")
         if got is None:
             if self.score not in ("softmax", "sigmoid"):
@@ -167,51 +172,49 @@ def moe_router_topk(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: 
     """topk_idx int32 [T, K] and topk_weights fp32 [T, K] of the experts chosen by logits [T, E]
     (fp32 or bf16) and, in the choice alone, bias fp32 [E]. -1 with weight 0 where a token's
     experts are used up (logits of -inf or NaN switch an expert off)."""
+    dev = _device(logits, "logits")
     lcode = _real_dtype(logits, "logits")
     if logits.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("logits must be [T, E], topk_idx [T, K]")
     (T, E), K = logits.shape, topk_idx.shape[1]
-    _shaped(topk_idx, "topk_idx", (T, K), torch.int32)
-    _shaped(topk_weights, "topk_weights", (T, K), torch.float32)
-    if bias is not None:
-        _shaped(bias, "bias", (E,), torch.float32)
-    _launch("moe_router_topk", (logits, bias, topk_idx, topk_weights), stream,
-            _vp(logits), lcode, _vp(bias), T, E, K, ctypes.byref(cfg.c()), _vp(topk_idx), _vp(topk_weights))
+    _launch("moe_router_topk", dev, stream,
+            _ptr(logits, "logits", dev, logits.shape, logits.dtype), lcode, _ptr(bias, "bias", dev, (E,), _F32), T, E, K,
+            cfg.c(), _ptr(topk_idx, "topk_idx", dev, (T, K), _I32), _ptr(topk_weights, "topk_weights", dev, (T, K), _F32))
 
 
 def moe_router_topk_backward(d_topk_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
                              d_logits: torch.Tensor, cfg: RouterConfig = RouterConfig(), *, stream=None) -> None:
     """d_logits [T, E] (in logits' type, every element) from d_topk_weights fp32 [T, K], e.g.
     moe_combine_backward's, for the topk_idx that moe_router_topk wrote with the same cfg."""
+    dev = _device(logits, "logits")
     lcode = _real_dtype(logits, "logits")
     if logits.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("logits must be [T, E], topk_idx [T, K]")
     (T, E), K = logits.shape, topk_idx.shape[1]
-    _shaped(topk_idx, "topk_idx", (T, K), torch.int32)
-    _shaped(d_topk_weights, "d_topk_weights", (T, K), torch.float32)
-    _shaped(d_logits, "d_logits", (T, E), logits.dtype)
-    _launch("moe_router_topk_backward", (d_topk_weights, logits, topk_idx, d_logits), stream,
-            _vp(d_topk_weights), _vp(logits), lcode, _vp(topk_idx), T, E, K, ctypes.byref(cfg.c()), _vp(d_logits))
+    _launch("moe_router_topk_backward", dev, stream,
+            _ptr(d_topk_weights, "d_topk_weights", dev, (T, K), _F32),
+            _ptr(logits, "logits", dev, logits.shape, logits.dtype), lcode, _ptr(topk_idx, "topk_idx", dev, (T, K), _I32),
+            T, E, K, cfg.c(), _ptr(d_logits, "d_logits", dev, logits.shape, logits.dtype))
 
 
 def moe_dispatch_quantized(q: torch.Tensor, q_s: torch.Tensor, plan: Plan, pool: torch.Tensor, pool_s: torch.Tensor,
                            epoch: int, ws: Workspace, dtype, stream=None) -> None:
     """moe_dispatch of rows that are codes [T, H] with row-major scales (quantized_scales()) already."""
+    dev = _device(q, "q")
     code = _dtype_code(dtype)
     if q.dim() != 2 or pool.dim() != 2:
         raise ValueError("q must be [T, H], pool [pool rows, H]")
-    H = q.shape[1]
-    _shaped(q, "q", (plan.T, H), _CODES)
-    if code != MOE_BF16:
-        _scale_words(q_s, "q_s", plan.T, H, code)
-    _shaped(pool, "pool", (pool.shape[0], H), _CODES)
-    _need_cuda(pool_s, "pool_s", (torch.float32, torch.uint8))
-    if pool_s.numel() * pool_s.element_size() < pool.shape[0] * ((H + 127) // 128) * 4:
+    H, rows = q.shape[1], pool.shape[0]
+    for t, n in ((plan.pos, "the plan"), (ws.buf, "ws")):
+        if t.get_device() != dev:
+            raise ValueError(f"{n} is on device {t.get_device()}, q on {dev}")
+    if pool_s.numel() * pool_s.element_size() < rows * ((H + 127) // 128) * 4:
         raise ValueError("pool_s holds fewer scale words than the pool has")
     c = plan.c()
-    _launch("moe_dispatch_quantized", (q, q_s, plan.pos, pool, pool_s, ws.buf), stream,
-            _vp(q), _vp(q_s), H, code, ctypes.byref(c), pool.shape[0], _vp(pool), _vp(pool_s), epoch, _vp(ws.buf),
-            ws.nbytes)
+    _launch("moe_dispatch_quantized", dev, stream,
+            _ptr(q, "q", dev, (plan.T, H), _CODES), None if code == MOE_BF16 else _scales(q_s, "q_s", dev, plan.T, H, code),
+            H, code, ctypes.byref(c), rows, _ptr(pool, "pool", dev, (rows, H), _CODES),
+            _ptr(pool_s, "pool_s", dev, pool_s.shape, (_F32, _U8)), epoch, ws.buf.data_ptr(), ws.nbytes)
 
 
 def expert_ffn_decode_workspace_bytes(T: int, K: int, I: int) -> int:
@@ -226,23 +229,16 @@ def moe_expert_ffn_decode(x: torch.Tensor, x_s: Optional[torch.Tensor], topk_idx
     [T, H] with x_s (moe_rmsnorm's q and q_s), or bf16 with x_s None. Weights and scales as
     moe_pack_weights and moe_pack_mx_scales give them: w1 [E_local, 2I, H/2], w2 [E_local, H, I/2].
     ws: a byte tensor of expert_ffn_decode_workspace_bytes(T, K, I)."""
+    dev = _device(x, "x")
     if x.dim() != 2 or w1.dim() != 3 or topk_idx.dim() != 2:
         raise ValueError("x must be [T, H], w1 [E_local, 2I, H/2], topk_idx [T, K]")
     (T, H), K = x.shape, topk_idx.shape[1]
     E, I = w1.shape[0], w1.shape[1] // 2
-    if x_s is None:
-        _need_cuda(x, "x", torch.bfloat16)
-    else:
-        _need_cuda(x, "x", _CODES)
-        _scale_words(x_s, "x_s", T, H, MOE_MXFP4)
-    _shaped(topk_idx, "topk_idx", (T, K), torch.int32)
-    _shaped(topk_weights, "topk_weights", (T, K), torch.float32)
-    _shaped(w1, "w1", (E, 2 * I, H // 2), torch.uint8)
-    _shaped(w1_s, "w1_s", (E, 2 * I, H // 32), torch.uint8)
-    _shaped(w2, "w2", (E, H, I // 2), torch.uint8)
-    _shaped(w2_s, "w2_s", (E, H, I // 32), torch.uint8)
-    _shaped(out, "out", (T, H), torch.bfloat16)
-    _need_cuda(ws, "ws", torch.uint8)
-    _launch("moe_expert_ffn_decode", (x, x_s, topk_idx, topk_weights, w1, w1_s, w2, w2_s, ws, out), stream,
-            _vp(x), _vp(x_s), MOE_BF16 if x_s is None else MOE_MXFP4, T, H, I, K, expert_begin, E, _vp(topk_idx),
-            _vp(topk_weights), _vp(w1), _vp(w1_s), _vp(w2), _vp(w2_s), _vp(ws), ws.numel(), _vp(out))
+    ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
+    _launch("moe_expert_ffn_decode", dev, stream,
+            _ptr(x, "x", dev, x.shape, _BF16 if x_s is None else _CODES), _scales(x_s, "x_s", dev, T, H, MOE_MXFP4),
+            MOE_BF16 if x_s is None else MOE_MXFP4, T, H, I, K, expert_begin, E,
+            _ptr(topk_idx, "topk_idx", dev, (T, K), _I32), _ptr(topk_weights, "topk_weights", dev, (T, K), _F32),
+            _ptr(w1, "w1", dev, (E, 2 * I, H // 2), _U8), _ptr(w1_s, "w1_s", dev, (E, 2 * I, H // 32), _U8),
+            _ptr(w2, "w2", dev, (E, H, I // 2), _U8), _ptr(w2_s, "w2_s", dev, (E, H, I // 32), _U8),
+            ws_ptr, ws_bytes, _ptr(out, "out", dev, (T, H), _BF16))

@@ -67,10 +67,11 @@ struct Reached {
   uint32_t bits[32];
 };
 
+template <int THREADS = kThreads>
 __device__ inline void find_reached(const DecodeArgs& a, Reached& r) {
   if (threadIdx.x < 32) r.bits[threadIdx.x] = 0;
   __syncthreads();
-  for (int q = threadIdx.x; q < a.T * a.K; q += kThreads) {
+  for (int q = threadIdx.x; q < a.T * a.K; q += THREADS) {
     const int64_t e = (int64_t)a.idx[q] - a.begin;
     const bool local = e >= 0 && e < a.E;
     r.id[q] = local ? (int16_t)e : (int16_t)-1;
@@ -93,37 +94,61 @@ __device__ inline int reached_expert(const Reached& r, int slot) {
   return at * 32 + __builtin_ctz(w);
 }
 
-// bf16 values of column l16 to MXFP8, laid out as mfma_mx takes them: f has the lane's 16 values of
-// K = 16 lhi .. and of K = 64 + 16 lhi .., so a block of 32 is half in this lane and half in lane
-// lhi ^ 1, and the scale of block lhi is found in lanes lhi ^ 2 for lhi 1 and 2. By the whole wave.
-__device__ inline uint32_t quantise_column(const float (&f)[32], int lhi, u32x4& b0, u32x4& b1) {
-  uint32_t m[2] = {0u, 0u};
-#pragma unroll
-  for (int j = 0; j < 32; ++j) m[j >> 4] = max(m[j >> 4], __builtin_bit_cast(uint32_t, f[j]) & 0x7fffffffu);
-  u32x4 c[2];
-  uint32_t byte[2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    m[p] = max(m[p], (uint32_t)__shfl_xor((int)m[p], 16, 64));
-    const bool bad = m[p] >= 0x7f800000u;   // NaN or infinity: the block is NaN
-    const int e = mx_e4m3_shared_exp(__builtin_bit_cast(float, m[p]));
-    const float inv = mx_inv_scale(e);
-    const float* v = f + 16 * p;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      c[p][j] = bad ? 0u : pack_e4m3x4(v[4 * j] * inv, v[4 * j + 1] * inv, v[4 * j + 2] * inv, v[4 * j + 3] * inv);
-    byte[p] = bad ? 255u : (uint32_t)(e + 127);
+// All reached experts, ascending, into `list`: thread e has experts e, e + THREADS, ...
+// Returns their number; a barrier follows.
+template <int THREADS>
+__device__ inline int list_reached(const Reached& r, int16_t* list) {
+  const int lane = lane_id();
+  const int n = lane < 32 ? __popc(r.bits[lane]) : 0;
+  const int upto = wave_inclusive_scan(n);
+  for (int e = threadIdx.x; e < 1024; e += THREADS) {
+    const uint32_t word = r.bits[e >> 5];
+    const int before = __shfl(upto - n, e >> 5, 64) + __popc(word & ((1u << (e & 31)) - 1u));
+    if ((word >> (e & 31)) & 1u) list[before] = (int16_t)e;
   }
-  b0 = c[0];
-  b1 = c[1];
-  const uint32_t other = (uint32_t)__shfl_xor((int)(lhi >= 2 ? byte[0] : byte[1]), 32, 64);
-  return lhi == 0 ? byte[0] : lhi == 3 ? byte[1] : other;
+  return readlane(upto, 63);
+}
+
+// LDS written by lanes of a wave is read by others of the same wave
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // ---------------------------------------------------------------------------------------
-// h: grid (I / 32 column blocks, slots); the waves share K, NG groups of 16 token columns
+// bf16 rows to MXFP8: a lane has 8 values, four lanes a block
 // ---------------------------------------------------------------------------------------
-template <bool XBF16, int NG, int U>
+__global__ __launch_bounds__(256) void decode_quantise_kernel(const uint16_t* x, int32_t chunks, uint8_t* q, uint8_t* q_s) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= chunks) return;                            // chunks % 16 == 0: whole blocks
+  const u32x4 v = reinterpret_cast<const u32x4*>(x)[c];
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(v[i]);
+    f[2 * i + 1] = bf16_hi(v[i]);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __builtin_bit_cast(uint32_t, f[j]) & 0x7fffffffu);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xf, 0xf, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xf, 0xf, false));
+  const bool bad = m >= 0x7f800000u;                  // NaN or infinity: the block is NaN
+  const int e = mx_e4m3_shared_exp(__builtin_bit_cast(float, m));
+  const float inv = mx_inv_scale(e);
+  u32x2 o = {pack_e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
+             pack_e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv)};
+  if (bad) o = u32x2{0u, 0u};
+  reinterpret_cast<u32x2*>(q)[c] = o;
+  if ((threadIdx.x & 3) == 0) q_s[c >> 2] = (uint8_t)(bad ? 255 : e + 127);
+}
+
+// ---------------------------------------------------------------------------------------
+// h: grid (I / 32 column blocks, slots); the waves share K. An expert of more than 16 tokens takes
+// them 16 at a time and reads its weights again (from the caches) for every 16.
+// ---------------------------------------------------------------------------------------
+template <int U>
 __global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
   __shared__ Reached reached;
   __shared__ int16_t s_q[kDecodeTokens];              // the expert's pairs, one of each of its tokens
@@ -155,78 +180,48 @@ __global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
     wr[i] = make_rsrc(w + (int64_t)rb * tiles, tiles);
     sr[i] = make_rsrc(ws + (int64_t)rb * tscales, tscales);
   }
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H * (XBF16 ? 2u : 1u));
-  const __amdgpu_buffer_rsrc_t xsr = make_rsrc(a.x_s, XBF16 ? 0u : (uint32_t)a.T * (uint32_t)KB * 4u);
-  uint32_t xo[NG], xso[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    const int c = g * 16 + l16;
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H);
+  const __amdgpu_buffer_rsrc_t xsr = make_rsrc(a.x_s, (uint32_t)a.T * (uint32_t)KB * 4u);
+
+  for (int c0 = 0; c0 < n; c0 += 16) {
+    const int c = c0 + l16;
     const uint32_t t = c < n ? (uint32_t)s_q[c] / (uint32_t)a.K : 0u;
-    xo[g] = c < n ? t * (uint32_t)a.H * (XBF16 ? 2u : 1u) + (uint32_t)lhi * (XBF16 ? 32u : 16u) : kNowhere;
-    xso[g] = c < n ? t * (uint32_t)KB * 4u + (uint32_t)lhi : kNowhere;
-  }
-
-  f32x4 acc[NG][4];
+    // tokens past the last: past the buffers, zeros
+    const uint32_t xo = c < n ? t * (uint32_t)a.H + (uint32_t)lhi * 16u : kNowhere;
+    const uint32_t xso = c < n ? t * (uint32_t)KB * 4u + (uint32_t)lhi : kNowhere;
+    f32x4 acc[4];
 #pragma unroll
-  for (int g = 0; g < NG; ++g)
+    for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // K blocks wave, wave + 8, ...: at every moment the waves read neighbouring tiles
+    for (int kb0 = wave; kb0 < KB; kb0 += kWaves * U) {
+      u32x4 wt[U][4], b0[U], b1[U];
+      uint32_t wsc[U][4], sb[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // K blocks wave, wave + 8, ...: at every moment the waves read neighbouring tiles
-  for (int kb0 = wave; kb0 < KB; kb0 += kWaves * U) {
-    u32x4 wt[U][4];
-    uint32_t wsc[U][4];
+      for (int u = 0; u < U; ++u) {
+        const uint32_t kb = (uint32_t)(kb0 + u * kWaves);   // past KB: weights past the buffer, zeros
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t kb = (uint32_t)(kb0 + u * kWaves);   // past KB: past the buffer, zeros
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wt[u][i] = buf_load16_nt(wr[i], kb * 1024u + (uint32_t)lane * 16u);
-        wsc[u][i] = buf_load1(sr[i], kb * 64u + (uint32_t)lane);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t kb = (uint32_t)(kb0 + u * kWaves);
-      const bool in = kb < (uint32_t)KB;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (NG > 1 && g * 16 >= n) break;
-        u32x4 b0, b1;
-        uint32_t sb;
-        if constexpr (XBF16) {
-          float f[32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const u32x4 v = buf_load16(xr, in && xo[g] != kNowhere ? xo[g] + kb * 256u + (uint32_t)(j & 1) * 16u + (uint32_t)(j >> 1) * 128u : kNowhere);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f[8 * j + 2 * i] = bf16_lo(v[i]);
-              f[8 * j + 2 * i + 1] = bf16_hi(v[i]);
-            }
-          }
-          sb = quantise_column(f, lhi, b0, b1);
-        } else {
-          const uint32_t o = in && xo[g] != kNowhere ? xo[g] + kb * 128u : kNowhere;
-          b0 = buf_load16(xr, o);
-          b1 = buf_load16(xr, o == kNowhere ? kNowhere : o + 64u);
-          sb = buf_load1(xsr, in && xso[g] != kNowhere ? xso[g] + kb * 4u : kNowhere);
+        for (int i = 0; i < 4; ++i) {
+          wt[u][i] = buf_load16_nt(wr[i], kb * 1024u + (uint32_t)lane * 16u);
+          wsc[u][i] = buf_load1(sr[i], kb * 64u + (uint32_t)lane);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][i] = mfma_mx(wt[u][i], wsc[u][i], b0, b1, sb, acc[g][i]);
+        const bool in = kb < (uint32_t)KB && c < n;
+        b0[u] = buf_load16(xr, in ? xo + kb * 128u : kNowhere);
+        b1[u] = buf_load16(xr, in ? xo + kb * 128u + 64u : kNowhere);
+        sb[u] = buf_load1(xsr, in ? xso + kb * 4u : kNowhere);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = mfma_mx(wt[u][i], wsc[u][i], b0[u], b1[u], sb[u], acc[i]);
     }
-  }
 
-  // the waves' sums, then SwiGLU and the MXFP8 of 32 columns: lane (l16, lhi) has token column
-  // l16 and columns 4 lhi .. + 4 of both tiles of 16
+    // the waves' sums, then SwiGLU and the MXFP8 of 32 columns: lane (l16, lhi) has token column
+    // l16 and columns 4 lhi .. + 4 of both tiles of 16
+    if (c0 > 0) __syncthreads();
 #pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    if (g * 16 >= n) break;
-    if (g > 0) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_red[wave][i][lane] = acc[g][i];
+    for (int i = 0; i < 4; ++i) s_red[wave][i][lane] = acc[i];
     __syncthreads();
-    if (wave != g) continue;
+    if (wave != 0) continue;
     f32x4 s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -247,7 +242,6 @@ __global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
     const bool bad = m >= 0x7f800000u;
     const int ex = mx_e4m3_shared_exp(__builtin_bit_cast(float, m));
     const float inv = mx_inv_scale(ex);
-    const int c = g * 16 + l16;
     if (c < n) {
       const int64_t p = s_q[c];
       uint32_t* d = reinterpret_cast<uint32_t*>(a.h + p * a.I + nb * 32 + lhi * 4);
@@ -258,20 +252,50 @@ __global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
   }
 }
 
+// A token's experts and weights in a lane's registers, so that finding its pair with an expert
+// reads no memory
+struct TokenPairs {
+  int id[16];
+  float w[16];
+  __device__ void load(const DecodeArgs& a, const Reached& r, const float* weights, int t) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const bool on = k < a.K && t < a.T;
+      const int at = on ? t * a.K + k : 0;
+      id[k] = on ? r.id[at] : -1;
+      w[k] = weights[at];
+    }
+  }
+  // the first pair with expert e (-1: none) and the weight of all of them
+  __device__ int find(int e, float& weight) const {
+    int first = -1;
+    weight = 0.f;
+#pragma unroll
+    for (int k = 15; k >= 0; --k) first = id[k] == e ? k : first;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) weight += id[k] == e ? w[k] : 0.f;
+    return first;
+  }
+};
+
 // ---------------------------------------------------------------------------------------
 // out: a workgroup has 16 columns of out for all tokens; its waves share the (expert, K block)
-// pairs evenly, token t is column t % 16 of group t / 16
+// pairs evenly. Up to 16 tokens: token t is column t, so the sums stay in registers.
 // ---------------------------------------------------------------------------------------
-template <int NG, int U>
-__global__ __launch_bounds__(kThreads) void decode_out_kernel(DecodeArgs a) {
+template <int NW, int U>
+__global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
   __shared__ Reached reached;
   __shared__ float s_w[kDecodePairs];
-  __shared__ f32x4 s_red[kWaves][NG][64];
+  __shared__ int16_t s_expert[kDecodePairs];          // the reached experts
+  __shared__ f32x4 s_red[NW][64];
   const int lane = lane_id(), l16 = lane & 15, lhi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int q = threadIdx.x; q < a.T * a.K; q += kThreads) s_w[q] = a.weights[q];
-  find_reached(a, reached);
-  const int slots = readlane(wave_inclusive_scan(lane < 32 ? __popc(reached.bits[lane]) : 0), 63);
+  for (int q = threadIdx.x; q < a.T * a.K; q += 64 * NW) s_w[q] = a.weights[q];
+  find_reached<64 * NW>(a, reached);
+  const int slots = list_reached<64 * NW>(reached, s_expert);
+  TokenPairs pairs;
+  pairs.load(a, reached, s_w, l16);
+  __syncthreads();
 
   const int KB = a.I >> 7;
   const int rb = blockIdx.x;
@@ -279,85 +303,140 @@ __global__ __launch_bounds__(kThreads) void decode_out_kernel(DecodeArgs a) {
   const uint32_t rows = (uint32_t)a.T * (uint32_t)a.K;
   const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, rows * (uint32_t)a.I);
   const __amdgpu_buffer_rsrc_t hsr = make_rsrc(a.h_s, rows * (uint32_t)(a.I >> 5));
-  f32x4 sum[NG];
-#pragma unroll
-  for (int g = 0; g < NG; ++g) sum[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
   const int64_t items = (int64_t)slots * KB;
-  const int first = (int)(items * wave / kWaves), last = (int)(items * (wave + 1) / kWaves);
+  const int first = (int)(items * wave / NW), last = (int)(items * (wave + 1) / NW);
   for (int it = first; it < last;) {
     const int slot = it / KB, kb_first = it - slot * KB;
     const int kb_last = min(KB, kb_first + last - it);
     it += kb_last - kb_first;
-    const int e = reached_expert(reached, slot);
-    // this lane's token in every group: its pair with the expert and the pairs' weight
-    uint32_t ho[NG], hso[NG];
-    float wt[NG];
-    bool mine[NG], any[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int t = g * 16 + l16;
-      int q = -1;
-      float s = 0.f;
-      if (t < a.T)
-        for (int k = 0; k < a.K; ++k)
-          if (reached.id[t * a.K + k] == e) {
-            if (q < 0) q = t * a.K + k;
-            s += s_w[t * a.K + k];
-          }
-      mine[g] = q >= 0;
-      any[g] = ballot(q >= 0) != 0;
-      wt[g] = s;
-      ho[g] = q >= 0 ? (uint32_t)q * (uint32_t)a.I + (uint32_t)lhi * 16u : kNowhere;
-      hso[g] = q >= 0 ? (uint32_t)q * (uint32_t)(a.I >> 5) + (uint32_t)lhi : kNowhere;
-    }
+    const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
+    // this lane's token: its first pair with the expert and its pairs' weight
+    float wt;
+    const int k = pairs.find(e, wt);
+    const int q = k < 0 ? -1 : l16 * a.K + k;
+    const bool mine = q >= 0;
+    const uint32_t ho = (uint32_t)max(q, 0) * (uint32_t)a.I + (uint32_t)lhi * 16u;
+    const uint32_t hso = (uint32_t)max(q, 0) * (uint32_t)(a.I >> 5) + (uint32_t)lhi;
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w2 + ((int64_t)e * (a.H >> 4) + rb) * tiles, tiles);
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.w2_s + ((int64_t)e * (a.H >> 4) + rb) * tscales, tscales);
-    f32x4 acc[NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) acc[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     for (int kb0 = kb_first; kb0 < kb_last; kb0 += U) {
-      u32x4 w[U];
-      uint32_t wsc[U];
+      u32x4 w[U], b0[U], b1[U];
+      uint32_t wsc[U], sb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const bool in = kb0 + u < kb_last;
         const uint32_t kb = (uint32_t)(kb0 + u);
         w[u] = buf_load16_nt(wr, in ? kb * 1024u + (uint32_t)lane * 16u : kNowhere);
         wsc[u] = buf_load1(sr, in ? kb * 64u + (uint32_t)lane : kNowhere);
+        b0[u] = buf_load16(hr, in && mine ? ho + kb * 128u : kNowhere);
+        b1[u] = buf_load16(hr, in && mine ? ho + kb * 128u + 64u : kNowhere);
+        sb[u] = buf_load1(hsr, in && mine ? hso + kb * 4u : kNowhere);
       }
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (!any[g]) continue;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const bool in = mine[g] && kb0 + u < kb_last;
-          const uint32_t kb = (uint32_t)(kb0 + u);
-          const u32x4 b0 = buf_load16(hr, in ? ho[g] + kb * 128u : kNowhere);
-          const u32x4 b1 = buf_load16(hr, in ? ho[g] + kb * 128u + 64u : kNowhere);
-          const uint32_t sb = buf_load1(hsr, in ? hso[g] + kb * 4u : kNowhere);
-          acc[g] = mfma_mx(w[u], wsc[u], b0, b1, sb, acc[g]);
-        }
-      }
+      for (int u = 0; u < U; ++u) acc = mfma_mx(w[u], wsc[u], b0[u], b1[u], sb[u], acc);
     }
     // a token without this expert takes nothing of it, a NaN of its weights neither
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[g][i] += mine[g] ? wt[g] * acc[g][i] : 0.f;
+    for (int i = 0; i < 4; ++i) sum[i] += mine ? wt * acc[i] : 0.f;
   }
 
-#pragma unroll
-  for (int g = 0; g < NG; ++g) s_red[wave][g][lane] = sum[g];
+  s_red[wave][lane] = sum;
   __syncthreads();
-  if (wave >= NG) return;
-  f32x4 s = s_red[0][wave][lane];
+  if (wave != 0) return;
+  f32x4 s = s_red[0][lane];
 #pragma unroll
-  for (int v = 1; v < kWaves; ++v) s += s_red[v][wave][lane];
-  const int t = wave * 16 + l16;
-  if (t < a.T) {
+  for (int v = 1; v < NW; ++v) s += s_red[v][lane];
+  if (l16 < a.T) {
     const u32x2 o = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
-    *reinterpret_cast<u32x2*>(a.out + (int64_t)t * a.H + rb * 16 + lhi * 4) = o;
+    *reinterpret_cast<u32x2*>(a.out + (int64_t)l16 * a.H + rb * 16 + lhi * 4) = o;
+  }
+}
+
+// The same for more than 16 tokens, where an expert has a few of them: its tokens are gathered
+// into columns, and the columns' sums go to the tokens' sums in the wave's part of LDS.
+template <int NW, int U>
+__global__ __launch_bounds__(64 * NW) void decode_out_many_kernel(DecodeArgs a) {
+  __shared__ Reached reached;
+  __shared__ float s_w[kDecodePairs];
+  __shared__ int16_t s_expert[kDecodePairs];          // the reached experts
+  __shared__ f32x4 s_sum[NW][4][kDecodeTokens];       // [wave][columns 4 lhi ..][token]
+  __shared__ int16_t s_pair[NW][kDecodeTokens], s_token[NW][kDecodeTokens];
+  __shared__ float s_weight[NW][kDecodeTokens];
+  const int lane = lane_id(), l16 = lane & 15, lhi = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int q = threadIdx.x; q < a.T * a.K; q += 64 * NW) s_w[q] = a.weights[q];
+  find_reached<64 * NW>(a, reached);
+  const int slots = list_reached<64 * NW>(reached, s_expert);
+  TokenPairs pairs;                                   // lane t: token t
+  pairs.load(a, reached, s_w, lane);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s_sum[wave][i][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int KB = a.I >> 7;
+  const int rb = blockIdx.x;
+  const uint32_t tiles = (uint32_t)KB * 1024u, tscales = (uint32_t)KB * 64u;
+  const uint32_t rows = (uint32_t)a.T * (uint32_t)a.K;
+  const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, rows * (uint32_t)a.I);
+  const __amdgpu_buffer_rsrc_t hsr = make_rsrc(a.h_s, rows * (uint32_t)(a.I >> 5));
+  const int64_t items = (int64_t)slots * KB;
+  const int first = (int)(items * wave / NW), last = (int)(items * (wave + 1) / NW);
+  for (int it = first; it < last;) {
+    const int slot = it / KB, kb_first = it - slot * KB;
+    const int kb_last = min(KB, kb_first + last - it);
+    it += kb_last - kb_first;
+    const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
+    float s;
+    const int k = pairs.find(e, s);
+    const int q = k < 0 ? -1 : lane * a.K + k;
+    const uint64_t has = ballot(q >= 0);
+    const int n = __popcll(has);
+    if (q >= 0) {
+      const int at = mask_rank(has);
+      s_pair[wave][at] = (int16_t)q;
+      s_token[wave][at] = (int16_t)lane;
+      s_weight[wave][at] = s;
+    }
+    wave_sync();
+    const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w2 + ((int64_t)e * (a.H >> 4) + rb) * tiles, tiles);
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.w2_s + ((int64_t)e * (a.H >> 4) + rb) * tscales, tscales);
+    for (int c0 = 0; c0 < n; c0 += 16) {
+      const int c = c0 + l16;
+      const bool mine = c < n;
+      const uint32_t p = mine ? (uint32_t)s_pair[wave][c] : 0u;
+      const uint32_t ho = p * (uint32_t)a.I + (uint32_t)lhi * 16u;
+      const uint32_t hso = p * (uint32_t)(a.I >> 5) + (uint32_t)lhi;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      for (int kb0 = kb_first; kb0 < kb_last; kb0 += U) {
+        u32x4 w[U], b0[U], b1[U];
+        uint32_t wsc[U], sb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool in = kb0 + u < kb_last;
+          const uint32_t kb = (uint32_t)(kb0 + u);
+          w[u] = buf_load16_nt(wr, in ? kb * 1024u + (uint32_t)lane * 16u : kNowhere);
+          wsc[u] = buf_load1(sr, in ? kb * 64u + (uint32_t)lane : kNowhere);
+          b0[u] = buf_load16(hr, in && mine ? ho + kb * 128u : kNowhere);
+          b1[u] = buf_load16(hr, in && mine ? ho + kb * 128u + 64u : kNowhere);
+          sb[u] = buf_load1(hsr, in && mine ? hso + kb * 4u : kNowhere);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc = mfma_mx(w[u], wsc[u], b0[u], b1[u], sb[u], acc);
+      }
+      if (mine) s_sum[wave][lhi][s_token[wave][c]] += s_weight[wave][c] * acc;   // a token has one column
+    }
+    wave_sync();
+  }
+
+  __syncthreads();
+  if (wave >= 4) return;
+  f32x4 s = s_sum[0][wave][lane];
+#pragma unroll
+  for (int v = 1; v < NW; ++v) s += s_sum[v][wave][lane];
+  if (lane < a.T) {
+    const u32x2 o = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+    *reinterpret_cast<u32x2*>(a.out + (int64_t)lane * a.H + rb * 16 + wave * 4) = o;
   }
 }
 
@@ -366,11 +445,6 @@ __global__ __launch_bounds__(kThreads) void decode_out_kernel(DecodeArgs a) {
 // ---------------------------------------------------------------------------------------
 size_t decode_scales_at(int32_t T, int32_t K, int32_t I) { return align_up((size_t)T * K * I, 256); }
 size_t decode_ws_bytes(int32_t T, int32_t K, int32_t I) { return decode_scales_at(T, K, I) + (size_t)T * K * (I / 32); }
-
-template <bool XBF16, int NG, int U>
-static void launch_h(dim3 grid, hipStream_t s, const DecodeArgs& a) {
-  hipLaunchKernelGGL((decode_h_kernel<XBF16, NG, U>), grid, dim3(kThreads), 0, s, a);
-}
 
 int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t H, int32_t I, int32_t K, int32_t begin,
                              int32_t E, const int32_t* idx, const float* weights, const void* w1, const void* w1_s,
@@ -394,16 +468,28 @@ int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t 
   a.h_s = a.h + decode_scales_at(T, K, I);
   a.out = static_cast<uint16_t*>(out);
   const dim3 gh(I / 32, std::min(T * K, E)), go(H / 16);
-  if (x_s) {
-    if (T <= 16) launch_h<false, 1, 4>(gh, stream, a);
-    else launch_h<false, 4, 2>(gh, stream, a);
-  } else {
-    if (T <= 16) launch_h<true, 1, 4>(gh, stream, a);
-    else launch_h<true, 4, 2>(gh, stream, a);
+  if (!x_s) {
+    // bf16 rows are quantised into out, which has room for them and is written only after h is done
+    uint8_t* q = static_cast<uint8_t*>(out);
+    uint8_t* q_s = q + (size_t)T * H;
+    const int chunks = T * (H / 8);
+    hipLaunchKernelGGL(decode_quantise_kernel, dim3((chunks + 255) / 256), dim3(256), 0, stream,
+                       static_cast<const uint16_t*>(x), chunks, q, q_s);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+    a.x = q;
+    a.x_s = q_s;
   }
+  hipLaunchKernelGGL((decode_h_kernel<4>), gh, dim3(kThreads), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
-  if (T <= 16) hipLaunchKernelGGL((decode_out_kernel<1, 4>), go, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((decode_out_kernel<4, 4>), go, dim3(kThreads), 0, stream, a);
+  // 16 waves a workgroup where that is one workgroup a CU at most, else 8
+  const bool wide = H / 16 <= std::max(1, device_cu_count());
+  if (T <= 16) {
+    if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 6>), go, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((decode_out_kernel<8, 6>), go, dim3(512), 0, stream, a);
+  } else {
+    if (wide) hipLaunchKernelGGL((decode_out_many_kernel<16, 6>), go, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((decode_out_many_kernel<8, 6>), go, dim3(512), 0, stream, a);
+  }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
