@@ -27,8 +27,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kDecodeTokens = 64;                     // at most
 constexpr int kDecodePairs = kDecodeTokens * 16;
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
 
 struct DecodeArgs {
   const uint8_t* x;
@@ -67,7 +65,7 @@ struct Reached {
   uint32_t bits[32];
 };
 
-template <int THREADS = kThreads>
+template <int THREADS>
 __device__ inline void find_reached(const DecodeArgs& a, Reached& r) {
   if (threadIdx.x < 32) r.bits[threadIdx.x] = 0;
   __syncthreads();
@@ -148,14 +146,14 @@ __global__ __launch_bounds__(256) void decode_quantise_kernel(const uint16_t* x,
 // h: grid (I / 32 column blocks, slots); the waves share K. An expert of more than 16 tokens takes
 // them 16 at a time and reads its weights again (from the caches) for every 16.
 // ---------------------------------------------------------------------------------------
-template <int U>
-__global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
+template <int NW, int U>
+__global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
   __shared__ Reached reached;
   __shared__ int16_t s_q[kDecodeTokens];              // the expert's pairs, one of each of its tokens
-  __shared__ f32x4 s_red[kWaves][4][64];
+  __shared__ f32x4 s_red[NW][4][64];
   const int lane = lane_id(), l16 = lane & 15, lhi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  find_reached(a, reached);
+  find_reached<64 * NW>(a, reached);
   const int e = reached_expert(reached, blockIdx.y);
   if (e < 0) return;                                  // the same in every wave
   // lane t: token t's first pair with this expert (h of a later one would be the same)
@@ -192,13 +190,13 @@ __global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
     f32x4 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // K blocks wave, wave + 8, ...: at every moment the waves read neighbouring tiles
-    for (int kb0 = wave; kb0 < KB; kb0 += kWaves * U) {
+    // K blocks wave, wave + NW, ...: at every moment the waves read neighbouring tiles
+    for (int kb0 = wave; kb0 < KB; kb0 += NW * U) {
       u32x4 wt[U][4], b0[U], b1[U];
       uint32_t wsc[U][4], sb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t kb = (uint32_t)(kb0 + u * kWaves);   // past KB: weights past the buffer, zeros
+        const uint32_t kb = (uint32_t)(kb0 + u * NW);   // past KB: weights past the buffer, zeros
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           wt[u][i] = buf_load16_nt(wr[i], kb * 1024u + (uint32_t)lane * 16u);
@@ -227,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void decode_h_kernel(DecodeArgs a) {
     for (int i = 0; i < 4; ++i) {
       s[i] = s_red[0][i][lane];
 #pragma unroll
-      for (int v = 1; v < kWaves; ++v) s[i] += s_red[v][i][lane];
+      for (int v = 1; v < NW; ++v) s[i] += s_red[v][i][lane];
     }
     float h[8];
     uint32_t m = 0;
@@ -317,7 +315,7 @@ __global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
     const int q = k < 0 ? -1 : l16 * a.K + k;
     const bool mine = q >= 0;
     const uint32_t ho = (uint32_t)max(q, 0) * (uint32_t)a.I + (uint32_t)lhi * 16u;
-    const uint32_t hso = (uint32_t)max(q, 0) * (uint32_t)(a.I >> 5) + (uint32_t)lhi;
+    const uint32_t hso = (uint32_t)max(q, 0) * (uint32_t)(a.I >> 5);
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w2 + ((int64_t)e * (a.H >> 4) + rb) * tiles, tiles);
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.w2_s + ((int64_t)e * (a.H >> 4) + rb) * tscales, tscales);
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -332,8 +330,14 @@ __global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
         wsc[u] = buf_load1(sr, in ? kb * 64u + (uint32_t)lane : kNowhere);
         b0[u] = buf_load16(hr, in && mine ? ho + kb * 128u : kNowhere);
         b1[u] = buf_load16(hr, in && mine ? ho + kb * 128u + 64u : kNowhere);
-        sb[u] = buf_load1(hsr, in && mine ? hso + kb * 4u : kNowhere);
       }
+      // the scales of four K blocks in one load: byte lhi of each word
+      u32x4 sw[(U + 3) / 4];
+#pragma unroll
+      for (int v = 0; v < (U + 3) / 4; ++v)
+        sw[v] = buf_load16(hsr, mine ? hso + (uint32_t)(kb0 + 4 * v) * 4u : kNowhere);
+#pragma unroll
+      for (int u = 0; u < U; ++u) sb[u] = kb0 + u < kb_last ? sw[u / 4][u % 4] >> (8 * lhi) : 0u;
 #pragma unroll
       for (int u = 0; u < U; ++u) acc = mfma_mx(w[u], wsc[u], b0[u], b1[u], sb[u], acc);
     }
@@ -406,7 +410,7 @@ __global__ __launch_bounds__(64 * NW) void decode_out_many_kernel(DecodeArgs a) 
       const bool mine = c < n;
       const uint32_t p = mine ? (uint32_t)s_pair[wave][c] : 0u;
       const uint32_t ho = p * (uint32_t)a.I + (uint32_t)lhi * 16u;
-      const uint32_t hso = p * (uint32_t)(a.I >> 5) + (uint32_t)lhi;
+      const uint32_t hso = p * (uint32_t)(a.I >> 5);
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
       for (int kb0 = kb_first; kb0 < kb_last; kb0 += U) {
         u32x4 w[U], b0[U], b1[U];
@@ -419,8 +423,14 @@ __global__ __launch_bounds__(64 * NW) void decode_out_many_kernel(DecodeArgs a) 
           wsc[u] = buf_load1(sr, in ? kb * 64u + (uint32_t)lane : kNowhere);
           b0[u] = buf_load16(hr, in && mine ? ho + kb * 128u : kNowhere);
           b1[u] = buf_load16(hr, in && mine ? ho + kb * 128u + 64u : kNowhere);
-          sb[u] = buf_load1(hsr, in && mine ? hso + kb * 4u : kNowhere);
         }
+        // the scales of four K blocks in one load: byte lhi of each word
+        u32x4 sw[(U + 3) / 4];
+#pragma unroll
+        for (int v = 0; v < (U + 3) / 4; ++v)
+          sw[v] = buf_load16(hsr, mine ? hso + (uint32_t)(kb0 + 4 * v) * 4u : kNowhere);
+#pragma unroll
+        for (int u = 0; u < U; ++u) sb[u] = kb0 + u < kb_last ? sw[u / 4][u % 4] >> (8 * lhi) : 0u;
 #pragma unroll
         for (int u = 0; u < U; ++u) acc = mfma_mx(w[u], wsc[u], b0[u], b1[u], sb[u], acc);
       }
@@ -479,16 +489,21 @@ int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t 
     a.x = q;
     a.x_s = q_s;
   }
-  hipLaunchKernelGGL((decode_h_kernel<4>), gh, dim3(kThreads), 0, stream, a);
+  const int cus = std::max(1, device_cu_count());
+  // 8 waves a workgroup while there are few workgroups, 4 where there are many (one token of top-8:
+  // 11.9 against 13.6 us; 13 tokens at H 7168: 29.8 against 27.3)
+  if ((int)(gh.x * gh.y) <= 2 * cus) hipLaunchKernelGGL((decode_h_kernel<8, 2>), gh, dim3(512), 0, stream, a);
+  else hipLaunchKernelGGL((decode_h_kernel<4, 2>), gh, dim3(256), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
-  // 16 waves a workgroup where that is one workgroup a CU at most, else 8
-  const bool wide = H / 16 <= std::max(1, device_cu_count());
-  if (T <= 16) {
-    if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 6>), go, dim3(1024), 0, stream, a);
-    else hipLaunchKernelGGL((decode_out_kernel<8, 6>), go, dim3(512), 0, stream, a);
+  // 16 waves a workgroup where that is one workgroup a CU at most and each wave has a dozen tiles and more
+  // (96 tiles a workgroup: 9.0 against 8.5 us with 8 waves, 1536 tiles: 80 against 95)
+  const bool wide = H / 16 <= cus && (int64_t)gh.y * (I / 128) >= 256;
+  if (T > 16) {
+    if (wide) hipLaunchKernelGGL((decode_out_many_kernel<16, 4>), go, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((decode_out_many_kernel<8, 4>), go, dim3(512), 0, stream, a);
   } else {
-    if (wide) hipLaunchKernelGGL((decode_out_many_kernel<16, 6>), go, dim3(1024), 0, stream, a);
-    else hipLaunchKernelGGL((decode_out_many_kernel<8, 6>), go, dim3(512), 0, stream, a);
+    if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 4>), go, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((decode_out_kernel<8, 4>), go, dim3(512), 0, stream, a);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

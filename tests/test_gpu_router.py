@@ -155,6 +155,65 @@ def test_close_scores_are_told_apart():
     check(l, 8, moe.RouterConfig(score="softmax"), b)
 
 
+def hard_rows(E, dt, seed):
+    """Rows whose order hangs on a key's last bits: clusters a few units apart, exact ties, both, around any
+    place of the choice, masked or not."""
+    g = torch.Generator().manual_seed(seed)
+    rows = [torch.randn(E, generator=g), torch.zeros(E), torch.randn(E, generator=g).sign()]
+    for unit in (2.0 ** -23, 2.0 ** -20, 2.0 ** -16):
+        steps = torch.randint(0, 40, (4, E), generator=g).float()
+        rows += list(1.0 + steps * unit)                                     # one cluster
+        rows += list(torch.randint(0, 3, (4, E), generator=g).float() + steps * unit)
+    for i in range(3, len(rows), 3):
+        rows[i] = torch.where(torch.rand(E, generator=g) < 0.4, torch.tensor(-INF), rows[i])
+    return torch.stack(rows).to(dt)
+
+
+HARD = [moe.RouterConfig(), moe.RouterConfig(score="sigmoid", normalize=False), moe.RouterConfig(groups=4, topk_groups=2),
+        moe.RouterConfig(score="sigmoid", groups=8, topk_groups=3, group_top=2, scale=2.5),
+        moe.RouterConfig(score="softmax", groups=4, topk_groups=3, group_top=2)]
+
+
+@pytest.mark.parametrize("E", [16, 64, 72, 128, 200, 256, 512, 1024])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_close_keys(E, dt):
+    """The kernels choose by shortened keys first: every way that can end, one token a wave."""
+    say("router close keys", E, dt)
+    rows = hard_rows(E, dt, E)
+    bias = 2.0 ** -22 * torch.randint(-4, 4, (E,), generator=torch.Generator().manual_seed(E)).float()
+    for cfg in HARD:
+        K = min(8, cfg.topk_groups * (E // cfg.groups))
+        for k in (1, K):
+            check(rows, k, cfg)
+        check(rows, K, cfg, bias)
+
+
+@pytest.mark.parametrize("E", [16, 60, 64, 72, 128, 200, 256])
+@pytest.mark.parametrize("cfg", HARD, ids=ids)
+def test_four_tokens_a_wave(E, cfg):
+    """More than 4096 tokens take another layout: the same rows again and again, an odd number."""
+    say("router many", E, cfg)
+    if E % cfg.groups:
+        E += cfg.groups - E % cfg.groups
+    for dt, with_bias in ((torch.float32, False), (torch.float32, True), (torch.bfloat16, False)):
+        rows = hard_rows(E, dt, E + 1)
+        bias = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E)) if with_bias else None
+        n, T = rows.shape[0], 4097 + 30
+        for K in {1, min(8, cfg.topk_groups * (E // cfg.groups)), min(16, cfg.topk_groups * (E // cfg.groups))}:
+            few, few_w = check(rows, K, cfg, bias)
+            at = (torch.arange(T) * 5) % n
+            idx, w = run(rows[at], K, cfg, bias)
+            assert torch.equal(idx, few[at.cuda()])
+            assert (w - few_w[at.cuda()]).abs().max() <= 2.0 ** -20 * cfg.scale      # sums in another order
+            dw = torch.randn(n, K, generator=torch.Generator().manual_seed(1))[at].contiguous().cuda()
+            dl, ref = torch.empty(T, E, dtype=dt, device="cuda"), torch.empty(n, E, dtype=dt, device="cuda")
+            moe.moe_router_topk_backward(dw, rows[at].cuda(), idx, dl, cfg)
+            first = torch.tensor([int((at == i).nonzero()[0]) for i in range(n)])
+            moe.moe_router_topk_backward(dw[first.cuda()].contiguous(), rows.cuda(), few, ref, cfg)
+            torch.cuda.synchronize()
+            assert torch.equal(dl, ref[at.cuda()])
+
+
 def test_many_tokens_match_few():
     say("router many tokens")
     for E, K, cfg in ((24, 4, moe.RouterConfig()), (130, 8, moe.RouterConfig(score="sigmoid"))):
