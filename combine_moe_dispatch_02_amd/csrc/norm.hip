@@ -100,6 +100,16 @@ __device__ inline uint32_t row_umax(uint32_t v) {
   return umax_dpp(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
 }
 
+// NT: with the non-temporal cache policy, for rows that are not read again soon
+template <bool NT>
+__device__ inline u32x4 load_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return NT ? buf_load16_nt(r, off) : buf_load16(r, off);
+}
+template <bool NT>
+__device__ inline void store_row(u32x4 v, __amdgpu_buffer_rsrc_t r, uint32_t off) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, NT ? 2 : 0);
+}
+
 struct NormArgs {
   const uint16_t* x;
   const uint16_t* res;
@@ -113,6 +123,24 @@ struct NormArgs {
   uint8_t* q;
   void* q_s;
 };
+
+// v = f / sc, rounded as IEEE division rounds it. With the correctly rounded reciprocal i, f * i is
+// within a unit of the quotient, the fused remainder f - (f * i) * sc is exact and the corrected
+// quotient rounds right (Markstein's theorem); what could underflow on the way (`plain` false:
+// sc below 2^-99) is divided in full.
+__device__ inline void divide8(const float (&f)[8], float sc, bool plain, float (&v)[8]) {
+  if (plain) {
+    const float i = 1.0f / sc;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q = f[j] * i;
+      v[j] = __builtin_fmaf(__builtin_fmaf(-q, sc, f[j]), i, q);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = f[j] / sc;
+  }
+}
 
 // QF: 0 none, 1 fp8 (1x128 groups), 2 MXFP8 (1x32 blocks); formats and rounding as in dispatch.
 // The group's largest magnitude is taken over bit patterns: those of NaN and infinity are the
@@ -134,8 +162,10 @@ __device__ inline void store_quantised(u32x4 v, int c, int nch, int words, __amd
     const bool bad = m >= 0x7f800000u;
     const float amax = __builtin_bit_cast(float, m);
     const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
-    q.x = pack_e4m3x4(f[0] / sc, f[1] / sc, f[2] / sc, f[3] / sc);
-    q.y = pack_e4m3x4(f[4] / sc, f[5] / sc, f[6] / sc, f[7] / sc);
+    float v[8];
+    divide8(f, sc, amax >= 0x1p-90f, v);
+    q.x = pack_e4m3x4(v[0], v[1], v[2], v[3]);
+    q.y = pack_e4m3x4(v[4], v[5], v[6], v[7]);
     if (bad) q = u32x2{0u, 0u};
     buf_store8(q, qr, (uint32_t)c * 8u);
     if ((lane & 15) == 0 && c < nch)
@@ -155,10 +185,13 @@ __device__ inline void store_quantised(u32x4 v, int c, int nch, int words, __amd
   }
 }
 
-// W waves a row, W = 1: four rows a workgroup
+// W waves a row, W = 1: four rows a workgroup. With an 8-bit output, the codes are what the next
+// kernel reads: x, res, s_out and y pass the caches by (norm, plan and dispatch of 8192 x 4096 fp8 rows:
+// 223 us without, 186 with; 2048: 81.6 and 77.0; 256: no difference). Without one, y is read next.
 template <int W, int CPL, int QF>
 __global__ __launch_bounds__(W == 16 ? 1024 : 256) void rmsnorm_kernel(NormArgs a) {
   constexpr int ROWS = W == 1 ? 4 : 1;
+  constexpr bool NT = QF != 0;
   __shared__ double red[2 * W];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -172,12 +205,12 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void rmsnorm_kernel(NormArgs 
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + t * H, row_bytes);
     u32x4 v[CPL];
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) v[i] = buf_load16(xr, (uint32_t)(c0 + i * kWave) * 16u);
+    for (int i = 0; i < CPL; ++i) v[i] = load_row<NT>(xr, (uint32_t)(c0 + i * kWave) * 16u);
     if (a.res) {
       const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.res + t * H, row_bytes);
       u32x4 r[CPL];
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) r[i] = buf_load16(rr, (uint32_t)(c0 + i * kWave) * 16u);
+      for (int i = 0; i < CPL; ++i) r[i] = load_row<NT>(rr, (uint32_t)(c0 + i * kWave) * 16u);
 #pragma unroll
       for (int i = 0; i < CPL; ++i) {
         float f[8], g[8];
@@ -190,7 +223,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void rmsnorm_kernel(NormArgs 
       if (a.s_out) {
         const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.s_out + t * H, row_bytes);
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) buf_store16(v[i], sr, (uint32_t)(c0 + i * kWave) * 16u);
+        for (int i = 0; i < CPL; ++i) store_row<NT>(v[i], sr, (uint32_t)(c0 + i * kWave) * 16u);
       }
     }
     double ss = 0.0;
@@ -217,7 +250,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 256) void rmsnorm_kernel(NormArgs 
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = (f[j] * rstd) * w[j];
       const u32x4 o = pack8(f);
-      buf_store16(o, yr, (uint32_t)c * 16u);
+      store_row<NT>(o, yr, (uint32_t)c * 16u);
       if constexpr (QF != 0) store_quantised<QF>(o, c, nch, words, qr, q_s);
     }
   }
@@ -265,9 +298,9 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const uint32_t o = (uint32_t)(c0 + i * kWave) * 16u;
-      vd[i] = buf_load16(dr, o);
-      vs[i] = buf_load16(sr, o);
-      vr[i] = buf_load16(rr, o);
+      vd[i] = buf_load16_nt(dr, o);
+      vs[i] = buf_load16_nt(sr, o);
+      vr[i] = buf_load16_nt(rr, o);
     }
     const float rstd = a.rstd[t];
     float dot = 0.f;
@@ -294,7 +327,7 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
       unpack8(vr[i], r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = rstd * (d[j] * w[i][j] - (s[j] * rstd) * c) + r[j];
-      buf_store16(pack8(o), xr, (uint32_t)(c0 + i * kWave) * 16u);
+      store_row<true>(pack8(o), xr, (uint32_t)(c0 + i * kWave) * 16u);
     }
   }
   if (a.part) {
