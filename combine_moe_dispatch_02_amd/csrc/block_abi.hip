@@ -142,7 +142,7 @@ MOE355_API int moe_dispatch_quantized(const void* q, const void* q_s, int32_t H,
   if ((int64_t)H * 2 > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
   const WsLayout L = ws_layout(plan->T, plan->K, plan->E_local, plan->tile, 0, 0, MOE_BF16);
   if (ws_bytes < L.plan_end) return MOE_ERR_INVALID;
-  return launch_dispatch(q, q_s, H, act_dtype, *plan, pool_rows, pool, pool_s, epoch, L, static_cast<char*>(ws),
+  return launch_dispatch_quantized(q, q_s, H, *plan, pool_rows, pool, pool_s, epoch, L, static_cast<char*>(ws),
                          static_cast<hipStream_t>(stream));
 }
 

@@ -27,8 +27,7 @@
 namespace moe {
 
 struct DispatchArgs {
-  const uint16_t* x;           // FMT 3: the rows' codes
-  const uint32_t* x_s;         // FMT 3: the rows' scale words, row-major [T][ceil(H / 128)]
+  const uint16_t* x;
   int32_t T, K, H;
   int32_t tile, tile_shift;
   const int32_t* pos;
@@ -54,39 +53,11 @@ __device__ inline float quad_max(float v) {
 }
 
 // One token's row: read once, stored to each of its local pairs' rows.
-// FMT: 0 bf16 copy, 1 fp8 1x128 groups, 2 MXFP8 1x32 blocks, 3 rows that are codes with
-// scale words already (either format: both move H bytes and a word for 128 columns).
+// FMT: 0 bf16 copy, 1 fp8 1x128 groups, 2 MXFP8 1x32 blocks.
 template <int CPL, int FMT>
 __device__ inline void dispatch_token(const DispatchArgs& a, int t, int p, uint64_t dest, int lane) {
   constexpr bool FP8 = FMT != 0;
   const int H = a.H;
-  if constexpr (FMT == 3) {
-    const int nch = H >> 4;   // 16-byte chunks of 16 codes
-    const int words = (H + 127) >> 7;
-    const __amdgpu_buffer_rsrc_t xr = make_rsrc(reinterpret_cast<const uint8_t*>(a.x) + (int64_t)t * H, (uint32_t)H);
-    const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.x_s + (int64_t)t * words, (uint32_t)words * 4u);
-    for (int c0 = 0; c0 < nch; c0 += kWave * CPL) {
-      u32x4 v[CPL];
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) v[i] = buf_load16_nt(xr, (uint32_t)(c0 + i * kWave + lane) * 16u);
-      for (int k = 0; k < a.K; ++k) {
-        if (!((dest >> k) & 1ull)) continue;
-        const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.pool + (int64_t)readlane(p, k) * H, (uint32_t)H);
-#pragma unroll
-        for (int i = 0; i < CPL; ++i) buf_store16(v[i], pr, (uint32_t)(c0 + i * kWave + lane) * 16u);
-      }
-    }
-    for (int g0 = 0; g0 < words; g0 += kWave) {
-      const int g = g0 + lane;
-      const uint32_t w = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr, (uint32_t)g * 4u, 0, 2);
-      for (int k = 0; k < a.K; ++k) {
-        if (!((dest >> k) & 1ull)) continue;
-        uint32_t* srow = static_cast<uint32_t*>(a.pool_s) + scale_word(readlane(p, k), 0, words, a.tile_shift);
-        if (g < words) srow[(int64_t)g << a.tile_shift] = w;
-      }
-    }
-    return;
-  }
   const int nch = H >> 3;  // 16-byte chunks of 8 bf16 in a row
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + (int64_t)t * H, (uint32_t)H * 2u);
   const int64_t out_row_bytes = FP8 ? H : (int64_t)H * 2;
@@ -244,12 +215,11 @@ static void launch_wpb(int wpb, int cpl, int waves, hipStream_t s, const Dispatc
   }
 }
 
-int launch_dispatch(const void* x, const void* x_s, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
+int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
                     void* pool, void* pool_s, uint32_t epoch, const WsLayout& L, char* ws,
                     hipStream_t stream) {
   DispatchArgs a;
   a.x = static_cast<const uint16_t*>(x);
-  a.x_s = static_cast<const uint32_t*>(x_s);
   a.T = p.T;
   a.K = p.K;
   a.H = H;
@@ -267,7 +237,7 @@ int launch_dispatch(const void* x, const void* x_s, int32_t H, int32_t dtype, co
   a.tiles_done = reinterpret_cast<uint32_t*>(ws + L.tiles_done);
   a.epoch = epoch;
   a.err = reinterpret_cast<uint32_t*>(ws + L.err);
-  const int nch = H / (x_s ? 16 : 8);
+  const int nch = H / 8;
   const int cpl = nch <= 64 ? 1 : nch <= 128 ? 2 : nch <= 256 ? 4 : 8;
   const int cus = std::max(1, device_cu_count());
   // tokens per wave: up to 64/K (one pos load per wave and token run), fewer when that
@@ -278,14 +248,153 @@ int launch_dispatch(const void* x, const void* x_s, int32_t H, int32_t dtype, co
   // waves per block: the largest power of two up to 16 that leaves a block per CU
   int wpb = 1;
   while (wpb < 16 && waves / (2 * wpb) >= cus) wpb *= 2;
-  if (x_s)
-    launch_wpb<3>(wpb, cpl, waves, stream, a);
-  else if (dtype == MOE_FP8_E4M3_G128)
+  if (dtype == MOE_FP8_E4M3_G128)
     launch_wpb<1>(wpb, cpl, waves, stream, a);
   else if (dtype == MOE_MXFP4)
     launch_wpb<2>(wpb, cpl, waves, stream, a);
   else
     launch_wpb<0>(wpb, cpl, waves, stream, a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+// ---------------------------------------------------------------------------------------
+// rows that are codes with scale words already
+// ---------------------------------------------------------------------------------------
+// Both formats move H bytes and a 4-byte word for 128 columns a row, so one kernel serves them.
+// The codes go as above: a wave reads a token's row once and stores it to each of its pool rows.
+// The words do not: stored beside the rows, a word of each 128 columns lands alone in its line of the
+// tile-major array (20 of 92 us at 8192 x 4096, top-8). The first `scale_blocks` workgroups fill
+// them tile by tile instead, tile consecutive words at a time, and count as one more row of the tile.
+// (Filling the codes tile by tile too reads every row K times: 122 us there.)
+struct DispatchQArgs {
+  DispatchArgs d;               // x: the codes
+  const uint32_t* x_s;          // [T][ceil(H / 128)]
+  const int32_t* src;
+  const int32_t* num_tiles;
+  int32_t scale_blocks;
+};
+// Few, large workgroups, since each pays an L2 write-back to publish: 16 waves of up to 8 tokens, 32
+// workgroups for the scales (8192 x 4096, top-8: 78 us; 4 waves of 4 tokens with 128: 101).
+constexpr int kQWaves = 16;
+constexpr int kQTokens = 8;
+constexpr int kQScaleBlocks = 32;
+
+// one more of tile ti is in; `more` rows count beside its real ones
+__device__ inline void count_tile(const DispatchArgs& a, int ti, int more) {
+  const uint32_t old = __hip_atomic_fetch_add(&a.tile_fill[ti], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int e = a.tile_expert[ti];
+  const int real = min(a.tile, a.offsets[e] + a.counts[e] - (ti << a.tile_shift));
+  if ((int)old + 1 == real + more) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    __hip_atomic_store(&a.tile_ready[ti], a.epoch, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_fetch_add(a.tiles_done, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+template <int CPL>
+__global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(DispatchQArgs b) {
+  const DispatchArgs& a = b.d;
+  const int lane = lane_id();
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int words = (a.H + 127) >> 7;
+
+  if ((int)blockIdx.x < b.scale_blocks) {
+    __shared__ int s_token[128];
+    const int tiles = min(b.num_tiles[0], a.pool_rows >> a.tile_shift);
+    for (int ti = blockIdx.x; ti < tiles; ti += b.scale_blocks) {
+      __syncthreads();
+      for (int r = threadIdx.x; r < a.tile; r += 64 * kQWaves) {
+        const int q = b.src[((int64_t)ti << a.tile_shift) + r];
+        s_token[r] = q < 0 ? -1 : (int)((uint32_t)q / (uint32_t)a.K);
+      }
+      __syncthreads();
+      uint32_t* to = static_cast<uint32_t*>(a.pool_s) + ((int64_t)ti << a.tile_shift) * words;
+#pragma unroll 4
+      for (int i = threadIdx.x; i < words << a.tile_shift; i += 64 * kQWaves) {
+        const int t = s_token[i & (a.tile - 1)];
+        if (t >= 0) to[i] = b.x_s[(int64_t)t * words + (i >> a.tile_shift)];
+      }
+    }
+    __syncthreads();
+    if (w != 0) return;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    for (int ti = blockIdx.x + lane * b.scale_blocks; ti < tiles; ti += 64 * b.scale_blocks) count_tile(a, ti, 1);
+    return;
+  }
+
+  const int tpw = a.tokens_per_wave;
+  const int tb = ((int)blockIdx.x - b.scale_blocks) * kQWaves * tpw;   // the block's first token
+  const int t0 = tb + w * tpw;
+  const int ntok = t0 < a.T ? min(tpw, a.T - t0) : 0;
+  const int nch = a.H >> 4;   // 16-byte chunks of 16 codes
+  for (int i = 0; i < ntok; ++i) {
+    const int t = t0 + i;
+    int p = lane < a.K ? a.pos[(int64_t)t * a.K + lane] : -1;
+    if (p >= a.pool_rows) {
+      record_error(a.err, MOE_ERR_INVALID);
+      p = -1;
+    }
+    const uint64_t dest = ballot(p >= 0);
+    if (dest == 0) continue;
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(reinterpret_cast<const uint8_t*>(a.x) + (int64_t)t * a.H, (uint32_t)a.H);
+    for (int c0 = 0; c0 < nch; c0 += kWave * CPL) {
+      u32x4 v[CPL];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) v[j] = buf_load16_nt(xr, (uint32_t)(c0 + j * kWave + lane) * 16u);
+      for (uint64_t m = dest; m != 0; m &= m - 1) {
+        const int pk = readlane(p, __builtin_ctzll(m));
+        const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.pool + (int64_t)pk * a.H, (uint32_t)a.H);
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) buf_store16(v[j], pr, (uint32_t)(c0 + j * kWave + lane) * 16u);
+      }
+    }
+  }
+  // published as above, once a workgroup
+  __syncthreads();
+  if (w != 0) return;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+  const int npairs = (min(a.T, tb + kQWaves * tpw) - tb) * a.K;
+  for (int q = lane; q < npairs; q += 64) {
+    const int p = a.pos[(int64_t)tb * a.K + q];
+    if (p >= 0 && p < a.pool_rows) count_tile(a, p >> a.tile_shift, 1);
+  }
+}
+
+int launch_dispatch_quantized(const void* q, const void* q_s, int32_t H, const moe_plan_t& p, int32_t pool_rows,
+                              void* pool, void* pool_s, uint32_t epoch, const WsLayout& L, char* ws,
+                              hipStream_t stream) {
+  DispatchQArgs b;
+  DispatchArgs& a = b.d;
+  a.x = static_cast<const uint16_t*>(q);
+  a.T = p.T;
+  a.K = p.K;
+  a.H = H;
+  a.tile = p.tile;
+  a.tile_shift = __builtin_ctz((unsigned)p.tile);
+  a.pos = p.pos;
+  a.tile_expert = p.tile_expert;
+  a.offsets = p.offsets;
+  a.counts = p.counts;
+  a.pool = static_cast<uint8_t*>(pool);
+  a.pool_s = pool_s;
+  a.pool_rows = pool_rows;
+  a.tile_fill = reinterpret_cast<uint32_t*>(ws + L.fill);
+  a.tile_ready = p.tile_ready;
+  a.tiles_done = reinterpret_cast<uint32_t*>(ws + L.tiles_done);
+  a.epoch = epoch;
+  a.err = reinterpret_cast<uint32_t*>(ws + L.err);
+  b.x_s = static_cast<const uint32_t*>(q_s);
+  b.src = p.src;
+  b.num_tiles = p.num_tiles;
+  const int cus = std::max(1, device_cu_count());
+  a.tokens_per_wave = std::max(1, std::min(kQTokens, p.T / (8 * cus)));
+  b.scale_blocks = std::min(p.rows_cap / p.tile, kQScaleBlocks);
+  const int per = kQWaves * a.tokens_per_wave;
+  const dim3 grid((unsigned)(b.scale_blocks + (p.T + per - 1) / per)), block(64 * kQWaves);
+  const int nch = H / 16;
+  if (nch <= 64) hipLaunchKernelGGL((dispatch_quantized_kernel<1>), grid, block, 0, stream, b);
+  else if (nch <= 128) hipLaunchKernelGGL((dispatch_quantized_kernel<2>), grid, block, 0, stream, b);
+  else hipLaunchKernelGGL((dispatch_quantized_kernel<4>), grid, block, 0, stream, b);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -14,10 +14,14 @@ int check_plan(const moe_plan_t* p);
 int launch_plan(const int32_t* topk_idx, const moe_plan_t& p, const WsLayout& L, char* ws,
                 hipStream_t stream);
 
-// x_s null: x is bf16; else x holds codes of format dtype and x_s their row-major scale words
-int launch_dispatch(const void* x, const void* x_s, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
+int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p, int32_t pool_rows,
                     void* pool, void* pool_s, uint32_t epoch, const WsLayout& L, char* ws,
                     hipStream_t stream);
+
+// q: codes [T][H], q_s: their row-major scale words (fp8 and mxfp4 alike)
+int launch_dispatch_quantized(const void* q, const void* q_s, int32_t H, const moe_plan_t& p, int32_t pool_rows,
+                              void* pool, void* pool_s, uint32_t epoch, const WsLayout& L, char* ws,
+                              hipStream_t stream);
 
 struct FfnLaunch {
   const moe_plan_t* plan;
