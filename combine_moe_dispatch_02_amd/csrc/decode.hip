@@ -278,96 +278,28 @@ struct TokenPairs {
 
 // ---------------------------------------------------------------------------------------
 // out: a workgroup has 16 columns of out for all tokens; its waves share the (expert, K block)
-// pairs evenly. Up to 16 tokens: token t is column t, so the sums stay in registers.
+// pairs evenly. An expert's tokens are gathered into the columns of the product, eight at a time
+// (more than eight are rare: 64 tokens on 128 experts have four each), and the columns' sums go to
+// their tokens' sums in the wave's part of LDS.
+//
+// A weight tile is one load, and what belongs to it must not cost several: the address unit
+// takes as long for a scattered load of 16 bytes a lane as for a weight tile, and with two of
+// those for h, one for its scale and one for the weight's it was busy 77% of the time (64 tokens:
+// 96 us). So h comes in whole lines, several K blocks a load, and goes to the lanes that want it
+// by way of LDS, and the scales of four K blocks come as words (80 us with the latter alone).
 // ---------------------------------------------------------------------------------------
-template <int NW, int U>
+template <int NW, int TOK>
 __global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
+  constexpr int U = 4;                                // K blocks at a time
+  constexpr int COLS = 8;
   __shared__ Reached reached;
-  __shared__ float s_w[kDecodePairs];
-  __shared__ int16_t s_expert[kDecodePairs];          // the reached experts
-  __shared__ f32x4 s_red[NW][64];
-  const int lane = lane_id(), l16 = lane & 15, lhi = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int q = threadIdx.x; q < a.T * a.K; q += 64 * NW) s_w[q] = a.weights[q];
-  find_reached<64 * NW>(a, reached);
-  const int slots = list_reached<64 * NW>(reached, s_expert);
-  TokenPairs pairs;
-  pairs.load(a, reached, s_w, l16);
-  __syncthreads();
-
-  const int KB = a.I >> 7;
-  const int rb = blockIdx.x;
-  const uint32_t tiles = (uint32_t)KB * 1024u, tscales = (uint32_t)KB * 64u;
-  const uint32_t rows = (uint32_t)a.T * (uint32_t)a.K;
-  const __amdgpu_buffer_rsrc_t hr = make_rsrc(a.h, rows * (uint32_t)a.I);
-  const __amdgpu_buffer_rsrc_t hsr = make_rsrc(a.h_s, rows * (uint32_t)(a.I >> 5));
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  const int64_t items = (int64_t)slots * KB;
-  const int first = (int)(items * wave / NW), last = (int)(items * (wave + 1) / NW);
-  for (int it = first; it < last;) {
-    const int slot = it / KB, kb_first = it - slot * KB;
-    const int kb_last = min(KB, kb_first + last - it);
-    it += kb_last - kb_first;
-    const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
-    // this lane's token: its first pair with the expert and its pairs' weight
-    float wt;
-    const int k = pairs.find(e, wt);
-    const int q = k < 0 ? -1 : l16 * a.K + k;
-    const bool mine = q >= 0;
-    const uint32_t ho = (uint32_t)max(q, 0) * (uint32_t)a.I + (uint32_t)lhi * 16u;
-    const uint32_t hso = (uint32_t)max(q, 0) * (uint32_t)(a.I >> 5);
-    const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w2 + ((int64_t)e * (a.H >> 4) + rb) * tiles, tiles);
-    const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.w2_s + ((int64_t)e * (a.H >> 4) + rb) * tscales, tscales);
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int kb0 = kb_first; kb0 < kb_last; kb0 += U) {
-      u32x4 w[U], b0[U], b1[U];
-      uint32_t wsc[U], sb[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = kb0 + u < kb_last;
-        const uint32_t kb = (uint32_t)(kb0 + u);
-        w[u] = buf_load16_nt(wr, in ? kb * 1024u + (uint32_t)lane * 16u : kNowhere);
-        wsc[u] = buf_load1(sr, in ? kb * 64u + (uint32_t)lane : kNowhere);
-        b0[u] = buf_load16(hr, in && mine ? ho + kb * 128u : kNowhere);
-        b1[u] = buf_load16(hr, in && mine ? ho + kb * 128u + 64u : kNowhere);
-      }
-      // the scales of four K blocks in one load: byte lhi of each word
-      u32x4 sw[(U + 3) / 4];
-#pragma unroll
-      for (int v = 0; v < (U + 3) / 4; ++v)
-        sw[v] = buf_load16(hsr, mine ? hso + (uint32_t)(kb0 + 4 * v) * 4u : kNowhere);
-#pragma unroll
-      for (int u = 0; u < U; ++u) sb[u] = kb0 + u < kb_last ? sw[u / 4][u % 4] >> (8 * lhi) : 0u;
-#pragma unroll
-      for (int u = 0; u < U; ++u) acc = mfma_mx(w[u], wsc[u], b0[u], b1[u], sb[u], acc);
-    }
-    // a token without this expert takes nothing of it, a NaN of its weights neither
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] += mine ? wt * acc[i] : 0.f;
-  }
-
-  s_red[wave][lane] = sum;
-  __syncthreads();
-  if (wave != 0) return;
-  f32x4 s = s_red[0][lane];
-#pragma unroll
-  for (int v = 1; v < NW; ++v) s += s_red[v][lane];
-  if (l16 < a.T) {
-    const u32x2 o = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
-    *reinterpret_cast<u32x2*>(a.out + (int64_t)l16 * a.H + rb * 16 + lhi * 4) = o;
-  }
-}
-
-// The same for more than 16 tokens, where an expert has a few of them: its tokens are gathered
-// into columns, and the columns' sums go to the tokens' sums in the wave's part of LDS.
-template <int NW, int U>
-__global__ __launch_bounds__(64 * NW) void decode_out_many_kernel(DecodeArgs a) {
-  __shared__ Reached reached;
-  __shared__ float s_w[kDecodePairs];
-  __shared__ int16_t s_expert[kDecodePairs];          // the reached experts
-  __shared__ f32x4 s_sum[NW][4][kDecodeTokens];       // [wave][columns 4 lhi ..][token]
-  __shared__ int16_t s_pair[NW][kDecodeTokens], s_token[NW][kDecodeTokens];
-  __shared__ float s_weight[NW][kDecodeTokens];
+  __shared__ float s_w[TOK * 16];
+  __shared__ int16_t s_expert[TOK * 16];              // the reached experts
+  __shared__ f32x4 s_sum[NW][4][TOK];                 // [wave][columns 4 lhi ..][token]
+  __shared__ int16_t s_pair[NW][TOK], s_token[NW][TOK];
+  __shared__ float s_weight[NW][TOK];
+  __shared__ u32x4 s_h[NW][U][COLS][8];               // a column's 128 codes, 16-byte chunk k at k ^ column
+  __shared__ uint32_t s_scale[NW][U * 16];            // weight scales, 64 bytes a tile
   const int lane = lane_id(), l16 = lane & 15, lhi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int q = threadIdx.x; q < a.T * a.K; q += 64 * NW) s_w[q] = a.weights[q];
@@ -376,8 +308,10 @@ __global__ __launch_bounds__(64 * NW) void decode_out_many_kernel(DecodeArgs a) 
   TokenPairs pairs;                                   // lane t: token t
   pairs.load(a, reached, s_w, lane);
   __syncthreads();
+  if (lane < TOK)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s_sum[wave][i][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 4; ++i) s_sum[wave][i][lane] = f32x4{0.f, 0.f, 0.f, 0.f};
+
   const int KB = a.I >> 7;
   const int rb = blockIdx.x;
   const uint32_t tiles = (uint32_t)KB * 1024u, tscales = (uint32_t)KB * 64u;
@@ -393,58 +327,71 @@ __global__ __launch_bounds__(64 * NW) void decode_out_many_kernel(DecodeArgs a) 
     const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
     float s;
     const int k = pairs.find(e, s);
-    const int q = k < 0 ? -1 : lane * a.K + k;
-    const uint64_t has = ballot(q >= 0);
+    const uint64_t has = ballot(k >= 0);
     const int n = __popcll(has);
-    if (q >= 0) {
+    if (k >= 0) {
       const int at = mask_rank(has);
-      s_pair[wave][at] = (int16_t)q;
+      s_pair[wave][at] = (int16_t)(lane * a.K + k);
       s_token[wave][at] = (int16_t)lane;
       s_weight[wave][at] = s;
     }
     wave_sync();
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w2 + ((int64_t)e * (a.H >> 4) + rb) * tiles, tiles);
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.w2_s + ((int64_t)e * (a.H >> 4) + rb) * tscales, tscales);
-    for (int c0 = 0; c0 < n; c0 += 16) {
-      const int c = c0 + l16;
-      const bool mine = c < n;
-      const uint32_t p = mine ? (uint32_t)s_pair[wave][c] : 0u;
-      const uint32_t ho = p * (uint32_t)a.I + (uint32_t)lhi * 16u;
-      const uint32_t hso = p * (uint32_t)(a.I >> 5);
+    for (int c0 = 0; c0 < n; c0 += COLS) {
+      // loading: 2^p >= the columns, eight lanes a column's 128 codes, 8 >> p K blocks a load
+      const int cols = min(COLS, n - c0);
+      const int p = cols > 4 ? 3 : cols > 2 ? 2 : cols > 1 ? 1 : 0;
+      const int lc = (lane >> 3) & ((1 << p) - 1), chunk = lane & 7, lu = lane >> (3 + p);
+      const uint32_t from = lc < cols ? (uint32_t)s_pair[wave][c0 + lc] * (uint32_t)a.I + (uint32_t)chunk * 16u : kNowhere;
+      // computing: column l16
+      const bool mine = l16 < cols;
+      const uint32_t hso = mine ? (uint32_t)s_pair[wave][c0 + l16] * (uint32_t)(a.I >> 5) : 0u;
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
       for (int kb0 = kb_first; kb0 < kb_last; kb0 += U) {
-        u32x4 w[U], b0[U], b1[U];
-        uint32_t wsc[U], sb[U];
+        u32x4 w[U], h[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          w[u] = buf_load16_nt(wr, kb0 + u < kb_last ? (uint32_t)(kb0 + u) * 1024u + (uint32_t)lane * 16u : kNowhere);
+        const uint32_t ws = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr, (uint32_t)kb0 * 64u + (uint32_t)lane * 4u, 0, 0);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (i == 0 || i < (1 << p) / 2) {           // (1 << p) * U columns of K blocks, 8 a load
+            const int u = i * (8 >> p) + lu;
+            h[i] = buf_load16(hr, u < U && kb0 + u < kb_last && from != kNowhere ? from + (uint32_t)(kb0 + u) * 128u : kNowhere);
+          }
+        const u32x4 hs = buf_load16(hsr, mine ? hso + (uint32_t)kb0 * 4u : kNowhere);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (i == 0 || i < (1 << p) / 2) {
+            const int u = i * (8 >> p) + lu;
+            if (u < U) s_h[wave][u][lc][chunk ^ lc] = h[i];
+          }
+        s_scale[wave][lane] = ws;
+        wave_sync();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+          // K blocks past the last have zero weights and codes, and no NaN for a scale
           const bool in = kb0 + u < kb_last;
-          const uint32_t kb = (uint32_t)(kb0 + u);
-          w[u] = buf_load16_nt(wr, in ? kb * 1024u + (uint32_t)lane * 16u : kNowhere);
-          wsc[u] = buf_load1(sr, in ? kb * 64u + (uint32_t)lane : kNowhere);
-          b0[u] = buf_load16(hr, in && mine ? ho + kb * 128u : kNowhere);
-          b1[u] = buf_load16(hr, in && mine ? ho + kb * 128u + 64u : kNowhere);
+          const int c = l16 & (COLS - 1);
+          u32x4 b0 = s_h[wave][u][c][lhi ^ c], b1 = s_h[wave][u][c][(lhi + 4) ^ c];
+          if (!mine) b0 = b1 = u32x4{0u, 0u, 0u, 0u};
+          const uint32_t wb = reinterpret_cast<const uint8_t*>(s_scale[wave])[u * 64 + lane];
+          acc = mfma_mx(w[u], in ? wb : 0u, b0, b1, in ? hs[u] >> (8 * lhi) : 0u, acc);
         }
-        // the scales of four K blocks in one load: byte lhi of each word
-        u32x4 sw[(U + 3) / 4];
-#pragma unroll
-        for (int v = 0; v < (U + 3) / 4; ++v)
-          sw[v] = buf_load16(hsr, mine ? hso + (uint32_t)(kb0 + 4 * v) * 4u : kNowhere);
-#pragma unroll
-        for (int u = 0; u < U; ++u) sb[u] = kb0 + u < kb_last ? sw[u / 4][u % 4] >> (8 * lhi) : 0u;
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc = mfma_mx(w[u], wsc[u], b0[u], b1[u], sb[u], acc);
+        wave_sync();
       }
-      if (mine) s_sum[wave][lhi][s_token[wave][c]] += s_weight[wave][c] * acc;   // a token has one column
+      if (mine) s_sum[wave][lhi][s_token[wave][c0 + l16]] += s_weight[wave][c0 + l16] * acc;   // a token has one column
     }
     wave_sync();
   }
 
   __syncthreads();
   if (wave >= 4) return;
-  f32x4 s = s_sum[0][wave][lane];
-#pragma unroll
-  for (int v = 1; v < NW; ++v) s += s_sum[v][wave][lane];
   if (lane < a.T) {
+    f32x4 s = s_sum[0][wave][lane];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) s += s_sum[v][wave][lane];
     const u32x2 o = {pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
     *reinterpret_cast<u32x2*>(a.out + (int64_t)lane * a.H + rb * 16 + wave * 4) = o;
   }
@@ -499,11 +446,11 @@ int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t 
   // (96 tiles a workgroup: 9.0 against 8.5 us with 8 waves, 1536 tiles: 80 against 95)
   const bool wide = H / 16 <= cus && (int64_t)gh.y * (I / 128) >= 256;
   if (T > 16) {
-    if (wide) hipLaunchKernelGGL((decode_out_many_kernel<16, 4>), go, dim3(1024), 0, stream, a);
-    else hipLaunchKernelGGL((decode_out_many_kernel<8, 4>), go, dim3(512), 0, stream, a);
+    if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 64>), go, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((decode_out_kernel<8, 64>), go, dim3(512), 0, stream, a);
   } else {
-    if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 4>), go, dim3(1024), 0, stream, a);
-    else hipLaunchKernelGGL((decode_out_kernel<8, 4>), go, dim3(512), 0, stream, a);
+    if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 16>), go, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((decode_out_kernel<8, 16>), go, dim3(512), 0, stream, a);
   }
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
