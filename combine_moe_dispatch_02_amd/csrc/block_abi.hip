@@ -76,7 +76,7 @@ MOE355_API int moe_rmsnorm(const void* x, const void* res, const void* weight, i
 
 MOE355_API size_t moe_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H) {
   if (T < 1 || H < 8 || H % 8 != 0 || H > kMaxWidth) return 0;
-  return (size_t)rmsnorm_backward_blocks(T) * H * sizeof(float);
+  return (size_t)rmsnorm_backward_blocks(T, H) * H * sizeof(float);
 }
 
 MOE355_API int moe_rmsnorm_backward(const void* dy, const void* s, const void* weight, int32_t weight_dtype,

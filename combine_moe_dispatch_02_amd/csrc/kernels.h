@@ -127,7 +127,7 @@ int device_cu_count();
 // norm.hip
 int launch_rmsnorm(const void* x, const void* res, const void* weight, bool w_f32, int32_t T, int32_t H, double eps,
                    void* s_out, void* y, float* rstd, int32_t q_dtype, void* q, void* q_s, hipStream_t stream);
-int32_t rmsnorm_backward_blocks(int32_t T);
+int32_t rmsnorm_backward_blocks(int32_t T, int32_t H);
 int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, bool w_f32, const float* rstd,
                             const void* d_res, int32_t T, int32_t H, void* dx, float* dweight, void* ws,
                             hipStream_t stream);

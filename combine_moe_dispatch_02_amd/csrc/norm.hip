@@ -282,10 +282,13 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
   const int c0 = sub * (kWave * CPL) + lane;
   const uint32_t row_bytes = (uint32_t)H * 2u;
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, a.w_f32 ? (uint32_t)H * 4u : row_bytes);
-  float w[CPL][8], dw[CPL][8];
+  // the weight stays in registers too, except with the widest rows, which have none left for it
+  // (1024 x 32768: 155 us with it, spilled)
+  constexpr bool HELD = CPL < 4;
+  float w[HELD ? CPL : 1][8], dw[CPL][8];
 #pragma unroll
   for (int i = 0; i < CPL; ++i) {
-    load_weight(wr, a.w_f32, c0 + i * kWave, w[i]);
+    if constexpr (HELD) load_weight(wr, a.w_f32, c0 + i * kWave, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   }
@@ -300,20 +303,23 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
       const uint32_t o = (uint32_t)(c0 + i * kWave) * 16u;
       vd[i] = buf_load16_nt(dr, o);
       vs[i] = buf_load16_nt(sr, o);
-      vr[i] = buf_load16_nt(rr, o);
+      if constexpr (HELD) vr[i] = buf_load16_nt(rr, o);
     }
     const float rstd = a.rstd[t];
+    int cw = c0;
+    if constexpr (!HELD) asm volatile("" : "+v"(cw));   // else the compiler holds what it loads and unpacks after all
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       float d[8], s[8];
       unpack8(vd[i], d);
       unpack8(vs[i], s);
+      if constexpr (!HELD) load_weight(wr, a.w_f32, cw + i * kWave, w[0]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float dxh = d[j] * (s[j] * rstd);
         dw[i][j] += dxh;
-        dot += dxh * w[i][j];
+        dot += dxh * w[HELD ? i : 0][j];
       }
     }
     const float c = row_sum<W>(dot, red, sub, odd) / (float)H;
@@ -322,11 +328,13 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       float d[8], s[8], r[8], o[8];
+      if constexpr (!HELD) asm volatile("" : "+v"(vd[i]), "+v"(vs[i]));
       unpack8(vd[i], d);
       unpack8(vs[i], s);
-      unpack8(vr[i], r);
+      unpack8(HELD ? vr[i] : buf_load16_nt(rr, (uint32_t)(c0 + i * kWave) * 16u), r);
+      if constexpr (!HELD) load_weight(wr, a.w_f32, cw + i * kWave, w[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = rstd * (d[j] * w[i][j] - (s[j] * rstd) * c) + r[j];
+      for (int j = 0; j < 8; ++j) o[j] = rstd * (d[j] * w[HELD ? i : 0][j] - (s[j] * rstd) * c) + r[j];
       store_row<true>(pack8(o), xr, (uint32_t)(c0 + i * kWave) * 16u);
     }
   }
@@ -348,8 +356,8 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
 }
 
 // dweight[h] = sum of the n partial rows, always in the same order. A workgroup has 32 columns,
-// lane (r, c) of wave v sums rows 8 v + r, + 128, ... of columns 4 c .. + 4: at most four loads,
-// all in flight (with 8 row groups of a column a thread it took 18 us at n = 512, H = 4096).
+// lane (r, c) of wave v sums rows 8 v + r, + 128, ... of columns 4 c .. + 4, eight loads in flight
+// (n = 512, H = 4096: 4.8 us; with 8 row groups of a column a thread 18).
 __global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* part, int n, int H, float* dweight) {
   typedef float f32x4 __attribute__((ext_vector_type(4)));
   __shared__ f32x4 red[16][8];
@@ -358,7 +366,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* part
   const int h = blockIdx.x * 32 + c * 4;   // H % 8 == 0: four columns are in or out together
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
   if (h < H)
-#pragma unroll 4
+#pragma unroll 8
     for (int i = wave * 8 + r; i < n; i += 128) v += *reinterpret_cast<const f32x4*>(part + (int64_t)i * H + h);
 #pragma unroll
   for (int o = 8; o < 64; o *= 2)
@@ -404,7 +412,7 @@ int launch_rmsnorm(const void* x, const void* res, const void* weight, bool w_f3
   a.q_s = q_s;
   const int qf = q_dtype == MOE_FP8_E4M3_G128 ? 1 : q_dtype == MOE_MXFP4 ? 2 : 0;
   const int nch = ((H + 127) / 128) * 16;   // chunks, the last scale word's whole
-  const auto blocks = [&](int rows) { return dim3((unsigned)std::min((T + rows - 1) / rows, kNormMaxBlocks)); };
+  const auto blocks = [&](int rows) { return dim3((unsigned)std::min<int64_t>(((int64_t)T + rows - 1) / rows, kNormMaxBlocks)); };
   if (nch <= 64) launch_norm_q<1, 1>(qf, blocks(4), stream, a);
   else if (nch <= 128) launch_norm_q<1, 2>(qf, blocks(4), stream, a);
   else if (nch <= 256) launch_norm_q<4, 1>(qf, blocks(1), stream, a);
@@ -415,9 +423,14 @@ int launch_rmsnorm(const void* x, const void* res, const void* weight, bool w_f3
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
-// workgroups of the backward pass: rows of partial sums that the workspace holds. The number
-// depends on T alone, so the workspace and the order of the sums do.
-int32_t rmsnorm_backward_blocks(int32_t T) { return std::min(T, 512); }
+// Waves that share a row of the backward pass, and its workgroups (4096 waves, 16 a CU): rows of
+// partial sums that the workspace holds. Both depend on T and H alone, and so does the order of
+// the sums.
+static int backward_waves(int32_t H) {
+  const int nch = H / 8;
+  return nch <= 64 ? 1 : nch <= 256 ? 4 : nch <= 1024 ? 8 : 16;
+}
+int32_t rmsnorm_backward_blocks(int32_t T, int32_t H) { return std::min(T, 4096 / backward_waves(H)); }
 
 int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, bool w_f32, const float* rstd,
                             const void* d_res, int32_t T, int32_t H, void* dx, float* dweight, void* ws,
@@ -433,7 +446,7 @@ int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, b
   a.H = H;
   a.dx = static_cast<uint16_t*>(dx);
   a.part = dweight ? static_cast<float*>(ws) : nullptr;
-  const int n = T > 0 ? rmsnorm_backward_blocks(T) : 0;
+  const int n = T > 0 ? rmsnorm_backward_blocks(T, H) : 0;
   if (n > 0) {
     const int nch = H / 8;
     const dim3 grid(n);
