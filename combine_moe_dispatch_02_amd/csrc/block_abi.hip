@@ -167,6 +167,10 @@ MOE355_API int moe_expert_ffn_decode(const void* x, const void* x_s, int32_t x_d
   }
   if (T > 64 || H % 128 != 0 || I % 128 != 0 || H > kMaxWidth || I > kMaxWidth) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
+  // out is scratch while x is still read
+  const char* from = static_cast<const char*>(x);
+  const char* to = static_cast<const char*>(out);
+  if (from < to + (size_t)T * H * 2 && to < from + (size_t)T * H * (x_dtype == MOE_BF16 ? 2 : 1)) return MOE_ERR_INVALID;
   if (ws_bytes < decode_ws_bytes(T, K, I)) return MOE_ERR_INVALID;
   return launch_expert_ffn_decode(x, x_s, T, H, I, K, expert_begin, E_local, topk_idx, topk_weights, w1, w1_s, w2,
                                   w2_s, ws, out, static_cast<hipStream_t>(stream));

@@ -163,10 +163,11 @@ MOE355_API size_t moe_expert_ffn_decode_workspace_bytes(int32_t T, int32_t K, in
  * [T][H] with x_s null (x_dtype MOE_BF16: quantised to MXFP8 on the way, as moe_dispatch
  * does). w1, w2: codes as moe_pack_weights lays them out, w1_s, w2_s: scales as
  * moe_pack_mx_scales does -- what moe_expert_ffn takes in mxfp4 mode. topk_idx: int32 [T][K],
- * topk_weights: fp32 [T][K], out: bf16 [T][H], every row written.
+ * topk_weights: fp32 [T][K], out: bf16 [T][H], every row written (bf16 rows of x are held there,
+ * quantised, until then).
  * Errors: MOE_ERR_INVALID (null or misaligned pointers, T < 0, K not in [1,16], E_local not
  * in [1,1024], expert_begin < 0, H or I < 1, unknown x_dtype, x_s not as x_dtype wants it,
- * small workspace), MOE_ERR_UNSUPPORTED (T > 64, H % 128 or I % 128 nonzero, H or I above
+ * small workspace, out overlapping x), MOE_ERR_UNSUPPORTED (T > 64, H % 128 or I % 128 nonzero, H or I above
  * 32768).
  */
 MOE355_API int moe_expert_ffn_decode(const void* x, const void* x_s, int32_t x_dtype, int32_t T, int32_t H, int32_t I,

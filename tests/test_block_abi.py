@@ -143,7 +143,7 @@ def decode(lib, **kw):
     *[({n: ODD}, INVALID) for n in ("x", "xs", "idx", "wt", "w1", "w1s", "w2", "w2s", "ws", "out")],
     (dict(dt=0), INVALID), (dict(dt=1), INVALID), (dict(T=-1), INVALID), (dict(K=0), INVALID), (dict(K=17), INVALID),
     (dict(E=0), INVALID), (dict(E=1025), INVALID), (dict(begin=-1), INVALID), (dict(H=0), INVALID), (dict(I=0), INVALID),
-    (dict(n=16), INVALID), (dict(T=65), UNSUPPORTED), (dict(H=192), UNSUPPORTED), (dict(I=64), UNSUPPORTED),
+    (dict(n=16), INVALID), (dict(out=A[0]), INVALID), (dict(out=ctypes.c_void_p(0x10000 + 512)), INVALID), (dict(T=65), UNSUPPORTED), (dict(H=192), UNSUPPORTED), (dict(I=64), UNSUPPORTED),
     (dict(H=1 << 16), UNSUPPORTED), (dict(I=1 << 16), UNSUPPORTED)], ids=str)
 def test_decode_refuses(lib, kw, rc):
     assert decode(lib, **kw) == rc

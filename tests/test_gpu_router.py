@@ -248,7 +248,7 @@ def test_backward_takes_foreign_indices():
         moe.moe_router_topk_backward(dw.cuda(), d, idx.cuda(), d, cfg)
         torch.cuda.synchronize()
         ref = ob.router_topk_backward(torch.nan_to_num(dw).numpy(), l.double().numpy(), idx.numpy(), **oracle_kw(cfg))
-        assert np.abs(d.cpu().numpy() - ref).max() <= 64 * U * max(1.0, np.abs(dw[~dw.isnan()]).max().item()) * cfg.scale * 4
+        assert np.abs(d.cpu().numpy() - ref).max() <= 64 * U * max(1.0, dw[~dw.isnan()].abs().max().item()) * cfg.scale * 4
 
 
 def test_no_tokens_and_refusals():
