@@ -122,6 +122,13 @@ __device__ inline uint64_t match_key(uint32_t key, bool valid, int nbits) {
   return peers;
 }
 
+// LDS written by lanes of a wave is read by others of the same wave
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 template <int CTRL, int ROW_MASK>
 __device__ inline int dpp_or_zero(int v) {
   // lanes without a valid source (outside the row, or rows masked off) read 0

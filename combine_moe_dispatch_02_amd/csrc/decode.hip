@@ -110,13 +110,6 @@ __device__ inline int list_reached(const Reached& r, int16_t* list) {
   return readlane(upto, 63);
 }
 
-// LDS written by lanes of a wave is read by others of the same wave
-__device__ inline void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // ---------------------------------------------------------------------------------------
 // bf16 rows to MXFP8: a lane has 8 values, four lanes a block
 // ---------------------------------------------------------------------------------------

@@ -264,7 +264,7 @@ int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p
 // The codes go as above: a wave reads a token's row once and stores it to each of its pool rows.
 // The words do not: stored beside the rows, a word of each 128 columns lands alone in its line of the
 // tile-major array (20 of 92 us at 8192 x 4096, top-8). The first `scale_blocks` workgroups fill
-// them tile by tile instead, tile consecutive words at a time, and count as one more row of the tile.
+// them tile by tile instead, consecutive words at a time; a piece of a tile's words counts as one more row.
 // (Filling the codes tile by tile too reads every row K times: 122 us there.)
 struct DispatchQArgs {
   DispatchArgs d;               // x: the codes
@@ -273,11 +273,14 @@ struct DispatchQArgs {
   const int32_t* num_tiles;
   int32_t scale_blocks;
 };
-// Few, large workgroups, since each pays an L2 write-back to publish: 16 waves of up to 8 tokens, 32
-// workgroups for the scales (8192 x 4096, top-8: 78 us; 4 waves of 4 tokens with 128: 101).
+// Few, large workgroups, since each pays an L2 write-back to publish: 16 waves of up to 8 tokens and
+// 16 workgroups for the scales. 8192 x 4096, top-8: 89 us, of which the write-backs are 9 and the rows' writes
+// (278 MB in 4 KB pieces) nearly all the rest; 4 waves a workgroup 125, 256 workgroups of 16 waves 100,
+// 8 or 32 for the scales 112 or 91.
 constexpr int kQWaves = 16;
 constexpr int kQTokens = 8;
-constexpr int kQScaleBlocks = 32;
+constexpr int kQScaleBlocks = 16;
+constexpr int kQWords = 8;   // scale words of a row in an item
 
 // one more of tile ti is in; `more` rows count beside its real ones
 __device__ inline void count_tile(const DispatchArgs& a, int ti, int more) {
@@ -298,27 +301,65 @@ __global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(Dispat
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int words = (a.H + 127) >> 7;
 
+  // an item is eight of a tile's words a row: read along the rows, written along the tile
+  const int per_tile = (words + kQWords - 1) / kQWords;
   if ((int)blockIdx.x < b.scale_blocks) {
-    __shared__ int s_token[128];
-    const int tiles = min(b.num_tiles[0], a.pool_rows >> a.tile_shift);
-    for (int ti = blockIdx.x; ti < tiles; ti += b.scale_blocks) {
-      __syncthreads();
-      for (int r = threadIdx.x; r < a.tile; r += 64 * kQWaves) {
-        const int q = b.src[((int64_t)ti << a.tile_shift) + r];
-        s_token[r] = q < 0 ? -1 : (int)((uint32_t)q / (uint32_t)a.K);
+    __shared__ uint32_t s_word[kQWaves][128][kQWords + 1];
+    __shared__ int s_token[kQWaves][128];
+    const int items = min(b.num_tiles[0], a.pool_rows >> a.tile_shift) * per_tile;
+    const int first = (int)blockIdx.x * kQWaves, step = b.scale_blocks * kQWaves;
+    for (int it = first + w; it < items; it += step) {
+      const int ti = it / per_tile;
+      const int g0 = (it - ti * per_tile) * kQWords;
+      const int64_t row0 = (int64_t)ti << a.tile_shift;
+      for (int r = lane; r < a.tile; r += kWave) {
+        const int q = b.src[row0 + r];
+        s_token[w][r] = q < 0 ? -1 : (int)((uint32_t)q / (uint32_t)a.K);
       }
-      __syncthreads();
-      uint32_t* to = static_cast<uint32_t*>(a.pool_s) + ((int64_t)ti << a.tile_shift) * words;
-#pragma unroll 4
-      for (int i = threadIdx.x; i < words << a.tile_shift; i += 64 * kQWaves) {
-        const int t = s_token[i & (a.tile - 1)];
-        if (t >= 0) to[i] = b.x_s[(int64_t)t * words + (i >> a.tile_shift)];
+      wave_sync();
+      // two lanes a row, four words each
+      const int g = g0 + 4 * (lane & 1);
+      u32x4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = (lane >> 1) + 32 * j;
+        const int t = r < a.tile ? s_token[w][r] : -1;
+        v[j] = u32x4{0u, 0u, 0u, 0u};
+        if (t >= 0) {
+          const uint32_t* from = b.x_s + (int64_t)t * words;
+          if (g + 4 <= words) {
+            __builtin_memcpy(&v[j], from + g, 16);
+          } else {
+            for (int k = 0; k < 4; ++k)
+              if (g + k < words) v[j][k] = from[g + k];
+          }
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = (lane >> 1) + 32 * j;
+        if (r < a.tile)
+          for (int k = 0; k < 4; ++k) s_word[w][r][4 * (lane & 1) + k] = v[j][k];
+      }
+      wave_sync();
+      uint32_t* to = static_cast<uint32_t*>(a.pool_s) + row0 * words;
+      for (int r = lane; r < a.tile; r += kWave) {
+        if (s_token[w][r] < 0) continue;   // padding rows' words are left alone
+#pragma unroll
+        for (int k = 0; k < kQWords; ++k)
+          if (g0 + k < words) to[((int64_t)(g0 + k) << a.tile_shift) + r] = s_word[w][r][k];
+      }
+      wave_sync();
     }
     __syncthreads();
     if (w != 0) return;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    for (int ti = blockIdx.x + lane * b.scale_blocks; ti < tiles; ti += 64 * b.scale_blocks) count_tile(a, ti, 1);
+    // this workgroup's items: kQWaves at `first`, then every `step`
+    for (int n = lane;; n += 64) {
+      const int it = first + n / kQWaves * step + n % kQWaves;
+      if (first + n / kQWaves * step >= items) break;
+      if (it < items) count_tile(a, it / per_tile, per_tile);
+    }
     return;
   }
 
@@ -356,7 +397,7 @@ __global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(Dispat
   const int npairs = (min(a.T, tb + kQWaves * tpw) - tb) * a.K;
   for (int q = lane; q < npairs; q += 64) {
     const int p = a.pos[(int64_t)tb * a.K + q];
-    if (p >= 0 && p < a.pool_rows) count_tile(a, p >> a.tile_shift, 1);
+    if (p >= 0 && p < a.pool_rows) count_tile(a, p >> a.tile_shift, per_tile);
   }
 }
 

@@ -158,13 +158,6 @@ __device__ inline uint64_t token_lane(uint64_t v, int sub, int k) {
   return ((uint64_t)token_lane<L>((uint32_t)(v >> 32), sub, k) << 32) | token_lane<L>((uint32_t)v, sub, k);
 }
 
-// LDS written by lanes of a wave is read by others of the same wave
-__device__ inline void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 __device__ inline float sigmoidf(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 // ---------------------------------------------------------------------------------------
