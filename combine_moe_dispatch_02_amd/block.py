@@ -15,7 +15,7 @@ from typing import Optional
 import torch
 
 from . import _abi
-from ._abi import MOE_BF16, MOE_F32, MOE_FP8_E4M3_G128, MOE_MXFP4, check, load
+from ._abi import MOE_BF16, MOE_F32, MOE_FP8_E4M3_G128, MOE_MXFP4, MoeError, check, load
 from .layer import Plan, Workspace, _dtype_code, _need_cuda
 
 __all__ = [
@@ -202,6 +202,8 @@ def moe_dispatch_quantized(q: torch.Tensor, q_s: torch.Tensor, plan: Plan, pool:
     """moe_dispatch of rows that are codes [T, H] with row-major scales (quantized_scales()) already."""
     dev = _device(q, "q")
     code = _dtype_code(dtype)
+    if code == MOE_BF16:                      # a bf16 pool has no codes to take (and no scales)
+        raise MoeError("moe_dispatch_quantized", _abi.MOE_ERR_INVALID)
     if q.dim() != 2 or pool.dim() != 2:
         raise ValueError("q must be [T, H], pool [pool rows, H]")
     H, rows = q.shape[1], pool.shape[0]
@@ -212,7 +214,7 @@ def moe_dispatch_quantized(q: torch.Tensor, q_s: torch.Tensor, plan: Plan, pool:
         raise ValueError("pool_s holds fewer scale words than the pool has")
     c = plan.c()
     _launch("moe_dispatch_quantized", dev, stream,
-            _ptr(q, "q", dev, (plan.T, H), _CODES), None if code == MOE_BF16 else _scales(q_s, "q_s", dev, plan.T, H, code),
+            _ptr(q, "q", dev, (plan.T, H), _CODES), _scales(q_s, "q_s", dev, plan.T, H, code),
             H, code, ctypes.byref(c), rows, _ptr(pool, "pool", dev, (rows, H), _CODES),
             _ptr(pool_s, "pool_s", dev, pool_s.shape, (_F32, _U8)), epoch, ws.buf.data_ptr(), ws.nbytes)
 
