@@ -271,6 +271,7 @@ struct DispatchQArgs {
   const uint32_t* x_s;          // [T][ceil(H / 128)]
   const int32_t* src;
   const int32_t* num_tiles;
+  int32_t max_tiles;            // that pool and plan have room for
   int32_t scale_blocks;
 };
 // Few, large workgroups, since each pays an L2 write-back to publish: 16 waves of up to 8 tokens and
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(Dispat
   if ((int)blockIdx.x < b.scale_blocks) {
     __shared__ uint32_t s_word[kQWaves][128][kQWords + 1];
     __shared__ int s_token[kQWaves][128];
-    const int items = min(b.num_tiles[0], a.pool_rows >> a.tile_shift) * per_tile;
+    const int items = min(b.num_tiles[0], b.max_tiles) * per_tile;
     const int first = (int)blockIdx.x * kQWaves, step = b.scale_blocks * kQWaves;
     for (int it = first + w; it < items; it += step) {
       const int ti = it / per_tile;
@@ -314,7 +315,7 @@ __global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(Dispat
       const int64_t row0 = (int64_t)ti << a.tile_shift;
       for (int r = lane; r < a.tile; r += kWave) {
         const int q = b.src[row0 + r];
-        s_token[w][r] = q < 0 ? -1 : (int)((uint32_t)q / (uint32_t)a.K);
+        s_token[w][r] = q < 0 || q >= a.T * a.K ? -1 : (int)((uint32_t)q / (uint32_t)a.K);
       }
       wave_sync();
       // two lanes a row, four words each
@@ -427,6 +428,7 @@ int launch_dispatch_quantized(const void* q, const void* q_s, int32_t H, const m
   b.x_s = static_cast<const uint32_t*>(q_s);
   b.src = p.src;
   b.num_tiles = p.num_tiles;
+  b.max_tiles = std::min(pool_rows, p.rows_cap) / p.tile;
   const int cus = std::max(1, device_cu_count());
   a.tokens_per_wave = std::max(1, std::min(kQTokens, p.T / (8 * cus)));
   b.scale_blocks = std::min(p.rows_cap / p.tile, kQScaleBlocks);
