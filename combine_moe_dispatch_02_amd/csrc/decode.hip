@@ -22,6 +22,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
@@ -139,10 +140,10 @@ __global__ __launch_bounds__(256) void decode_quantise_kernel(const uint16_t* x,
 }
 
 // ---------------------------------------------------------------------------------------
-// h: grid (I / 32 column blocks, slots); the waves share K. An expert of more than 16 tokens takes
-// them 16 at a time and reads its weights again (from the caches) for every 16.
+// h: grid (I / 32 column blocks, slots); the waves share K. An expert of more than 16 C tokens takes
+// them 16 C at a time and reads its weights again (from the caches) for every 16 C.
 // ---------------------------------------------------------------------------------------
-template <int NW, int U>
+template <int NW, int U, int C>
 __global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
   __shared__ Reached reached;
   __shared__ int16_t s_q[kDecodeTokens];              // the expert's pairs, one of each of its tokens
@@ -177,19 +178,27 @@ __global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, (uint32_t)a.T * (uint32_t)a.H);
   const __amdgpu_buffer_rsrc_t xsr = make_rsrc(a.x_s, (uint32_t)a.T * (uint32_t)KB * 4u);
 
-  for (int c0 = 0; c0 < n; c0 += 16) {
-    const int c = c0 + l16;
-    const uint32_t t = c < n ? (uint32_t)s_q[c] / (uint32_t)a.K : 0u;
+  // C times 16 tokens from c0 on
+  const auto pass = [&](auto columns, int c0) {
+    constexpr int N = columns;
     // tokens past the last: past the buffers, zeros
-    const uint32_t xo = c < n ? t * (uint32_t)a.H + (uint32_t)lhi * 16u : kNowhere;
-    const uint32_t xso = c < n ? t * (uint32_t)KB * 4u + (uint32_t)lhi : kNowhere;
-    f32x4 acc[4];
+    uint32_t xo[N], xso[N];
+    bool on[N];
+    f32x4 acc[N][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < N; ++g) {
+      const int c = c0 + g * 16 + l16;
+      on[g] = c < n;
+      const uint32_t t = on[g] ? (uint32_t)s_q[c] / (uint32_t)a.K : 0u;
+      xo[g] = t * (uint32_t)a.H + (uint32_t)lhi * 16u;
+      xso[g] = t * (uint32_t)KB * 4u + (uint32_t)lhi;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     // K blocks wave, wave + NW, ...: at every moment the waves read neighbouring tiles
     for (int kb0 = wave; kb0 < KB; kb0 += NW * U) {
-      u32x4 wt[U][4], b0[U], b1[U];
-      uint32_t wsc[U][4], sb[U];
+      u32x4 wt[U][4], b0[U][N], b1[U][N];
+      uint32_t wsc[U][4], sb[U][N];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const uint32_t kb = (uint32_t)(kb0 + u * NW);   // past KB: weights past the buffer, zeros
@@ -198,52 +207,63 @@ __global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
           wt[u][i] = buf_load16_nt(wr[i], kb * 1024u + (uint32_t)lane * 16u);
           wsc[u][i] = buf_load1(sr[i], kb * 64u + (uint32_t)lane);
         }
-        const bool in = kb < (uint32_t)KB && c < n;
-        b0[u] = buf_load16(xr, in ? xo + kb * 128u : kNowhere);
-        b1[u] = buf_load16(xr, in ? xo + kb * 128u + 64u : kNowhere);
-        sb[u] = buf_load1(xsr, in ? xso + kb * 4u : kNowhere);
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+          const bool in = kb < (uint32_t)KB && on[g];
+          b0[u][g] = buf_load16(xr, in ? xo[g] + kb * 128u : kNowhere);
+          b1[u][g] = buf_load16(xr, in ? xo[g] + kb * 128u + 64u : kNowhere);
+          sb[u][g] = buf_load1(xsr, in ? xso[g] + kb * 4u : kNowhere);
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = mfma_mx(wt[u][i], wsc[u][i], b0[u], b1[u], sb[u], acc[i]);
+        for (int g = 0; g < N; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[g][i] = mfma_mx(wt[u][i], wsc[u][i], b0[u][g], b1[u][g], sb[u][g], acc[g][i]);
     }
 
     // the waves' sums, then SwiGLU and the MXFP8 of 32 columns: lane (l16, lhi) has token column
     // l16 and columns 4 lhi .. + 4 of both tiles of 16
-    if (c0 > 0) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_red[wave][i][lane] = acc[i];
-    __syncthreads();
-    if (wave != 0) continue;
-    f32x4 s[4];
+    for (int g = 0; g < N; ++g) {
+      if (c0 + g > 0) __syncthreads();                // wave 0 has read the sums before
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] = s_red[0][i][lane];
+      for (int i = 0; i < 4; ++i) s_red[wave][i][lane] = acc[g][i];
+      __syncthreads();
+      if (wave != 0) continue;
+      f32x4 s[4];
 #pragma unroll
-      for (int v = 1; v < NW; ++v) s[i] += s_red[v][i][lane];
+      for (int i = 0; i < 4; ++i) {
+        s[i] = s_red[0][i][lane];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) s[i] += s_red[v][i][lane];
+      }
+      float h[8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float gate = s[j >> 2][j & 3], up = s[2 + (j >> 2)][j & 3];
+        h[j] = gate / (1.0f + __expf(-gate)) * up;
+        m = max(m, __builtin_bit_cast(uint32_t, h[j]) & 0x7fffffffu);
+      }
+      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      const bool bad = m >= 0x7f800000u;
+      const int ex = mx_e4m3_shared_exp(__builtin_bit_cast(float, m));
+      const float inv = mx_inv_scale(ex);
+      if (on[g]) {
+        const int64_t p = s_q[c0 + g * 16 + l16];
+        uint32_t* d = reinterpret_cast<uint32_t*>(a.h + p * a.I + nb * 32 + lhi * 4);
+        d[0] = bad ? 0u : pack_e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+        d[4] = bad ? 0u : pack_e4m3x4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
+        if (lhi == 0) a.h_s[p * (a.I >> 5) + nb] = (uint8_t)(bad ? 255 : ex + 127);
+      }
     }
-    float h[8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float gate = s[j >> 2][j & 3], up = s[2 + (j >> 2)][j & 3];
-      h[j] = gate / (1.0f + __expf(-gate)) * up;
-      m = max(m, __builtin_bit_cast(uint32_t, h[j]) & 0x7fffffffu);
-    }
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-    const bool bad = m >= 0x7f800000u;
-    const int ex = mx_e4m3_shared_exp(__builtin_bit_cast(float, m));
-    const float inv = mx_inv_scale(ex);
-    if (c < n) {
-      const int64_t p = s_q[c];
-      uint32_t* d = reinterpret_cast<uint32_t*>(a.h + p * a.I + nb * 32 + lhi * 4);
-      d[0] = bad ? 0u : pack_e4m3x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-      d[4] = bad ? 0u : pack_e4m3x4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv);
-      if (lhi == 0) a.h_s[p * (a.I >> 5) + nb] = (uint8_t)(bad ? 255 : ex + 127);
-    }
-  }
+  };
+  for (int c0 = 0; c0 < n; c0 += 16 * C)
+    if (C > 1 && n - c0 > 16) pass(std::integral_constant<int, C>(), c0);
+    else pass(std::integral_constant<int, 1>(), c0);
 }
 
 // A token's experts and weights in a lane's registers, so that finding its pair with an expert
@@ -274,9 +294,9 @@ struct TokenPairs {
 
 // ---------------------------------------------------------------------------------------
 // out: a workgroup has 16 columns of out for all tokens; its waves share the (expert, K block)
-// pairs evenly. An expert's tokens are gathered into the columns of the product, eight at a time
-// (more than eight are rare: 64 tokens on 128 experts have four each), and the columns' sums go to
-// their tokens' sums in the wave's part of LDS.
+// pairs evenly. An expert's tokens are gathered into the columns of the product, eight at a time, or
+// sixteen where it has more (8 experts with 64 tokens each at H 5120, eight at a time: 92 us, so 64),
+// and the columns' sums go to their tokens' sums in the wave's part of LDS.
 //
 // A weight tile is one load, and what belongs to it must not cost several: the address unit
 // takes as long for a scattered load of 16 bytes a lane as for a weight tile, and with two of
@@ -294,7 +314,7 @@ __global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
   __shared__ f32x4 s_sum[NW][4][TOK];                 // [wave][columns 4 lhi ..][token]
   __shared__ int16_t s_pair[NW][TOK], s_token[NW][TOK];
   __shared__ float s_weight[NW][TOK];
-  __shared__ u32x4 s_h[NW][U][COLS][8];               // a column's 128 codes, 16-byte chunk k at k ^ column
+  __shared__ u32x4 s_h[NW][U * COLS][8];              // a column's 128 codes, 16-byte chunk k at k ^ column % 8
   __shared__ uint32_t s_scale[NW][U * 16];            // weight scales, 64 bytes a tile
   const int lane = lane_id(), l16 = lane & 15, lhi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -334,51 +354,68 @@ __global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
     wave_sync();
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w2 + ((int64_t)e * (a.H >> 4) + rb) * tiles, tiles);
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.w2_s + ((int64_t)e * (a.H >> 4) + rb) * tscales, tscales);
-    for (int c0 = 0; c0 < n; c0 += COLS) {
+    // G times 8 columns from c0 on
+    const auto pass = [&](auto groups, int c0) {
+      constexpr int G = groups;
+      constexpr int R = U / G;                        // K blocks that LDS holds at a time
       // loading: 2^p >= the columns, eight lanes a column's 128 codes, 8 >> p K blocks a load
-      const int cols = min(COLS, n - c0);
+      const int cols = min(COLS * G, n - c0);
       const int p = cols > 4 ? 3 : cols > 2 ? 2 : cols > 1 ? 1 : 0;
       const int lc = (lane >> 3) & ((1 << p) - 1), chunk = lane & 7, lu = lane >> (3 + p);
-      const uint32_t from = lc < cols ? (uint32_t)s_pair[wave][c0 + lc] * (uint32_t)a.I + (uint32_t)chunk * 16u : kNowhere;
+      uint32_t from[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        from[g] = g * COLS + lc < cols ? (uint32_t)s_pair[wave][c0 + g * COLS + lc] * (uint32_t)a.I + (uint32_t)chunk * 16u : kNowhere;
       // computing: column l16
       const bool mine = l16 < cols;
       const uint32_t hso = mine ? (uint32_t)s_pair[wave][c0 + l16] * (uint32_t)(a.I >> 5) : 0u;
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
       for (int kb0 = kb_first; kb0 < kb_last; kb0 += U) {
-        u32x4 w[U], h[U];
+        u32x4 w[U], h[G][U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
           w[u] = buf_load16_nt(wr, kb0 + u < kb_last ? (uint32_t)(kb0 + u) * 1024u + (uint32_t)lane * 16u : kNowhere);
         const uint32_t ws = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(sr, (uint32_t)kb0 * 64u + (uint32_t)lane * 4u, 0, 0);
 #pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (i == 0 || i < (1 << p) / 2) {           // (1 << p) * U columns of K blocks, 8 a load
-            const int u = i * (8 >> p) + lu;
-            h[i] = buf_load16(hr, u < U && kb0 + u < kb_last && from != kNowhere ? from + (uint32_t)(kb0 + u) * 128u : kNowhere);
-          }
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int i = 0; i < U; ++i)
+            if (i == 0 || G > 1 || i < (1 << p) / 2) {  // (1 << p) * U columns of K blocks, 8 a load
+              const int u = i * (8 >> p) + lu;
+              h[g][i] = buf_load16(hr, u < U && kb0 + u < kb_last && from[g] != kNowhere ? from[g] + (uint32_t)(kb0 + u) * 128u : kNowhere);
+            }
         const u32x4 hs = buf_load16(hsr, mine ? hso + (uint32_t)kb0 * 4u : kNowhere);
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          if (i == 0 || i < (1 << p) / 2) {
-            const int u = i * (8 >> p) + lu;
-            if (u < U) s_h[wave][u][lc][chunk ^ lc] = h[i];
-          }
         s_scale[wave][lane] = ws;
-        wave_sync();
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          // K blocks past the last have zero weights and codes, and no NaN for a scale
-          const bool in = kb0 + u < kb_last;
-          const int c = l16 & (COLS - 1);
-          u32x4 b0 = s_h[wave][u][c][lhi ^ c], b1 = s_h[wave][u][c][(lhi + 4) ^ c];
-          if (!mine) b0 = b1 = u32x4{0u, 0u, 0u, 0u};
-          const uint32_t wb = reinterpret_cast<const uint8_t*>(s_scale[wave])[u * 64 + lane];
-          acc = mfma_mx(w[u], in ? wb : 0u, b0, b1, in ? hs[u] >> (8 * lhi) : 0u, acc);
+        for (int r = 0; r < G; ++r) {
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int i = r * R; i < (r + 1) * R; ++i)
+              if (i == 0 || G > 1 || i < (1 << p) / 2) {
+                const int u = i * (8 >> p) + lu;
+                if (u < U) s_h[wave][((u - r * R) * G + g) * COLS + lc][chunk ^ lc] = h[g][i];
+              }
+          wave_sync();
+#pragma unroll
+          for (int u = r * R; u < (r + 1) * R; ++u) {
+            // K blocks past the last have zero weights and codes, and no NaN for a scale
+            const bool in = kb0 + u < kb_last;
+            const int c = l16 & (COLS * G - 1), x = c & (COLS - 1);
+            const u32x4* col = s_h[wave][(u - r * R) * G * COLS + c];
+            u32x4 b0 = col[lhi ^ x], b1 = col[(lhi + 4) ^ x];
+            if (!mine) b0 = b1 = u32x4{0u, 0u, 0u, 0u};
+            const uint32_t wb = reinterpret_cast<const uint8_t*>(s_scale[wave])[u * 64 + lane];
+            acc = mfma_mx(w[u], in ? wb : 0u, b0, b1, in ? hs[u] >> (8 * lhi) : 0u, acc);
+          }
+          wave_sync();
         }
-        wave_sync();
       }
       if (mine) s_sum[wave][lhi][s_token[wave][c0 + l16]] += s_weight[wave][c0 + l16] * acc;   // a token has one column
-    }
+    };
+    for (int c0 = 0; c0 < n; c0 += 2 * COLS)
+      if (n - c0 > COLS) pass(std::integral_constant<int, 2>(), c0);
+      else pass(std::integral_constant<int, 1>(), c0);
     wave_sync();
   }
 
@@ -436,8 +473,12 @@ int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t 
   // 8 waves a workgroup for few pairs, whose workgroups leave the CUs room, 4 for more. 8 against 4, of 128
   // experts at H 4096: 11.6 / 13.2 us (8 pairs), 33.5 / 34.8 (32), 58.6 / 52.9 (64); two of them on one
   // of 8 ranks at H 7168: 12.5 / 15.4
-  if (T * K <= 32) hipLaunchKernelGGL((decode_h_kernel<8, 2>), gh, dim3(512), 0, stream, a);
-  else hipLaunchKernelGGL((decode_h_kernel<4, 2>), gh, dim3(256), 0, stream, a);
+  if (T * K <= 32) hipLaunchKernelGGL((decode_h_kernel<8, 2, 1>), gh, dim3(512), 0, stream, a);
+  // 32 tokens for one read of the weights where the experts have more than 8 pairs on average and so
+  // some of them more than 16 tokens; it leaves room for 3 waves a SIMD instead of 5. 32 against 16: 49 / 68 us (8 experts with
+  // 64 tokens each, H 5120), 24 / 31 (16 with up to 24, H 4096), 59 / 53 (64 with 8), 148 / 130 (127 with 4)
+  else if (T > 16 && T * K > 8 * E) hipLaunchKernelGGL((decode_h_kernel<4, 2, 2>), gh, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL((decode_h_kernel<4, 2, 1>), gh, dim3(256), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   // 16 waves a workgroup where that is one workgroup a CU at most and each wave has a dozen tiles and more
   // (16 against 8 waves: 9.0 / 8.5 us at 96 tiles a workgroup, 80 / 95 at 1536)

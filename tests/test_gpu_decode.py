@@ -111,6 +111,18 @@ def test_every_token_to_the_same_experts_and_doubled_ids():
     assert close(c.run(c.quantised()), c.ref())
 
 
+@pytest.mark.parametrize("E", [2, 40])
+@pytest.mark.parametrize("n", [7, 8, 9, 15, 16, 17, 24, 25, 31, 32, 33, 40, 41, 48, 49, 63, 64])
+def test_an_expert_of_n_tokens(n, E):
+    """n tokens for one expert next to one that all 64 reach: every count of column groups, whole and partly
+    filled, where the experts are few and where they are many. The n tokens are spread over the batch."""
+    say("decode expert of n tokens", n, E)
+    c = Case(64, 384, 640, E, 2, seed=8)
+    c.idx[:, 0], c.idx[:, 1] = E - 1, -1
+    c.idx[torch.randperm(64, generator=torch.Generator().manual_seed(n))[:n], 1] = 0
+    assert close(c.run(), c.ref())
+
+
 def test_1024_experts():
     say("decode 1024 experts")
     c = Case(64, 128, 128, 1024, 16, seed=7)
