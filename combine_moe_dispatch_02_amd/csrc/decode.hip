@@ -17,7 +17,7 @@
 // the waves in order, so out needs no second pass and no atomics.
 //
 // H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 12 + 8 us (80 MB),
-// 64 tokens 123 + 72 us (1.26 GB: 7.3 and 5.8 TB/s). The pooled path takes 125 and 395 us.
+// 64 tokens 123 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 125 and 385 us.
 #include "common.h"
 #include "kernels.h"
 
