@@ -13,11 +13,11 @@ constexpr int kWave = 64;
 // --------------------------------------------------------------------------
 // workspace layout (shared by every entry point; offsets depend only on shape)
 // --------------------------------------------------------------------------
-constexpr int kPlanWaves = 4;            // waves per plan block
-constexpr int kPairsPerWave = 1024;      // pairs one plan wave ranks (at most)
-// a batch that one plan block covers is split over all of its waves
-inline int32_t plan_pairs_per_wave(int64_t pairs) {
-  return pairs <= (int64_t)kPlanWaves * kPairsPerWave ? kPairsPerWave / 4 : kPairsPerWave;
+constexpr int kPlanWaves = 16;           // waves per plan block
+constexpr int kPairsPerWave = 256;       // pairs one plan wave ranks (at most)
+// pairs per column: one block of one wave a column for small batches, then four waves a column
+inline int32_t plan_pairs_per_column(int64_t pairs) {
+  return pairs <= (int64_t)kPlanWaves * kPairsPerWave ? kPairsPerWave : 4 * kPairsPerWave;
 }
 
 struct WsLayout {
@@ -61,7 +61,7 @@ inline WsLayout ws_layout(int32_t T, int32_t K, int32_t E, int32_t tile, int64_t
   WsLayout L;
   const int64_t pairs = (int64_t)T * K;
   const int64_t cap = pool_rows_bound(T, K, E, tile);
-  L.ppw = plan_pairs_per_wave(pairs);
+  L.ppw = plan_pairs_per_column(pairs);
   L.ncols = (int32_t)((pairs + L.ppw - 1) / L.ppw);
   L.ntiles_cap = (int32_t)(cap / tile);
   L.fill = align_up(L.hist + (size_t)L.ncols * E * 4, 256);

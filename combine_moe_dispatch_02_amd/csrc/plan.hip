@@ -7,19 +7,20 @@
 // ids outside [expert_begin, expert_begin + E_local) are not local.
 //
 // Scheme (no global atomics on counts, so every result is deterministic):
-//   column c = one wave's run of ppw consecutive pairs (1024; 256 when one block
-//           covers the batch, so that its four waves share it).
-//   pass 1  each wave counts its column per expert: per 64 pairs, lanes with the
-//           same expert are matched with one ballot per key bit, the lowest lane
-//           of each group adds the group size to the wave's LDS counter row.
-//           Counts go to hist[c][e]. The last block to finish (a device-scope
-//           counter) reduces hist over columns into counts, scans the padded
-//           counts into offsets (DPP wave scan), turns hist into per-column
-//           bases, and writes tile_expert, num_tiles and the padding rows of src.
-//   pass 2  each wave re-ranks its column the same way; a pair's row is
-//           base[c][e] + (pairs of e earlier in the column), with the in-wave
-//           part from mbcnt over the group mask. Writes pos and src.
-// With a single block both passes run in one launch.
+//   column c = a run of ppw consecutive pairs (1024; 256 for small batches), shared by W waves of a
+//           block in order, so that a wave has 512 pairs at most.
+//   pass 1  each wave counts its pairs per expert in its LDS row (LDS atomics); the column's sums
+//           go to hist[c][e]. The last block to finish (a device-scope counter) reduces hist over
+//           columns into counts, scans the padded counts into offsets (DPP wave scan) and turns
+//           hist into per-column bases, several threads to an expert.
+//   pass 2  each wave counts again, takes its bases from hist and the column's earlier waves, and
+//           ranks its pairs: per 64 pairs, lanes with the same expert are matched with one
+//           ballot per key bit, and a pair's row is the base plus its rank in the lane mask. Writes
+//           pos and src; the plan's other arrays are filled by all blocks.
+// With a single block both passes run in one launch and the columns' counts stay in LDS. It is latency
+// alone: 128 experts, 65536 pairs 9.5 + 6.3 us (count and place), 8192 pairs 10.1, 1024 pairs 6.0; with one wave
+// a column, a serial scan and fills a thread an expert 19.9 + 9.8, 15.0 + 7.9 and 14.7.
+#include <algorithm>
 #include <mutex>
 
 #include "common.h"
@@ -42,6 +43,8 @@ struct PlanArgs {
   int32_t nfill;          // entries of the workspace's fill counters
   int32_t ncols;
   int32_t ppw;            // pairs per column
+  int32_t col_waves;      // W: waves a column
+  int32_t lanes_log2;     // scan: log2 of the threads side by side, which have the experts
   int32_t* counts;
   int32_t* offsets;
   int32_t* pos;
@@ -55,198 +58,238 @@ struct PlanArgs {
   uint32_t* tiles_done;   // dispatch's count of raised ready flags
 };
 
-// One wave's walk over its column. COUNT_ONLY: accumulate counts in run[];
-// otherwise run[] holds the column's bases and rows are written.
-template <bool COUNT_ONLY>
-__device__ inline void rank_column(const PlanArgs& a, int col, int* run) {
-  const int lane = lane_id();
-  const int begin = col * a.ppw;
-  const int end = min(begin + a.ppw, a.pairs);
-  // the column's ids are loaded up front: one memory round trip instead of one per
-  // 64 pairs (the walk below is serial through run[])
-  constexpr int kIters = kPairsPerWave / kWave;
-  int ids[kIters];
+constexpr int kScanThreads = 64 * kPlanWaves;
+constexpr int kWaveIters = 8;   // of 64 pairs a wave
+constexpr int kScanKeep = 32;   // columns a scan thread keeps in registers
+
+// A wave's pairs [begin, end): the local experts, -1 for none. Loaded up front, all in flight.
+struct WavePairs {
+  int begin, end;
+  int e[kWaveIters];
+  __device__ void load(const PlanArgs& a, int col, int part) {
+    const int lane = lane_id();
+    const int per_wave = a.ppw / a.col_waves;
+    const int stop = min(a.pairs, (int)min((int64_t)a.pairs, ((int64_t)col + 1) * a.ppw));
+    begin = (int)min((int64_t)stop, (int64_t)col * a.ppw + (int64_t)part * per_wave);
+    end = min(stop, begin + per_wave);
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(a.topk_idx + begin, (uint32_t)(end - begin) * 4u);
 #pragma unroll
-  for (int i = 0; i < kIters; ++i) {
-    const int q = begin + i * kWave + lane;
-    ids[i] = q < end ? a.topk_idx[q] : -1;
+    for (int i = 0; i < kWaveIters; ++i) {
+      const int id = (int)__builtin_amdgcn_raw_buffer_load_b32(r, (uint32_t)(i * kWave + lane) * 4u, 0, 0);
+      const int x = id - a.expert_begin;
+      e[i] = begin + i * kWave + lane < end && id >= a.expert_begin && x < a.E ? x : -1;
+    }
   }
+  // run[e] = the wave's pairs of e
+  __device__ void count(const PlanArgs& a, int* run) const {
+    for (int x = lane_id(); x < a.E; x += kWave) run[x] = 0;
+    wave_sync();
 #pragma unroll
-  for (int i = 0; i < kIters; ++i) {
-    const int base = begin + i * kWave;
-    if (base >= end) break;
-    const int q = base + lane;
-    const bool in = q < end;
-    const int id = ids[i];
-    const int e = id - a.expert_begin;
-    const bool local = in && id >= a.expert_begin && e < a.E;
-    const uint64_t peers = match_key(local ? (uint32_t)e : 0u, local, a.key_bits);
-    const int rank = mask_rank(peers);
-    const int cnt = __popcll(peers);
-    if (COUNT_ONLY) {
-      if (local && rank == 0) run[e] += cnt;
-    } else {
+    for (int i = 0; i < kWaveIters; ++i)
+      if (e[i] >= 0) atomicAdd(&run[e[i]], 1);
+  }
+  // run[e] = the row of the wave's first pair of e
+  __device__ void place(const PlanArgs& a, int* run) const {
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < kWaveIters; ++i) {
+      const int q = begin + i * kWave + lane;
+      if (begin + i * kWave >= end) break;
+      const bool local = e[i] >= 0;
+      const uint64_t peers = match_key(local ? (uint32_t)e[i] : 0u, local, a.key_bits);
+      const int rank = mask_rank(peers);
       int row = -1;
       if (local) {
-        const int b = run[e];
+        const int b = run[e[i]];
         row = b + rank;
-        if (rank == 0) run[e] = b + cnt;
+        if (rank == 0) run[e[i]] = b + __popcll(peers);
       }
-      if (in) a.pos[q] = row;
+      if (q < end) a.pos[q] = row;
       if (local) a.src[row] = q;
     }
   }
+};
+
+// Counts of the column's waves to bases, from the column's in hist: the lanes of its waves share the experts.
+__device__ inline void wave_bases(const PlanArgs& a, int col, int part, int first_base, int (*rows)[kMaxExperts]) {
+  for (int e = part * kWave + lane_id(); e < a.E; e += kWave * a.col_waves) {
+    int run = e < kWave * a.col_waves ? first_base : a.hist[(int64_t)col * a.E + e];
+    for (int v = 0; v < a.col_waves; ++v) {
+      const int c = rows[v][e];
+      rows[v][e] = run;
+      run += c;
+    }
+  }
 }
 
-// Block-wide exclusive scan of up to 4 ints per thread (256 threads); returns the
-// total. scratch: 4 ints of LDS.
-__device__ inline int block_exclusive_scan4(int v[4], int* scratch) {
+// What the plan holds beside pos and the real rows of src, by `waves` waves: padding rows, tile
+// owners, and a fresh start for the dispatch that follows.
+__device__ void plan_fill(const PlanArgs& a, const int* counts, const int* offsets, int wave, int waves) {
   const int lane = lane_id();
-  const int w = threadIdx.x >> 6;
-  const int s = v[0] + v[1] + v[2] + v[3];
-  const int incl = wave_inclusive_scan(s);
-  if (lane == 63) scratch[w] = incl;
-  __syncthreads();
-  int wave_base = 0, total = 0;
-  for (int i = 0; i < 4; ++i) {
-    const int t = scratch[i];
-    if (i < w) wave_base += t;
-    total += t;
+  for (int e = wave; e < a.E; e += waves) {
+    const int seg = offsets[e], seg_end = offsets[e + 1];
+    for (int r = seg + counts[e] + lane; r < seg_end; r += kWave) a.src[r] = -1;
+    for (int t = (seg >> a.tile_shift) + lane; t < (seg_end >> a.tile_shift); t += kWave) a.tile_expert[t] = e;
   }
-  int run = wave_base + incl - s;
-  for (int i = 0; i < 4; ++i) {
-    const int x = v[i];
-    v[i] = run;
-    run += x;
-  }
-  __syncthreads();
-  return total;
+  const int P = offsets[a.E];
+  const int first = wave * kWave + lane, step = waves * kWave;
+  for (int t = (P >> a.tile_shift) + first; t < a.ntiles_cap; t += step) a.tile_expert[t] = -1;
+  for (int r = P + first; r < a.rows_cap; r += step) a.src[r] = -1;
+  for (int t = first; t < a.ntiles_cap; t += step) a.tile_ready[t] = 0u;
+  for (int t = first; t < a.nfill; t += step) a.tile_fill[t] = 0u;
+  if (first == 0) *a.tiles_done = 0u;
 }
 
-// The scan step, run by the last block of pass 1 (all 256 threads).
-__device__ void plan_scan(const PlanArgs& a, int* s_cnt, int* s_off, int* s_half, int* scratch) {
+struct ScanMem {
+  int cnt[kMaxExperts], off[kMaxExperts + 1], part[kScanThreads], wave[kPlanWaves];
+};
+
+// counts and offsets, in memory and in `m`, from thread e's count of expert e; by a whole block
+__device__ inline void plan_offsets(const PlanArgs& a, ScanMem& m, int count) {
   const int tid = threadIdx.x;
   const int E = a.E;
-  // counts: reduce the columns. With E <= 128 two threads share an expert, each
-  // summing half of the columns (s_half keeps the first half's sum for the bases
-  // below); the loops are unrolled so that 16 column loads are in flight at a time
-  // (one load per iteration would serialise their latency).
-  const bool split = E <= 128;
-  const int half = (a.ncols + 1) >> 1;
-  for (int x = tid; x < (split ? 2 * E : E); x += 256) {
-    const int e = split ? x >> 1 : x;
-    const int c0 = split && (x & 1) ? half : 0;
-    const int c1 = split && !(x & 1) ? half : a.ncols;
-    int c = 0;
-#pragma unroll 16
-    for (int col = c0; col < c1; ++col) c += a.hist[col * E + e];
-    if (split) {
-      const int other = __shfl_xor(c, 1);
-      if (!(x & 1)) s_half[e] = c;
-      c += other;
-    }
-    if (!split || !(x & 1)) {
-      s_cnt[e] = c;
-      a.counts[e] = c;
-    }
-  }
+  const int padded = tid < E ? ((count + a.tile - 1) >> a.tile_shift) << a.tile_shift : 0;
+  const int upto = wave_inclusive_scan(padded);
+  if (lane_id() == 63) m.wave[tid >> 6] = upto;
   __syncthreads();
-  // offsets: exclusive scan of the padded counts, 4 consecutive experts per thread
-  int v[4];
-  for (int i = 0; i < 4; ++i) {
-    const int e = tid * 4 + i;
-    v[i] = e < E ? ((s_cnt[e] + a.tile - 1) >> a.tile_shift) << a.tile_shift : 0;
+  int before = upto - padded, P = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    const int t = m.wave[w];
+    if (w < (tid >> 6)) before += t;
+    P += t;
   }
-  const int P = block_exclusive_scan4(v, scratch);
-  for (int i = 0; i < 4; ++i) {
-    const int e = tid * 4 + i;
-    if (e < E) {
-      s_off[e] = v[i];
-      a.offsets[e] = v[i];
-    }
+  if (tid < E) {
+    m.cnt[tid] = count;
+    m.off[tid] = before;
+    a.counts[tid] = count;
+    a.offsets[tid] = before;
   }
   if (tid == 0) {
-    s_off[E] = P;
+    m.off[E] = P;
     a.offsets[E] = P;
     a.num_tiles[0] = P >> a.tile_shift;
   }
   __syncthreads();
-  const int ntiles = P >> a.tile_shift;
-  // per-column bases, tile owners, padding rows
-  for (int x = tid; x < (split ? 2 * E : E); x += 256) {
-    const int e = split ? x >> 1 : x;
-    const bool second = split && (x & 1);
-    const int c0 = second ? half : 0;
-    const int c1 = split && !second ? half : a.ncols;
-    int run = s_off[e] + (second ? s_half[e] : 0);
+}
+
+// The scan step, run by the last block of pass 1 (all its threads): thread (part, e) has a run of
+// the columns of expert e.
+__device__ void plan_scan(const PlanArgs& a, ScanMem& m) {
+  const int tid = threadIdx.x;
+  const int E = a.E;
+  const int parts = kScanThreads >> a.lanes_log2;
+  const int e = tid & ((1 << a.lanes_log2) - 1), part = tid >> a.lanes_log2;
+  const int each = (a.ncols + parts - 1) / parts;
+  const int c0 = min(a.ncols, part * each), c1 = e < E ? min(a.ncols, c0 + each) : c0;
+  int32_t* h = a.hist + min(e, E - 1);
+  // the first columns stay in registers; loads past the last read it again
+  int v[kScanKeep];
+#pragma unroll
+  for (int i = 0; i < kScanKeep; ++i) v[i] = h[(int64_t)min(c0 + i, a.ncols - 1) * E];
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kScanKeep; ++i) {
+    v[i] = c0 + i < c1 ? v[i] : 0;
+    sum += v[i];
+  }
 #pragma unroll 16
-    for (int col = c0; col < c1; ++col) {
-      const int c = a.hist[col * E + e];
-      a.hist[col * E + e] = run;
-      run += c;
+  for (int col = c0 + kScanKeep; col < c1; ++col) sum += h[(int64_t)col * E];
+  m.part[tid] = sum;
+  __syncthreads();
+  // an expert's count, and the pairs before each part
+  int count = 0;
+  if (tid < E) {
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) {
+      const int c = m.part[(p << a.lanes_log2) + tid];
+      m.part[(p << a.lanes_log2) + tid] = count;
+      count += c;
     }
-    if (second) continue;
-    const int seg_end = s_off[e + 1];
-    for (int t = s_off[e] >> a.tile_shift; t < (seg_end >> a.tile_shift); ++t) a.tile_expert[t] = e;
-    for (int r = s_off[e] + s_cnt[e]; r < seg_end; ++r) a.src[r] = -1;
   }
-  for (int t = ntiles + tid; t < a.ntiles_cap; t += 256) a.tile_expert[t] = -1;
-  for (int r = P + tid; r < a.rows_cap; r += 256) a.src[r] = -1;
-  // a fresh start for the dispatch that follows
-  for (int t = tid; t < a.ntiles_cap; t += 256) a.tile_ready[t] = 0u;
-  for (int t = tid; t < a.nfill; t += 256) a.tile_fill[t] = 0u;
-  if (tid == 0) *a.tiles_done = 0u;
+  plan_offsets(a, m, count);
+  // per-column bases
+  int run = e < E ? m.off[e] + m.part[tid] : 0;
+#pragma unroll
+  for (int i = 0; i < kScanKeep; ++i) {
+    if (c0 + i < c1) h[(int64_t)(c0 + i) * E] = run;
+    run += v[i];
+  }
+#pragma unroll 16
+  for (int col = c0 + kScanKeep; col < c1; ++col) {
+    const int c = h[(int64_t)col * E];
+    h[(int64_t)col * E] = run;
+    run += c;
+  }
 }
 
-__global__ __launch_bounds__(256) void plan_count_kernel(PlanArgs a) {
+__global__ __launch_bounds__(kScanThreads) void plan_count_kernel(PlanArgs a) {
   __shared__ int s_run[kPlanWaves][kMaxExperts];
-  __shared__ int s_off[kMaxExperts + 1];
-  __shared__ int scratch[4];
+  __shared__ ScanMem s_scan;
   __shared__ int s_last;
-  const int w = threadIdx.x >> 6;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = lane_id();
-  const int col = blockIdx.x * kPlanWaves + w;
-  int* run = s_run[w];
-  for (int e = lane; e < a.E; e += kWave) run[e] = 0;
-  if (col < a.ncols) {
-    rank_column<true>(a, col, run);
-    for (int e = lane; e < a.E; e += kWave) a.hist[col * a.E + e] = run[e];
-  }
+  const int part = w % a.col_waves;
+  const int col = blockIdx.x * (kPlanWaves / a.col_waves) + w / a.col_waves;
+  WavePairs pairs;
+  pairs.load(a, min(col, a.ncols - 1), part);
+  if (col < a.ncols) pairs.count(a, s_run[w]);
   __syncthreads();
-  if (gridDim.x > 1) {
-    // the last block to finish scans; a single block needs no device-scope handshake
-    if (threadIdx.x == 0) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-      const uint32_t prev = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      s_last = prev == gridDim.x - 1;
+  if (gridDim.x == 1) {
+    // single block: the waves' counts are all there is, and the pairs are placed right away
+    int count = 0;
+    if (threadIdx.x < a.E) {
+#pragma unroll 4
+      for (int v = 0; v < a.ncols * a.col_waves; ++v) {
+        const int c = s_run[v][threadIdx.x];
+        s_run[v][threadIdx.x] = count;
+        count += c;
+      }
     }
-    __syncthreads();
-    if (!s_last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    plan_offsets(a, s_scan, count);
+    if (col < a.ncols) {
+      for (int e = lane; e < a.E; e += kWave) s_run[w][e] += s_scan.off[e];
+      wave_sync();
+      pairs.place(a, s_run[w]);
+    }
+    plan_fill(a, s_scan.cnt, s_scan.off, w, kPlanWaves);
+    return;
   }
-  // s_run doubles as the counts array of the scan (the waves' rows are done)
-  int* s_cnt = &s_run[0][0];
-  int* s_half = &s_run[1][0];
+  if (col < a.ncols) {
+    for (int e = part * kWave + lane; e < a.E; e += kWave * a.col_waves) {
+      int c = 0;
+      for (int v = w - part; v < w - part + a.col_waves; ++v) c += s_run[v][e];
+      a.hist[(int64_t)col * a.E + e] = c;
+    }
+  }
   __syncthreads();
-  plan_scan(a, s_cnt, s_off, s_half, scratch);
+  if (threadIdx.x == 0) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    const uint32_t prev = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = prev == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  plan_scan(a, s_scan);
   if (threadIdx.x == 0) __hip_atomic_store(a.done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (gridDim.x != 1) return;
-  // single block: place the pairs right away
-  __syncthreads();
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-  for (int e = lane; e < a.E; e += kWave) run[e] = col < a.ncols ? a.hist[col * a.E + e] : 0;
-  if (col < a.ncols) rank_column<false>(a, col, run);
 }
 
-__global__ __launch_bounds__(256) void plan_place_kernel(PlanArgs a) {
+__global__ __launch_bounds__(kScanThreads) void plan_place_kernel(PlanArgs a) {
   __shared__ int s_run[kPlanWaves][kMaxExperts];
-  const int w = threadIdx.x >> 6;
-  const int lane = lane_id();
-  const int col = blockIdx.x * kPlanWaves + w;
-  if (col >= a.ncols) return;
-  int* run = s_run[w];
-  for (int e = lane; e < a.E; e += kWave) run[e] = a.hist[col * a.E + e];
-  rank_column<false>(a, col, run);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = w % a.col_waves;
+  const int col = blockIdx.x * (kPlanWaves / a.col_waves) + w / a.col_waves;
+  const int e = part * kWave + lane_id();
+  WavePairs pairs;
+  pairs.load(a, min(col, a.ncols - 1), part);
+  const int first_base = a.hist[(int64_t)min(col, a.ncols - 1) * a.E + min(e, a.E - 1)];
+  if (col < a.ncols) pairs.count(a, s_run[w]);
+  __syncthreads();
+  if (col < a.ncols) wave_bases(a, col, part, first_base, s_run + (w - part));
+  __syncthreads();
+  if (col < a.ncols) pairs.place(a, s_run[w]);
+  plan_fill(a, a.counts, a.offsets, blockIdx.x * kPlanWaves + w, gridDim.x * kPlanWaves);
 }
 
 int launch_plan(const int32_t* topk_idx, const moe_plan_t& p, const WsLayout& L, char* ws,
@@ -266,6 +309,11 @@ int launch_plan(const int32_t* topk_idx, const moe_plan_t& p, const WsLayout& L,
   a.nfill = 2 * L.ntiles_cap;   // dispatch's and combine backward's counters (adjacent)
   a.ncols = L.ncols;
   a.ppw = L.ppw;
+  // Four waves a column of 1024 pairs, one a column of 256; two and four where a block then still has
+  // all columns: 8168 pairs in one launch of one block 8.5 us, in two of two blocks 9.3 + 5.4 (16384 pairs,
+  // one wave a column: 15.3 and 8.2 + 6.5)
+  a.col_waves = L.ncols <= kPlanWaves / 4 ? 4 : L.ppw == kPairsPerWave ? 1 : L.ncols <= kPlanWaves / 2 ? 2 : 4;
+  a.lanes_log2 = bits < 5 ? 5 : bits;   // 32 parts at most
   a.counts = p.counts;
   a.offsets = p.offsets;
   a.pos = p.pos;
@@ -277,11 +325,14 @@ int launch_plan(const int32_t* topk_idx, const moe_plan_t& p, const WsLayout& L,
   a.hist = reinterpret_cast<int32_t*>(ws + L.hist);
   a.done = reinterpret_cast<uint32_t*>(ws + L.done);
   a.tiles_done = reinterpret_cast<uint32_t*>(ws + L.tiles_done);
-  const int blocks = (L.ncols + kPlanWaves - 1) / kPlanWaves;
-  hipLaunchKernelGGL(plan_count_kernel, dim3(blocks), dim3(256), 0, stream, a);
+  const int cols = kPlanWaves / a.col_waves;   // a block's
+  const int blocks = (L.ncols + cols - 1) / cols;
+  hipLaunchKernelGGL(plan_count_kernel, dim3(blocks), dim3(kScanThreads), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   if (blocks > 1) {
-    hipLaunchKernelGGL(plan_place_kernel, dim3(blocks), dim3(256), 0, stream, a);
+    // blocks past the columns' only fill; 4 rows a thread (8192 pairs on 1024 experts: 18 us by two blocks)
+    const int filling = std::min(256, (p.rows_cap + 4 * kScanThreads - 1) / (4 * kScanThreads));
+    hipLaunchKernelGGL(plan_place_kernel, dim3(std::max(blocks, filling)), dim3(kScanThreads), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   }
   return MOE_OK;
