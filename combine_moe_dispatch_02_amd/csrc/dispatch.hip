@@ -260,12 +260,18 @@ int launch_dispatch(const void* x, int32_t H, int32_t dtype, const moe_plan_t& p
 // ---------------------------------------------------------------------------------------
 // rows that are codes with scale words already
 // ---------------------------------------------------------------------------------------
-// Both formats move H bytes and a 4-byte word for 128 columns a row, so one kernel serves them.
-// The codes go as above: a wave reads a token's row once and stores it to each of its pool rows.
-// The words do not: stored beside the rows, a word of each 128 columns lands alone in its line of the
-// tile-major array (20 of 92 us at 8192 x 4096, top-8). The first `scale_blocks` workgroups fill
-// them tile by tile instead, consecutive words at a time; a piece of a tile's words counts as one more row.
-// (Filling the codes tile by tile too reads every row K times: 122 us there.)
+// Both formats move H bytes and a 4-byte word for 128 columns a row, so the same kernels serve them. The
+// first `scale_blocks` workgroups fill the scale words tile by tile, consecutive words at a time (stored
+// beside the rows, a word of each 128 columns lands alone in its line of the tile-major array: 20 of 92
+// us at 8192 x 4096, top-8). The others have the codes, by token or by tile:
+//   by token, as above: a wave reads a row once and stores it to each of its pool rows. Few steps
+//     one after another, so the faster one for small batches; but the pool's rows are then written
+//     all over it (8192 x 4096, top-8: 79 us, 3.9 TB/s).
+//   by tile: a workgroup has every so many tiles, so the pool is written nearly in order, and one of up
+//     to 8 slices of the columns. Workgroups go to the 8 XCDs in turn, so an XCD reads one slice of x
+//     alone (4 MB at 8192 x 4096, its L2's size) and a row's K readings come from there; the pool's
+//     stores pass the caches by to keep it so (67 us, 4.6 TB/s; with ordinary stores a fifth more, with
+//     whole rows, each read from memory K times, 122; 4 slices 86, two tiles' loads at once 70).
 struct DispatchQArgs {
   DispatchArgs d;               // x: the codes
   const uint32_t* x_s;          // [T][ceil(H / 128)]
@@ -273,25 +279,100 @@ struct DispatchQArgs {
   const int32_t* num_tiles;
   int32_t max_tiles;            // that pool and plan have room for
   int32_t scale_blocks;
+  int32_t slices;               // by tile: of the columns
+  int32_t slice_blocks;         // and workgroups of a slice
 };
-// Few, large workgroups, since each pays an L2 write-back to publish: 16 waves of up to 8 tokens and
-// 16 workgroups for the scales. 8192 x 4096, top-8: 89 us, of which the write-backs are 9 and the rows' writes
-// (278 MB in 4 KB pieces) nearly all the rest; 4 waves a workgroup 125, 256 workgroups of 16 waves 100,
-// 8 or 32 for the scales 112 or 91.
+// Few, large workgroups, since each pays an L2 write-back to publish: 16 waves (4 at 8192 x 4096 by token:
+// 125 us, 16: 89 on that machine); 16 workgroups for the scales (8: 112 us; more: no gain), and by tile
+// as many in all as there are CUs.
 constexpr int kQWaves = 16;
-constexpr int kQTokens = 8;
 constexpr int kQScaleBlocks = 16;
 constexpr int kQWords = 8;   // scale words of a row in an item
+constexpr int kQSlices = 8;
+constexpr int kQTileTokens = 4096;
+constexpr int kQSliceChunks = 16;   // 256 bytes, at least
 
-// one more of tile ti is in; `more` rows count beside its real ones
-__device__ inline void count_tile(const DispatchArgs& a, int ti, int more) {
-  const uint32_t old = __hip_atomic_fetch_add(&a.tile_fill[ti], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// a tile's real rows
+__device__ inline int tile_rows(const DispatchArgs& a, int ti) {
   const int e = a.tile_expert[ti];
-  const int real = min(a.tile, a.offsets[e] + a.counts[e] - (ti << a.tile_shift));
-  if ((int)old + 1 == real + more) {
+  return min(a.tile, a.offsets[e] + a.counts[e] - (ti << a.tile_shift));
+}
+// one more of the `all` parts of tile ti is in
+__device__ inline void count_tile(const DispatchArgs& a, int ti, int all) {
+  const uint32_t old = __hip_atomic_fetch_add(&a.tile_fill[ti], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if ((int)old + 1 == all) {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     __hip_atomic_store(&a.tile_ready[ti], a.epoch, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_fetch_add(a.tiles_done, 1u, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+// the token of pool row `row`, -1: none
+__device__ inline int row_token(const DispatchQArgs& b, int64_t row) {
+  const int q = b.src[row];
+  return q < 0 || q >= (int64_t)b.d.T * b.d.K ? -1 : (int)((uint32_t)q / (uint32_t)b.d.K);
+}
+
+// The scale words, by the first workgroups. An item is eight of a tile's words a row: read along the
+// rows, written along the tile. Each counts as one part of its tile, beside what `parts(tile)` says.
+template <typename PARTS>
+__device__ inline void dispatch_scales(const DispatchQArgs& b, int tiles, PARTS parts) {
+  const DispatchArgs& a = b.d;
+  const int lane = lane_id();
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int words = (a.H + 127) >> 7;
+  const int per_tile = (words + kQWords - 1) / kQWords;
+  __shared__ uint32_t s_word[kQWaves][128][kQWords + 1];
+  __shared__ int s_token[kQWaves][128];
+  const int items = tiles * per_tile;
+  const int first = (int)blockIdx.x * kQWaves, step = b.scale_blocks * kQWaves;
+  for (int it = first + w; it < items; it += step) {
+    const int ti = it / per_tile;
+    const int g0 = (it - ti * per_tile) * kQWords;
+    const int64_t row0 = (int64_t)ti << a.tile_shift;
+    for (int r = lane; r < a.tile; r += kWave) s_token[w][r] = row_token(b, row0 + r);
+    wave_sync();
+    // two lanes a row, four words each
+    const int g = g0 + 4 * (lane & 1);
+    u32x4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = (lane >> 1) + 32 * j;
+      const int t = r < a.tile ? s_token[w][r] : -1;
+      v[j] = u32x4{0u, 0u, 0u, 0u};
+      if (t >= 0) {
+        const uint32_t* from = b.x_s + (int64_t)t * words;
+        if (g + 4 <= words) {
+          __builtin_memcpy(&v[j], from + g, 16);
+        } else {
+          for (int k = 0; k < 4; ++k)
+            if (g + k < words) v[j][k] = from[g + k];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = (lane >> 1) + 32 * j;
+      if (r < a.tile)
+        for (int k = 0; k < 4; ++k) s_word[w][r][4 * (lane & 1) + k] = v[j][k];
+    }
+    wave_sync();
+    uint32_t* to = static_cast<uint32_t*>(a.pool_s) + row0 * words;
+    for (int r = lane; r < a.tile; r += kWave) {
+      if (s_token[w][r] < 0) continue;   // padding rows' words are left alone
+#pragma unroll
+      for (int k = 0; k < kQWords; ++k)
+        if (g0 + k < words) to[((int64_t)(g0 + k) << a.tile_shift) + r] = s_word[w][r][k];
+    }
+    wave_sync();
+  }
+  __syncthreads();
+  if (w != 0) return;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+  // this workgroup's items: kQWaves at `first`, then every `step`
+  for (int n = lane;; n += 64) {
+    const int it = first + n / kQWaves * step + n % kQWaves;
+    if (first + n / kQWaves * step >= items) break;
+    if (it < items) count_tile(a, it / per_tile, per_tile + parts(it / per_tile));
   }
 }
 
@@ -300,86 +381,24 @@ __global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(Dispat
   const DispatchArgs& a = b.d;
   const int lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int words = (a.H + 127) >> 7;
-
-  // an item is eight of a tile's words a row: read along the rows, written along the tile
-  const int per_tile = (words + kQWords - 1) / kQWords;
+  const int per_tile = (((a.H + 127) >> 7) + kQWords - 1) / kQWords;
   if ((int)blockIdx.x < b.scale_blocks) {
-    __shared__ uint32_t s_word[kQWaves][128][kQWords + 1];
-    __shared__ int s_token[kQWaves][128];
-    const int items = min(b.num_tiles[0], b.max_tiles) * per_tile;
-    const int first = (int)blockIdx.x * kQWaves, step = b.scale_blocks * kQWaves;
-    for (int it = first + w; it < items; it += step) {
-      const int ti = it / per_tile;
-      const int g0 = (it - ti * per_tile) * kQWords;
-      const int64_t row0 = (int64_t)ti << a.tile_shift;
-      for (int r = lane; r < a.tile; r += kWave) {
-        const int q = b.src[row0 + r];
-        s_token[w][r] = q < 0 || q >= a.T * a.K ? -1 : (int)((uint32_t)q / (uint32_t)a.K);
-      }
-      wave_sync();
-      // two lanes a row, four words each
-      const int g = g0 + 4 * (lane & 1);
-      u32x4 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = (lane >> 1) + 32 * j;
-        const int t = r < a.tile ? s_token[w][r] : -1;
-        v[j] = u32x4{0u, 0u, 0u, 0u};
-        if (t >= 0) {
-          const uint32_t* from = b.x_s + (int64_t)t * words;
-          if (g + 4 <= words) {
-            __builtin_memcpy(&v[j], from + g, 16);
-          } else {
-            for (int k = 0; k < 4; ++k)
-              if (g + k < words) v[j][k] = from[g + k];
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = (lane >> 1) + 32 * j;
-        if (r < a.tile)
-          for (int k = 0; k < 4; ++k) s_word[w][r][4 * (lane & 1) + k] = v[j][k];
-      }
-      wave_sync();
-      uint32_t* to = static_cast<uint32_t*>(a.pool_s) + row0 * words;
-      for (int r = lane; r < a.tile; r += kWave) {
-        if (s_token[w][r] < 0) continue;   // padding rows' words are left alone
-#pragma unroll
-        for (int k = 0; k < kQWords; ++k)
-          if (g0 + k < words) to[((int64_t)(g0 + k) << a.tile_shift) + r] = s_word[w][r][k];
-      }
-      wave_sync();
-    }
-    __syncthreads();
-    if (w != 0) return;
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    // this workgroup's items: kQWaves at `first`, then every `step`
-    for (int n = lane;; n += 64) {
-      const int it = first + n / kQWaves * step + n % kQWaves;
-      if (first + n / kQWaves * step >= items) break;
-      if (it < items) count_tile(a, it / per_tile, per_tile);
-    }
+    dispatch_scales(b, min(b.num_tiles[0], b.max_tiles), [&](int ti) { return tile_rows(a, ti); });
     return;
   }
 
-  const int tpw = a.tokens_per_wave;
-  const int tb = ((int)blockIdx.x - b.scale_blocks) * kQWaves * tpw;   // the block's first token
-  const int t0 = tb + w * tpw;
-  const int ntok = t0 < a.T ? min(tpw, a.T - t0) : 0;
+  const int tb = ((int)blockIdx.x - b.scale_blocks) * kQWaves;   // the block's first token
+  const int t = tb + w;
   const int nch = a.H >> 4;   // 16-byte chunks of 16 codes
-  for (int i = 0; i < ntok; ++i) {
-    const int t = t0 + i;
+  if (t < a.T) {
     int p = lane < a.K ? a.pos[(int64_t)t * a.K + lane] : -1;
     if (p >= a.pool_rows) {
       record_error(a.err, MOE_ERR_INVALID);
       p = -1;
     }
     const uint64_t dest = ballot(p >= 0);
-    if (dest == 0) continue;
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(reinterpret_cast<const uint8_t*>(a.x) + (int64_t)t * a.H, (uint32_t)a.H);
-    for (int c0 = 0; c0 < nch; c0 += kWave * CPL) {
+    for (int c0 = 0; dest != 0 && c0 < nch; c0 += kWave * CPL) {
       u32x4 v[CPL];
 #pragma unroll
       for (int j = 0; j < CPL; ++j) v[j] = buf_load16_nt(xr, (uint32_t)(c0 + j * kWave + lane) * 16u);
@@ -395,11 +414,65 @@ __global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_kernel(Dispat
   __syncthreads();
   if (w != 0) return;
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-  const int npairs = (min(a.T, tb + kQWaves * tpw) - tb) * a.K;
+  const int npairs = (min(a.T, tb + kQWaves) - tb) * a.K;
   for (int q = lane; q < npairs; q += 64) {
     const int p = a.pos[(int64_t)tb * a.K + q];
-    if (p >= 0 && p < a.pool_rows) count_tile(a, p >> a.tile_shift, per_tile);
+    if (p >= 0 && p < a.pool_rows) count_tile(a, p >> a.tile_shift, per_tile + tile_rows(a, p >> a.tile_shift));
   }
+}
+
+__global__ __launch_bounds__(64 * kQWaves) void dispatch_quantized_tiles_kernel(DispatchQArgs b) {
+  const DispatchArgs& a = b.d;
+  const int lane = lane_id();
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int all = b.num_tiles[0], tiles = min(all, b.max_tiles);
+  if ((int)blockIdx.x < b.scale_blocks) {
+    dispatch_scales(b, tiles, [&](int) { return b.slices; });
+    return;
+  }
+  if (all > tiles && threadIdx.x == 0) record_error(a.err, MOE_ERR_INVALID);
+  const int n = (int)blockIdx.x - b.scale_blocks;
+  const int slice = n % b.slices, wg = n / b.slices;
+  const int nch = a.H >> 4;   // 16-byte chunks of 16 codes
+  const int first = nch * slice / b.slices, cn = nch * (slice + 1) / b.slices - first;
+  constexpr int kRows = 128 / kQWaves;                 // a wave's rows of a tile, at most
+  const int rows = a.tile / kQWaves;                   // 1 .. kRows
+  const int rpi = cn >= kWave ? 1 : kWave / cn;        // rows of an instruction, if a slice's row fits
+  const int ro = cn >= kWave ? 0 : lane / cn, co = cn >= kWave ? lane : lane - ro * cn;
+  // lane r: the token of the wave's row r
+  const auto tokens = [&](int ti) {
+    return ti < tiles ? row_token(b, ((int64_t)ti << a.tile_shift) + w * rows + min(lane, rows - 1)) : -1;
+  };
+  int next = tokens(wg);
+  for (int ti = wg; ti < tiles; ti += b.slice_blocks) {
+    const int tok = next;
+    next = tokens(ti + b.slice_blocks);
+    const int64_t row0 = ((int64_t)ti << a.tile_shift) + w * rows;
+    for (int c0 = 0; c0 < cn; c0 += kWave) {
+      const int c = c0 + co;
+      const int64_t col = (int64_t)(first + min(c, cn - 1)) * 16;
+      u32x4 v[kRows];
+      int t[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (i * rpi >= rows) break;
+        const int r = i * rpi + ro;
+        t[i] = __shfl(tok, min(r, rows - 1), 64);
+        if (c >= cn || ro >= rpi || r >= rows) t[i] = -1;
+        // rows without a token read token 0's: all loads are in flight together
+        v[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(a.x) + (int64_t)max(t[i], 0) * a.H + col);
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (i * rpi < rows && t[i] >= 0)
+          __builtin_nontemporal_store(v[i], reinterpret_cast<u32x4*>(a.pool + (row0 + i * rpi + ro) * a.H + col));
+    }
+  }
+  __syncthreads();
+  if (w != 0) return;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+  const int per_tile = (((a.H + 127) >> 7) + kQWords - 1) / kQWords;
+  for (int ti = wg + lane * b.slice_blocks; ti < tiles; ti += kWave * b.slice_blocks) count_tile(a, ti, per_tile + b.slices);
 }
 
 int launch_dispatch_quantized(const void* q, const void* q_s, int32_t H, const moe_plan_t& p, int32_t pool_rows,
@@ -430,11 +503,21 @@ int launch_dispatch_quantized(const void* q, const void* q_s, int32_t H, const m
   b.num_tiles = p.num_tiles;
   b.max_tiles = std::min(pool_rows, p.rows_cap) / p.tile;
   const int cus = std::max(1, device_cu_count());
-  a.tokens_per_wave = std::max(1, std::min(kQTokens, p.T / (8 * cus)));
   b.scale_blocks = std::min(p.rows_cap / p.tile, kQScaleBlocks);
-  const int per = kQWaves * a.tokens_per_wave;
-  const dim3 grid((unsigned)(b.scale_blocks + (p.T + per - 1) / per)), block(64 * kQWaves);
   const int nch = H / 16;
+  const dim3 block(64 * kQWaves);
+  // By tile from 4096 tokens on, and from 2048 pairs on where the experts are few, whose tiles' counters the
+  // tokens of all workgroups share. By token / by tile, us: H 4096, 128 experts, top-8 27.6 / 30.2 (2048 tokens), 47 / 39
+  // (4096), 79 / 67 (8192); 32 of 256 experts at H 7168 16.1 / 16.6 (2560), 25 / 24 (4096), 81 / 51 (16384); 8
+  // experts, top-8 20.9 / 17.6 (512), 55 / 28 (2048)
+  if (p.T >= kQTileTokens || (p.E_local <= 16 && (int64_t)p.T * p.K > 2048)) {
+    b.slices = kQSlices;
+    while (b.slices > 1 && nch / b.slices < kQSliceChunks) b.slices /= 2;
+    b.slice_blocks = std::max(1, (cus - b.scale_blocks) / b.slices);
+    hipLaunchKernelGGL(dispatch_quantized_tiles_kernel, dim3(b.scale_blocks + b.slices * b.slice_blocks), block, 0, stream, b);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  }
+  const dim3 grid((unsigned)(b.scale_blocks + (p.T + kQWaves - 1) / kQWaves));   // a token a wave
   if (nch <= 64) hipLaunchKernelGGL((dispatch_quantized_kernel<1>), grid, block, 0, stream, b);
   else if (nch <= 128) hipLaunchKernelGGL((dispatch_quantized_kernel<2>), grid, block, 0, stream, b);
   else hipLaunchKernelGGL((dispatch_quantized_kernel<4>), grid, block, 0, stream, b);
