@@ -304,8 +304,9 @@ struct TokenPairs {
 // 96 us). So h comes in whole lines, several K blocks a load, and goes to the lanes that want it
 // by way of LDS, and the scales of four K blocks come as words (80 us with the latter alone).
 // ---------------------------------------------------------------------------------------
+// 4 waves a SIMD: two workgroups of 8 waves a CU, or one of 16 (13 tokens at H 7168: 18 us; 22 with 3)
 template <int NW, int TOK>
-__global__ __launch_bounds__(64 * NW) void decode_out_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(64 * NW, 4) void decode_out_kernel(DecodeArgs a) {
   constexpr int U = 4;                                // K blocks at a time
   constexpr int COLS = 8;
   __shared__ Reached reached;
