@@ -17,7 +17,7 @@
 // the waves in order, so out needs no second pass and no atomics.
 //
 // H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 12 + 8 us (80 MB),
-// 64 tokens 123 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 125 and 385 us.
+// 64 tokens 123 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 120 and 380 us.
 #include "common.h"
 #include "kernels.h"
 
