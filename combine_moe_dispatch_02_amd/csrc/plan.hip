@@ -132,11 +132,11 @@ __device__ void plan_fill(const PlanArgs& a, const int* counts, const int* offse
     for (int t = (seg >> a.tile_shift) + lane; t < (seg_end >> a.tile_shift); t += kWave) a.tile_expert[t] = e;
   }
   const int P = offsets[a.E];
-  const int first = wave * kWave + lane, step = waves * kWave;
-  for (int t = (P >> a.tile_shift) + first; t < a.ntiles_cap; t += step) a.tile_expert[t] = -1;
-  for (int r = P + first; r < a.rows_cap; r += step) a.src[r] = -1;
-  for (int t = first; t < a.ntiles_cap; t += step) a.tile_ready[t] = 0u;
-  for (int t = first; t < a.nfill; t += step) a.tile_fill[t] = 0u;
+  const int64_t first = wave * kWave + lane, step = waves * kWave;   // rows_cap + step may pass 2^31
+  for (int64_t t = (P >> a.tile_shift) + first; t < a.ntiles_cap; t += step) a.tile_expert[t] = -1;
+  for (int64_t r = P + first; r < a.rows_cap; r += step) a.src[r] = -1;
+  for (int64_t t = first; t < a.ntiles_cap; t += step) a.tile_ready[t] = 0u;
+  for (int64_t t = first; t < a.nfill; t += step) a.tile_fill[t] = 0u;
   if (first == 0) *a.tiles_done = 0u;
 }
 
@@ -331,7 +331,7 @@ int launch_plan(const int32_t* topk_idx, const moe_plan_t& p, const WsLayout& L,
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   if (blocks > 1) {
     // blocks past the columns' only fill; 4 rows a thread (8192 pairs on 1024 experts: 18 us by two blocks)
-    const int filling = std::min(256, (p.rows_cap + 4 * kScanThreads - 1) / (4 * kScanThreads));
+    const int filling = std::min(256, p.rows_cap / (4 * kScanThreads) + 1);
     hipLaunchKernelGGL(plan_place_kernel, dim3(std::max(blocks, filling)), dim3(kScanThreads), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   }
