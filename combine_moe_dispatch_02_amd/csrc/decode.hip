@@ -5,10 +5,10 @@
 //   out[t] = sum_k topk_weights[t,k] * (W2[e] . h[t,k]).
 //
 // Every reached expert's 3 * H * I * (1/2 + 1/32) bytes are read once and hardly anything
-// else moves: the memory's rate bounds it. The products run on the matrix cores all the same
-// (v_mfma_scale_f32_16x16x128_f8f6f4, 16 weight rows by 16 token columns): a 16 x 128 weight
-// tile of the layer's load-time layout is one 16-byte load a lane, taken as it is, scales
-// included, so no value is unpacked, and up to 16 tokens cost what one does.
+// else moves: the memory's rate bounds it. The products run on the matrix cores all the same, 16
+// weight rows by 16 token columns (for h in bf16, for out as v_mfma_scale_f32_16x16x128_f8f6f4): a
+// 16 x 128 weight tile of the layer's load-time layout is one 16-byte load a lane, and up to 16
+// tokens cost what one does.
 //
 // The pooled path's plan, dispatch and combine launches are not needed: with at most 64 * 16
 // pairs each workgroup finds the reached experts itself (a bitmap in LDS), the h kernel's
@@ -16,8 +16,8 @@
 // workgroup sums all experts' shares of its 16 columns in LDS, each wave for itself and then
 // the waves in order, so out needs no second pass and no atomics.
 //
-// H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 12 + 8 us (80 MB),
-// 64 tokens 123 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 120 and 380 us.
+// H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 13 + 8 us (80 MB),
+// 64 tokens 124 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 120 and 380 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -57,13 +57,47 @@ constexpr uint32_t kNowhere = 0x7fffff00u;   // past every buffer: reads 0
 // K = 64 + 16 lhi (b1), and the E8M0 scales of both sides' block K = 32 lhi .. + 32 (sa, sb).
 // The sum is fp32 from one instruction to the next, but inside one the matrix core lines its 128
 // products up on the largest and drops what is too small beside it: random codes come out up to
-// 2e-4 of the sum of their magnitudes off, normal values 1e-5. That is far below h's e4m3 (2^-4) and out's
-// bf16 (2^-9): 4 of 10000 codes of h go to the other neighbour. It is what the layer's pooled mxfp4 mode
-// computes with, too; products in bf16 would be exact and take 32 conversions a tile.
+// 2e-4 of the sum of their magnitudes off, normal values 1e-5. That is far below out's bf16 (2^-9), so
+// out is summed so.
 __device__ inline f32x4 mfma_mx(u32x4 a, uint32_t sa, u32x4 b0, u32x4 b1, uint32_t sb, f32x4 acc) {
   const i32x8 av = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
   const i32x8 bv = {(int)b0.x, (int)b0.y, (int)b0.z, (int)b0.w, (int)b1.x, (int)b1.y, (int)b1.z, (int)b1.w};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 4, 0, 0, (int)sa, 0, (int)sb);
+}
+
+// h's sums decide between neighbouring e4m3 codes, and with the above 4 in 10000 went to the wrong one, each
+// a sixteenth off or more. So they are formed in bf16, which holds both sides' values with their
+// scales exactly: four instructions of 32 K, the j-th of every lane's codes 8 j .. + 8 (of whatever K,
+// the same on both sides), fp32 throughout, and no code of 500000 differs from float64's. It costs 20
+// conversions a tile (one token 12.8 -> 13.3 us, 13 tokens at H 7168 26.8 -> 29.4, 64 tokens 122.5 -> 123.2).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+struct Bf16Block {
+  bf16x8 v[4];
+};
+__device__ inline float e8m0_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+__device__ inline bf16x8 join(bf16x2 a, bf16x2 b, bf16x2 c, bf16x2 d) {
+  return __builtin_shufflevector(__builtin_shufflevector(a, b, 0, 1, 2, 3), __builtin_shufflevector(c, d, 0, 1, 2, 3), 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ inline Bf16Block from_e2m1(u32x4 codes, float s) {
+  Bf16Block r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t c = codes[j];
+    r.v[j] = join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1),
+                  __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+  }
+  return r;
+}
+__device__ inline Bf16Block from_e4m3(u32x4 lo, u32x4 hi, float s) {
+  Bf16Block r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t c = j < 2 ? lo[2 * j] : hi[2 * j - 4], d = j < 2 ? lo[2 * j + 1] : hi[2 * j - 3];
+    r.v[j] = join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true),
+                  __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, s, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, s, true));
+  }
+  return r;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -149,7 +183,7 @@ __global__ __launch_bounds__(256) void decode_quantise_kernel(const uint16_t* x,
 // them 16 C at a time and reads its weights again (from the caches) for every 16 C.
 // ---------------------------------------------------------------------------------------
 template <int NW, int U, int C>
-__global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(64 * NW, C == 2 ? 3 : 1) void decode_h_kernel(DecodeArgs a) {
   __shared__ Reached reached;
   __shared__ int16_t s_q[kDecodeTokens];              // the expert's pairs, one of each of its tokens
   __shared__ f32x4 s_red[NW][4][64];
@@ -195,7 +229,7 @@ __global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
       const int c = c0 + g * 16 + l16;
       on[g] = c < n;
       const uint32_t t = on[g] ? (uint32_t)s_q[c] / (uint32_t)a.K : 0u;
-      xo[g] = t * (uint32_t)a.H + (uint32_t)lhi * 16u;
+      xo[g] = t * (uint32_t)a.H + (uint32_t)lhi * 32u;
       xso[g] = t * (uint32_t)KB * 4u + (uint32_t)lhi;
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[g][i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -216,16 +250,26 @@ __global__ __launch_bounds__(64 * NW) void decode_h_kernel(DecodeArgs a) {
         for (int g = 0; g < N; ++g) {
           const bool in = kb < (uint32_t)KB && on[g];
           b0[u][g] = buf_load16(xr, in ? xo[g] + kb * 128u : kNowhere);
-          b1[u][g] = buf_load16(xr, in ? xo[g] + kb * 128u + 64u : kNowhere);
+          b1[u][g] = buf_load16(xr, in ? xo[g] + kb * 128u + 16u : kNowhere);
           sb[u][g] = buf_load1(xsr, in ? xso[g] + kb * 4u : kNowhere);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
+      {
+        Bf16Block b[N];
 #pragma unroll
-        for (int g = 0; g < N; ++g)
+        for (int g = 0; g < N; ++g) b[g] = from_e4m3(b0[u][g], b1[u][g], e8m0_scale(sb[u][g]));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[g][i] = mfma_mx(wt[u][i], wsc[u][i], b0[u][g], b1[u][g], sb[u][g], acc[g][i]);
+        for (int i = 0; i < 4; ++i) {
+          const Bf16Block w = from_e2m1(wt[u][i], e8m0_scale(wsc[u][i]));
+#pragma unroll
+          for (int g = 0; g < N; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[g][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[j], b[g].v[j], acc[g][i], 0, 0, 0);
+        }
+      }
     }
 
     // the waves' sums, then SwiGLU and the MXFP8 of 32 columns: lane (l16, lhi) has token column

@@ -123,6 +123,36 @@ def test_an_expert_of_n_tokens(n, E):
     assert close(c.run(), c.ref())
 
 
+@pytest.mark.parametrize("T,H,I,E", [(64, 512, 128, 8), (10, 1792, 128, 30), (64, 4096, 128, 16), (5, 7168, 256, 4)])
+def test_no_code_of_h_is_off(T, H, I, E):
+    """One expert a token with weight 1: a token's row is W2 h of one h, and a code of h beside its own puts 1/16 or
+    more of that h into it, 1e-2 of the row's norm at I = 128 for one of average size. Row by row: bf16's half step 2^-8
+    of each value, and 2e-4 of the sums of I magnitudes, sqrt(I) times the result: 2e-4 * 16."""
+    say("decode codes of h", T, H, I)
+    c = Case(T, H, I, E, 1, seed=12)
+    c.weights[:] = 1.0
+    got, ref = oracle.bf16_to_f64(c.run().cpu()), c.ref()
+    off = np.linalg.norm(got - ref, axis=1) / np.linalg.norm(ref, axis=1)
+    assert off.max() <= 2.0 ** -8 + 2e-4 * 16
+
+
+def test_scales_of_all_sizes_and_nan():
+    """Weight and activation scales over many powers of two (no product past fp32's range), zero blocks, and a NaN scale."""
+    say("decode scales")
+    c = Case(6, 256, 128, 4, 2, seed=13)
+    g = torch.Generator().manual_seed(1)
+    c.w1_s = torch.randint(90, 150, c.w1_s.shape, generator=g, dtype=torch.uint8)
+    c.x = (torch.randn(6, 256, generator=g) * torch.exp2(torch.randint(-40, 5, (6, 8), generator=g).float()).repeat_interleave(32, 1)).bfloat16()
+    c.x[0, 32:64] = 0
+    c.w1_s[0, :, 0] = 0
+    assert close(c.run(), c.ref())
+    codes, scales = c.quantised()
+    scales = scales.copy()
+    scales[3, 1] = 255
+    got = c.run((codes, scales)).float().cpu()
+    assert bool(got[3].isnan().all()) and bool(got[[0, 1, 2, 4, 5]].isfinite().all())
+
+
 def test_1024_experts():
     say("decode 1024 experts")
     c = Case(64, 128, 128, 1024, 16, seed=7)
