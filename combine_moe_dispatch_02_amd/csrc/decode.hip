@@ -17,7 +17,7 @@
 // the waves in order, so out needs no second pass and no atomics.
 //
 // H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 13 + 8 us (80 MB),
-// 64 tokens 124 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 120 and 380 us.
+// 64 tokens 124 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 120 and 375 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -520,13 +520,13 @@ int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t 
     a.x_s = q_s;
   }
   const int cus = std::max(1, device_cu_count());
-  // 8 waves a workgroup for few pairs, whose workgroups leave the CUs room, 4 for more. 8 against 4, of 128
-  // experts at H 4096: 11.6 / 13.2 us (8 pairs), 33.5 / 34.8 (32), 58.6 / 52.9 (64); two of them on one
-  // of 8 ranks at H 7168: 12.5 / 15.4
-  if (T * K <= 32) hipLaunchKernelGGL((decode_h_kernel<8, 2, 1>), gh, dim3(512), 0, stream, a);
+  // 8 waves a workgroup for up to 8 pairs, 4 for more: from 16 on there may be three workgroups a CU, and
+  // registers admit two of 8 waves. 8 against 4, of 128 experts at H 4096: 13.3 / 13.8 us (8 pairs), 23.6 / 18.9
+  // (16), 37.1 / 33.1 (32); 6 of them on one of 8 ranks at H 7168 14.2 / 15.1
+  if (T * K <= 8) hipLaunchKernelGGL((decode_h_kernel<8, 2, 1>), gh, dim3(512), 0, stream, a);
   // 32 tokens for one read of the weights where the experts have more than 8 pairs on average and so
-  // some of them more than 16 tokens; it leaves room for 3 waves a SIMD instead of 5. 32 against 16: 49 / 68 us (8 experts with
-  // 64 tokens each, H 5120), 24 / 31 (16 with up to 24, H 4096), 59 / 53 (64 with 8), 148 / 130 (127 with 4)
+  // some of them more than 16 tokens; it leaves room for 3 waves a SIMD instead of 4. 32 against 16: 52 / 70 us (8 experts
+  // with 64 tokens each, H 5120), 25 / 34 (16 with up to 24, H 4096), 49 / 49 (64 with 8), 145 / 139 (127 with 4)
   else if (T > 16 && T * K > 8 * E) hipLaunchKernelGGL((decode_h_kernel<4, 2, 2>), gh, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((decode_h_kernel<4, 2, 1>), gh, dim3(256), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
