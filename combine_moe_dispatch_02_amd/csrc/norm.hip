@@ -271,13 +271,17 @@ struct NormBwdArgs {
   float* part;   // [gridDim.x][H] partial sums of dweight, or null
 };
 
-// One row at a time by the W waves of a workgroup; dweight's sums of the lane's columns stay
-// in its registers over all of the workgroup's rows.
+// One row at a time by the W waves of a workgroup (W = 1: four, by a wave each); dweight's sums of the
+// lane's columns stay in its registers over all of the workgroup's rows, and four waves' are
+// added before they are written (4333 x 472: 8.2 us and 11.3 for dweight with a partial row a wave, 4.5 and 4.8 so).
 template <int W, int CPL>
-__global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a) {
+__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_backward_kernel(NormBwdArgs a) {
+  constexpr int ROWS = W == 1 ? 4 : 1;
   __shared__ float red[2 * W];
+  __shared__ float s_dw[W == 1 ? 3 : 1][W == 1 ? 64 * 8 : 1];
   const int lane = lane_id();
-  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = W == 1 ? 0 : wave;
   const int H = a.H;
   const int c0 = sub * (kWave * CPL) + lane;
   const uint32_t row_bytes = (uint32_t)H * 2u;
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   }
   int odd = 0;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
     const __amdgpu_buffer_rsrc_t dr = make_rsrc(a.dy + t * H, row_bytes);
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.s + t * H, row_bytes);
     const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.d_res ? a.d_res + t * H : nullptr, a.d_res ? row_bytes : 0u);
@@ -339,6 +343,17 @@ __global__ __launch_bounds__(64 * W) void rmsnorm_backward_kernel(NormBwdArgs a)
     }
   }
   if (a.part) {
+    if constexpr (W == 1) {                            // CPL is 1
+      if (wave > 0)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_dw[wave - 1][j * 64 + lane] = dw[0][j];
+      __syncthreads();
+      if (wave > 0) return;
+#pragma unroll
+      for (int v = 0; v < 3; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[0][j] += s_dw[v][j * 64 + lane];
+    }
     const __amdgpu_buffer_rsrc_t pr = make_rsrc(a.part + (int64_t)blockIdx.x * H, (uint32_t)H * 4u);
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
@@ -430,7 +445,10 @@ static int backward_waves(int32_t H) {
   const int nch = H / 8;
   return nch <= 64 ? 1 : nch <= 256 ? 4 : nch <= 1024 ? 8 : 16;
 }
-int32_t rmsnorm_backward_blocks(int32_t T, int32_t H) { return std::min(T, 4096 / backward_waves(H)); }
+int32_t rmsnorm_backward_blocks(int32_t T, int32_t H) {
+  const int waves = backward_waves(H);
+  return waves == 1 ? std::min(T / 4 + (T % 4 != 0), 1024) : std::min(T, 4096 / waves);
+}
 
 int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, bool w_f32, const float* rstd,
                             const void* d_res, int32_t T, int32_t H, void* dx, float* dweight, void* ws,
@@ -450,7 +468,7 @@ int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, b
   if (n > 0) {
     const int nch = H / 8;
     const dim3 grid(n);
-    if (nch <= 64) hipLaunchKernelGGL((rmsnorm_backward_kernel<1, 1>), grid, dim3(64), 0, stream, a);
+    if (nch <= 64) hipLaunchKernelGGL((rmsnorm_backward_kernel<1, 1>), grid, dim3(256), 0, stream, a);
     else if (nch <= 256) hipLaunchKernelGGL((rmsnorm_backward_kernel<4, 1>), grid, dim3(256), 0, stream, a);
     else if (nch <= 512) hipLaunchKernelGGL((rmsnorm_backward_kernel<8, 1>), grid, dim3(512), 0, stream, a);
     else if (nch <= 1024) hipLaunchKernelGGL((rmsnorm_backward_kernel<8, 2>), grid, dim3(512), 0, stream, a);
