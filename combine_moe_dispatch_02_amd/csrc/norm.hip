@@ -297,7 +297,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rmsnorm_backward_kernel
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   }
   int odd = 0;
-  for (int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
+  for (int64_t t = blockIdx.x + (W == 1 ? (int64_t)wave * gridDim.x : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
     const __amdgpu_buffer_rsrc_t dr = make_rsrc(a.dy + t * H, row_bytes);
     const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.s + t * H, row_bytes);
     const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.d_res ? a.d_res + t * H : nullptr, a.d_res ? row_bytes : 0u);
@@ -446,8 +446,7 @@ static int backward_waves(int32_t H) {
   return nch <= 64 ? 1 : nch <= 256 ? 4 : nch <= 1024 ? 8 : 16;
 }
 int32_t rmsnorm_backward_blocks(int32_t T, int32_t H) {
-  const int waves = backward_waves(H);
-  return waves == 1 ? std::min(T / 4 + (T % 4 != 0), 1024) : std::min(T, 4096 / waves);
+  return std::min(T, 4096 / std::max(4, backward_waves(H)));
 }
 
 int launch_rmsnorm_backward(const void* dy, const void* s, const void* weight, bool w_f32, const float* rstd,
