@@ -442,14 +442,15 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_backward_kernel
       w = got ? sigmoidf(z) : 0.0f;
       if (a.normalize) total = token_sum<L>(w);
     }
-    const float s = w;                           // sigmoid: the score itself
-    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-    w *= inv;
+    // every part is the weight, at most 1, times a difference of d: 1 / total may be near fp32's end (sigmoids of
+    // logits near -88), and times d past it
+    w = total > 0.0f ? w / total : 0.0f;
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // of the dense share alone, whose total is 1 at least
     const float mean = token_sum<L>(w * d);
     float part;
     if (dense) part = w * d;
     else if (a.score == MOE_SCORE_SOFTMAX) part = w * (d - mean);
-    else part = (a.normalize ? (d - mean) * inv : d) * s * sigmoidf(-z);
+    else part = w * (a.normalize ? d - mean : d) * sigmoidf(-z);
     const int n = (int)min((int64_t)TPW, a.T - t0) * a.E;   // the run
     if (dense) {
 #pragma unroll
