@@ -164,6 +164,16 @@ __device__ inline uint64_t token_lane(uint64_t v, int sub, int k) {
 }
 
 __device__ inline float sigmoidf(float v) { return 1.0f / (1.0f + expf(-v)); }
+// sigmoid(v) e^-c for c <= 0, and c = 0 for v > 0: with c = min(0, the largest of some logits) their ratios are those of the
+// sigmoids, also where these are no fp32 numbers (v below -88). What is 0 in 64 bits, 1 / (1 + e^-v) for v below
+// -709.78, is 0.
+__device__ inline float sigmoid_over(float v, float c) {
+  const float top = v > 0.0f ? 1.0f : v < -709.78266f ? 0.0f : expf(v - c);
+  return top / (1.0f + expf(-fabsf(v)));
+}
+// c of a token: chosen logits, -infinity for none
+template <int L>
+__device__ inline float sigmoid_shift(float z, int normalize) { return normalize ? fminf(token_max<L>(z), 0.0f) : 0.0f; }
 
 // ---------------------------------------------------------------------------------------
 // forward: 64 / L tokens a wave, EPL experts a lane. SCORES: keys are scores (64 bits, in LDS),
@@ -367,7 +377,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_kernel(RouterAr
       }
       total = token_sum<L>(sum);
     } else {
-      w = got ? sigmoidf(z) : 0.0f;
+      const float c = sigmoid_shift<L>(z, a.normalize);
+      w = got ? sigmoid_over(z, c) : 0.0f;
       if (a.normalize) total = token_sum<L>(w);
     }
     if (live && l < a.K) {
@@ -439,11 +450,11 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_topk_backward_kernel
       w = got ? expf(z - m) : 0.0f;
       total = token_sum<L>(w);
     } else {
-      w = got ? sigmoidf(z) : 0.0f;
+      const float c = sigmoid_shift<L>(z, a.normalize);
+      w = got ? sigmoid_over(z, c) : 0.0f;
       if (a.normalize) total = token_sum<L>(w);
     }
-    // every part is the weight, at most 1, times a difference of d: 1 / total may be near fp32's end (sigmoids of
-    // logits near -88), and times d past it
+    // every part is the weight, at most 1, times a difference of d, so none passes fp32's end before the result does
     w = total > 0.0f ? w / total : 0.0f;
     const float inv = total > 0.0f ? 1.0f / total : 0.0f;   // of the dense share alone, whose total is 1 at least
     const float mean = token_sum<L>(w * d);

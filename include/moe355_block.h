@@ -109,7 +109,9 @@ typedef struct moe_router_config {
  * token: never chosen, and (logit) no part of the softmax. The type's lowest value is an
  * ordinary logit. +infinity counts as the largest finite value. A token with fewer than K
  * experts to choose from has topk_idx -1 and weight 0 in the places left over (the layer
- * takes -1 as another rank's expert); where all chosen scores are 0 the weights are 0.
+ * takes -1 as another rank's expert). Normalised weights are right however small the scores are: a token's whose scores
+ * are too small for fp32 as any other's. A sigmoid that is 0 in 64 bits (1 / (1 + exp(-logit)), logits below -709.78) is 0,
+ * and where all chosen scores are 0 the weights, and their gradients, are 0.
  * logits: fp32 or bf16 [T][E] (logits_dtype); topk_idx: int32 [T][K]; topk_weights: fp32
  * [T][K].
  * Errors: MOE_ERR_INVALID (null or misaligned pointers, T < 0, E not in [1,1024], K not in
