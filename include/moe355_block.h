@@ -159,9 +159,8 @@ MOE355_API size_t moe_expert_ffn_decode_workspace_bytes(int32_t T, int32_t K, in
  *   h[t,k] = silu(W1[e] gate . x[t]) * (W1[e] up . x[t]), quantised to MXFP8;
  *   out[t] = bf16(sum over the local pairs of topk_weights[t,k] * (W2[e] . h[t,k]))
  * with e = topk_idx[t,k] - expert_begin; pairs with e outside [0, E_local) are other ranks'
- * and add nothing, a token without a local pair gets zeros. fp32 accumulation in an order that the arguments' shapes
- * and topk_idx fix; out's sums are the matrix core's of 128 scaled products at a time, as in the layer's mxfp4 mode
- * (within 2e-4 of the sum of magnitudes), h's are exact products in fp32.
+ * and add nothing, a token without a local pair gets zeros. Products are exact and summed in fp32, in an order
+ * that the arguments' shapes and topk_idx fix.
  * x: MXFP8 codes [T][H] with x_s (the quantised rows above; x_dtype MOE_MXFP4), or bf16
  * [T][H] with x_s null (x_dtype MOE_BF16: quantised to MXFP8 on the way, as moe_dispatch
  * does). w1, w2: codes as moe_pack_weights lays them out, w1_s, w2_s: scales as
