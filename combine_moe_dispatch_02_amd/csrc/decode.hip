@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * NW, C == 2 ? 3 : 1) void decode_h_kernel(Decod
     }
 
     // the waves' sums, then SwiGLU and the MXFP8 of 32 columns: lane (l16, lhi) has token column
-    // l16 and columns 4 lhi .. + 4 of both tiles of 16
+    // l16 and columns 4 lhi .. + 4 of both tiles of 16. expf, since __expf is off by |gate| 2^-24 (one token 23.0 -> 23.3 us)
 #pragma unroll
     for (int g = 0; g < N; ++g) {
       if (c0 + g > 0) __syncthreads();                // wave 0 has read the sums before
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(64 * NW, C == 2 ? 3 : 1) void decode_h_kernel(Decod
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float gate = s[j >> 2][j & 3], up = s[2 + (j >> 2)][j & 3];
-        h[j] = gate / (1.0f + __expf(-gate)) * up;
+        h[j] = gate / (1.0f + expf(-gate)) * up;
         m = max(m, __builtin_bit_cast(uint32_t, h[j]) & 0x7fffffffu);
       }
       m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));

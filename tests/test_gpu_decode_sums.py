@@ -120,3 +120,34 @@ def test_out_is_summed_in_fp32(T, H, I, E, K, spread):
             mag[t] += p * (np.abs(v) @ np.abs(hv[t, k]))
     err = np.abs(oracle.bf16_to_f64(out.cpu()) - ref)
     assert (err <= 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -7) + (I + K + 20) * U * mag).all()
+
+
+def test_codes_of_h_far_below_zero():
+    """silu of gates near -80: exp has to be right to its last bits there too, not off by |g| 2^-24. Each gate is a sum of four
+    products, exact in fp32; exp is off by two units, 1 + exp, the quotient and the product by half a unit each: 6 * 2^-24 in all."""
+    say("decode codes of h far below zero")
+    T, H, I = 8, 128, 16384
+    rng = np.random.default_rng(0)
+    x = np.zeros((T, H), np.uint8)
+    x[:, ::32] = oracle.e4m3_encode(np.float32(1.0))
+    x[:, 96] = oracle.e4m3_encode((1 + np.arange(T) / 8).astype(np.float32))
+    w = np.zeros((1, 2 * I, H), np.uint8)
+    w[0, :I, 0], w[0, :I, 32] = 14, 14                                  # -4 * 16 - 4 * 4
+    w[0, :I, 64], w[0, :I, 96] = rng.integers(0, 16, I), rng.integers(0, 16, I)
+    w[0, I:, 64], w[0, I:, 96] = rng.integers(4, 8, I), rng.integers(0, 16, I)
+    w1 = (w[:, :, ::2] | (w[:, :, 1::2] << 4)).astype(np.uint8)
+    w1_s = np.broadcast_to(np.array([131, 129, 126, 121], np.uint8), (1, 2 * I, 4)).copy()
+    t = torch.from_numpy
+    w2, w2_s = torch.zeros(1, H, I // 2, dtype=torch.uint8), torch.full((1, H, I // 32), 127, dtype=torch.uint8)
+    x_s = np.full((T, 4), 127, np.uint8)
+    _, codes, scales = call((t(x), t(x_s)), torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1), t(w1), t(w1_s), w2, w2_s)
+    g = dequantize_mx_e4m3(x, x_s) @ dequantize_mx_fp4(w1[0], w1_s[0]).T
+    assert (g[:, :I] < -75).all()
+    h = (g[:, :I] / (1.0 + np.exp(-g[:, :I])) * g[:, I:]).reshape(-1, 32)
+    e = np.floor(np.log2(np.abs(h).max(1))) - 8
+    sure = np.floor(np.log2(np.abs(h).max(1) * (1 - 6 * U))) == np.floor(np.log2(np.abs(h).max(1) * (1 + 6 * U)))
+    v = h * np.exp2(-e)[:, None]
+    low, high = e4m3(v * (1 - 6 * U)), e4m3(v * (1 + 6 * U))
+    got = dequantize_mx_e4m3(codes, np.full((T, I // 32), 127, np.uint8)).reshape(-1, 32)
+    assert np.array_equal(scales.reshape(-1)[sure], (e + 127).astype(np.uint8)[sure])
+    assert (((got == low) | (got == high))[sure]).all() and (low != high).mean() < 1e-4
