@@ -137,10 +137,11 @@ MOE355_API int moe_router_topk_backward(const float* d_topk_weights, const void*
 
 /*
  * moe_dispatch for rows that are quantised already: pool[pos[t,k]] = q[t] with its scale
- * words, moved to their tile-major places. Everything else (flags, epoch, workspace, pool_rows,
- * what is left alone) is as moe_dispatch with act_dtype has it, and so is the result: with q
- * from moe_rmsnorm the pool has the bits moe_dispatch makes of the bf16 rows (and in MXFP8
- * zeros in a last scale word's bytes past the row's last block, which nothing reads).
+ * words, moved to their tile-major places. Epoch, workspace, pool_rows, what is left alone and the pool's
+ * content are as moe_dispatch with act_dtype has them: with q from moe_rmsnorm the pool has the bits moe_dispatch makes of
+ * the bf16 rows (and in MXFP8 zeros in a last scale word's bytes past the row's last block, which nothing reads).
+ * A tile's flag is raised, as there, after its rows and scale words are stored, but nearly all of them at the call's end (its
+ * workgroups publish once): an FFN that waits for them on another stream begins then.
  * Errors: those of moe_dispatch; MOE_ERR_INVALID for act_dtype MOE_BF16 and misaligned q,
  * q_s or pool.
  */
