@@ -55,6 +55,12 @@ def _bytes(t: Optional[torch.Tensor], name: str, dev: int):
     return (None, 0) if t is None else (_ptr(t, name, dev, t.shape, _U8), t.numel())
 
 
+def _i32(*sizes: int) -> None:
+    """Sizes and offsets that the C ABI takes as int32; a larger one would arrive as another number."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"a size of {max(sizes)} is past 2^31 - 1")
+
+
 def _launch(name: str, dev: int, stream, *args) -> None:
     """Call entry point ``name`` on device ``dev``, the stream as its last argument."""
     if stream is None:
@@ -109,6 +115,7 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: Optional[t
         raise ValueError("x must be [T, H]")
     shape = x.shape
     T, H = shape
+    _i32(T, H)
     code = MOE_BF16 if dtype == "bf16" else _dtype_code(dtype)
     wcode = _real_dtype(weight, "weight")
     _launch("moe_rmsnorm", dev, stream,
@@ -120,6 +127,7 @@ def moe_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, y: Optional[t
 
 
 def rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
+    _i32(T, H)
     return int(load().moe_rmsnorm_backward_workspace_bytes(T, H))
 
 
@@ -134,6 +142,7 @@ def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
         raise ValueError("dy must be [T, H]")
     shape = dy.shape
     T, H = shape
+    _i32(T, H)
     wcode = _real_dtype(weight, "weight")
     ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
     _launch("moe_rmsnorm_backward", dev, stream,
@@ -177,6 +186,7 @@ def moe_router_topk(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: 
     if logits.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("logits must be [T, E], topk_idx [T, K]")
     (T, E), K = logits.shape, topk_idx.shape[1]
+    _i32(T, E, K)
     _launch("moe_router_topk", dev, stream,
             _ptr(logits, "logits", dev, logits.shape, logits.dtype), lcode, _ptr(bias, "bias", dev, (E,), _F32), T, E, K,
             cfg.c(), _ptr(topk_idx, "topk_idx", dev, (T, K), _I32), _ptr(topk_weights, "topk_weights", dev, (T, K), _F32))
@@ -191,6 +201,7 @@ def moe_router_topk_backward(d_topk_weights: torch.Tensor, logits: torch.Tensor,
     if logits.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("logits must be [T, E], topk_idx [T, K]")
     (T, E), K = logits.shape, topk_idx.shape[1]
+    _i32(T, E, K)
     _launch("moe_router_topk_backward", dev, stream,
             _ptr(d_topk_weights, "d_topk_weights", dev, (T, K), _F32),
             _ptr(logits, "logits", dev, logits.shape, logits.dtype), lcode, _ptr(topk_idx, "topk_idx", dev, (T, K), _I32),
@@ -207,6 +218,9 @@ def moe_dispatch_quantized(q: torch.Tensor, q_s: torch.Tensor, plan: Plan, pool:
     if q.dim() != 2 or pool.dim() != 2:
         raise ValueError("q must be [T, H], pool [pool rows, H]")
     H, rows = q.shape[1], pool.shape[0]
+    _i32(H, rows)
+    if epoch > 0xFFFFFFFF:
+        raise ValueError(f"epoch {epoch} is past 2^32 - 1")
     for t, n in ((plan.pos, "the plan"), (ws.buf, "ws")):
         if t.get_device() != dev:
             raise ValueError(f"{n} is on device {t.get_device()}, q on {dev}")
@@ -220,6 +234,7 @@ def moe_dispatch_quantized(q: torch.Tensor, q_s: torch.Tensor, plan: Plan, pool:
 
 
 def expert_ffn_decode_workspace_bytes(T: int, K: int, I: int) -> int:
+    _i32(T, K, I)
     return int(load().moe_expert_ffn_decode_workspace_bytes(T, K, I))
 
 
@@ -236,6 +251,7 @@ def moe_expert_ffn_decode(x: torch.Tensor, x_s: Optional[torch.Tensor], topk_idx
         raise ValueError("x must be [T, H], w1 [E_local, 2I, H/2], topk_idx [T, K]")
     (T, H), K = x.shape, topk_idx.shape[1]
     E, I = w1.shape[0], w1.shape[1] // 2
+    _i32(T, H, K, E, I, expert_begin)
     ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
     _launch("moe_expert_ffn_decode", dev, stream,
             _ptr(x, "x", dev, x.shape, _BF16 if x_s is None else _CODES), _scales(x_s, "x_s", dev, T, H, MOE_MXFP4),
