@@ -327,7 +327,7 @@ struct TokenPairs {
 // ---------------------------------------------------------------------------------------
 // out: a workgroup has 16 columns of out for all tokens; its waves share the (expert, K block)
 // pairs evenly. An expert's tokens are gathered into the columns of the product, eight at a time, or
-// sixteen where it has more (8 experts with 64 tokens each at H 5120, eight at a time: 92 us, so 64),
+// sixteen where it has more (8 experts with 64 tokens each at H 5120, eight at a time: 76 us, so 51),
 // and the columns' sums go to their tokens' sums in the wave's part of LDS.
 //
 // A weight tile is one load, and what belongs to it must not cost several: the address unit
@@ -336,7 +336,7 @@ struct TokenPairs {
 // 96 us). So h comes in whole lines, several K blocks a load, and goes to the lanes that want it
 // by way of LDS, and the scales of four K blocks come as words (80 us with the latter alone).
 // ---------------------------------------------------------------------------------------
-// 4 waves a SIMD: two workgroups of 8 waves a CU, or one of 16 (13 tokens at H 7168: 18 us; 22 with 3)
+// 4 waves a SIMD: two workgroups of 8 waves a CU, or one of 16 (13 tokens at H 7168: 26 us; 35 with 2)
 template <int NW, int TOK>
 __global__ __launch_bounds__(64 * NW, 4) void decode_out_kernel(DecodeArgs a) {
   constexpr int U = 4;                                // K blocks at a time
@@ -510,15 +510,17 @@ int launch_expert_ffn_decode(const void* x, const void* x_s, int32_t T, int32_t 
   // registers admit two of 8 waves. 8 against 4, of 128 experts at H 4096: 13.3 / 13.8 us (8 pairs), 23.6 / 18.9
   // (16), 37.1 / 33.1 (32); 6 of them on one of 8 ranks at H 7168 14.2 / 15.1
   if (T * K <= 8) hipLaunchKernelGGL((decode_h_kernel<8, 2, 1>), gh, dim3(512), 0, stream, a);
-  // 32 tokens for one read of the weights where the experts have more than 8 pairs on average and so
-  // some of them more than 16 tokens; it leaves room for 3 waves a SIMD instead of 4. 32 against 16: 52 / 70 us (8 experts
-  // with 64 tokens each, H 5120), 25 / 34 (16 with up to 24, H 4096), 49 / 49 (64 with 8), 145 / 139 (127 with 4)
+  // 32 tokens for one read of the weights where there are more than 8 pairs for each local expert and so, if all pairs
+  // are local, some experts with more than 16 tokens; it leaves room for 3 waves a SIMD instead of 4. 32 against 16: 52 / 70 us (8
+  // experts with 64 tokens each, H 5120), 25 / 34 (16 with up to 24, H 4096), 49 / 49 (64 with 8), 145 / 139 (127 with 4). T K counts the
+  // pairs of all ranks; on one of several, where few of them are local, 32 is no slower (whole call, 64 tokens, top-8): 108 / 111 us
+  // (32 of 256 experts, up to 7 tokens each, H 7168), 37.4 / 38.4 (8 of 256), 59 / 60 (32 of 128, H 4096), 34.6 / 34.6 (16 of 128)
   else if (T > 16 && T * K > 8 * E) hipLaunchKernelGGL((decode_h_kernel<4, 2, 2>), gh, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL((decode_h_kernel<4, 2, 1>), gh, dim3(256), 0, stream, a);
   if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   // 16 waves a workgroup where that is one workgroup a CU at most and each wave has a dozen tiles and more
-  // (16 against 8 waves: 9.0 / 8.5 us at 96 tiles a workgroup, 80 / 95 at 1536)
-  const bool wide = H / 16 <= cus && (int64_t)gh.y * (I / 128) >= 256;
+  // (16 against 8 waves: 11.0 / 9.5 us at 96 tiles a workgroup, 14.5 / 15.7 and 18.9 / 20.6 at 192, 22 / 24 at 384, 85 / 100 at 1536)
+  const bool wide = H / 16 <= cus && (int64_t)gh.y * (I / 128) >= 192;
   if (T > 16) {
     if (wide) hipLaunchKernelGGL((decode_out_kernel<16, 64>), go, dim3(1024), 0, stream, a);
     else hipLaunchKernelGGL((decode_out_kernel<8, 64>), go, dim3(512), 0, stream, a);
