@@ -109,9 +109,9 @@ typedef struct moe_router_config {
  * token: never chosen, and (logit) no part of the softmax. The type's lowest value is an
  * ordinary logit. +infinity counts as the largest finite value. A token with fewer than K
  * experts to choose from has topk_idx -1 and weight 0 in the places left over (the layer
- * takes -1 as another rank's expert). Normalised weights are right however small the scores are: a token's whose scores
- * are too small for fp32 as any other's. A sigmoid that is 0 in 64 bits (1 / (1 + exp(-logit)), logits below -709.78) is 0,
- * and where all chosen scores are 0 the weights, and their gradients, are 0.
+ * takes -1 as another rank's expert). Normalised weights are right where the scores themselves are
+ * too small for fp32, too. A sigmoid that is 0 in 64 bits (1 / (1 + exp(-logit)), logits below
+ * -709.78) is 0; where all chosen scores are 0 the weights, and their gradients, are 0.
  * logits: fp32 or bf16 [T][E] (logits_dtype); topk_idx: int32 [T][K]; topk_weights: fp32
  * [T][K].
  * Errors: MOE_ERR_INVALID (null or misaligned pointers, T < 0, E not in [1,1024], K not in
@@ -137,11 +137,12 @@ MOE355_API int moe_router_topk_backward(const float* d_topk_weights, const void*
 
 /*
  * moe_dispatch for rows that are quantised already: pool[pos[t,k]] = q[t] with its scale
- * words, moved to their tile-major places. Epoch, workspace, pool_rows, what is left alone and the pool's
- * content are as moe_dispatch with act_dtype has them: with q from moe_rmsnorm the pool has the bits moe_dispatch makes of
- * the bf16 rows (and in MXFP8 zeros in a last scale word's bytes past the row's last block, which nothing reads).
- * A tile's flag is raised, as there, after its rows and scale words are stored, but nearly all of them at the call's end (its
- * workgroups publish once): an FFN that waits for them on another stream begins then.
+ * words, moved to their tile-major places. Epoch, workspace, pool_rows, what is left alone and
+ * the pool's content are as moe_dispatch with act_dtype has them: with q from moe_rmsnorm the
+ * pool has the bits moe_dispatch makes of the bf16 rows (and in MXFP8 zeros in a last scale
+ * word's bytes past the row's last block, which nothing reads). A tile's flag is raised, as
+ * there, after its rows and scale words are stored, but nearly all of them at the call's end
+ * (its workgroups publish once): an FFN that waits for them on another stream begins then.
  * Errors: those of moe_dispatch; MOE_ERR_INVALID for act_dtype MOE_BF16 and misaligned q,
  * q_s or pool.
  */
@@ -160,14 +161,16 @@ MOE355_API size_t moe_expert_ffn_decode_workspace_bytes(int32_t T, int32_t K, in
  *   h[t,k] = silu(W1[e] gate . x[t]) * (W1[e] up . x[t]), quantised to MXFP8;
  *   out[t] = bf16(sum over the local pairs of topk_weights[t,k] * (W2[e] . h[t,k]))
  * with e = topk_idx[t,k] - expert_begin; pairs with e outside [0, E_local) are other ranks'
- * and add nothing, a token without a local pair gets zeros. Products are exact and summed in fp32, in an order
- * that the arguments' shapes and topk_idx fix.
+ * and add nothing, a token without a local pair gets zeros. Products are exact and summed in
+ * fp32, in an order that the arguments' shapes and topk_idx fix.
  * x: MXFP8 codes [T][H] with x_s (the quantised rows above; x_dtype MOE_MXFP4), or bf16
  * [T][H] with x_s null (x_dtype MOE_BF16: quantised to MXFP8 on the way, as moe_dispatch
  * does). w1, w2: codes as moe_pack_weights lays them out, w1_s, w2_s: scales as
  * moe_pack_mx_scales does -- what moe_expert_ffn takes in mxfp4 mode. topk_idx: int32 [T][K],
  * topk_weights: fp32 [T][K], out: bf16 [T][H], every row written (bf16 rows of x are held there,
- * quantised, until then).
+ * quantised, until then). A code times its scale has to be a bf16 number: scale bytes up to 246
+ * for x (the largest that bf16 rows get) and 252 for weights, larger values count as infinite;
+ * those below 2^-126 are rounded to multiples of 2^-133. Scale byte 255 is NaN.
  * Errors: MOE_ERR_INVALID (null or misaligned pointers, T < 0, K not in [1,16], E_local not
  * in [1,1024], expert_begin < 0, H or I < 1, unknown x_dtype, x_s not as x_dtype wants it,
  * small workspace, out overlapping x), MOE_ERR_UNSUPPORTED (T > 64, H % 128 or I % 128 nonzero, H or I above

@@ -15,7 +15,7 @@ import torch
 
 import combine_moe_dispatch_02_amd as moe
 import oracle
-from oracle.mx import dequantize_mx_e4m3, dequantize_mx_fp4
+from oracle.mx import dequantize_mx_e4m3, dequantize_mx_fp4, quantize_mx_e4m3
 
 from _gpu import say
 
@@ -151,3 +151,21 @@ def test_codes_of_h_far_below_zero():
     got = dequantize_mx_e4m3(codes, np.full((T, I // 32), 127, np.uint8)).reshape(-1, 32)
     assert np.array_equal(scales.reshape(-1)[sure], (e + 127).astype(np.uint8)[sure])
     assert (((got == low) | (got == high))[sure]).all() and (low != high).mean() < 1e-4
+
+
+@pytest.mark.parametrize("w_byte,x_byte", [(0, 240), (1, 240), (10, 246), (127, 127), (240, 3), (252, 8)])
+def test_scales_at_the_ends(w_byte, x_byte):
+    """The largest and smallest scales that are taken, each against one that brings the products back: h's codes are float64's."""
+    say("decode scales at the ends", w_byte, x_byte)
+    T, H, I = 4, 128, 256
+    x, x_s, w1, w1_s = whole_case(T, H, I, 1, w_byte)
+    if w_byte == 252:                                           # and the products stay in fp32
+        x = np.where(x & 0x7F == 0x7E, x ^ 0x7E, x).astype(np.uint8)
+    x_s[:], w1_s[:] = x_byte, w_byte
+    t = torch.from_numpy
+    w2, w2_s = torch.zeros(1, H, I // 2, dtype=torch.uint8), torch.full((1, H, I // 32), 127, dtype=torch.uint8)
+    _, codes, scales = call((t(x), t(x_s)), torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1), t(w1), t(w1_s), w2, w2_s)
+    g = dequantize_mx_e4m3(x, x_s) @ dequantize_mx_fp4(w1[0], w1_s[0]).T
+    h = g[:, :I] / (1.0 + np.exp(-g[:, :I])) * g[:, I:]
+    ref, ref_s = quantize_mx_e4m3(h.astype(np.float32))
+    assert (codes == ref).mean() > 0.999 and (scales == ref_s).all()
