@@ -15,8 +15,8 @@
 // workgroup sums all experts' shares of its 16 columns in LDS, each wave for itself and then
 // the waves in order, so out needs no second pass and no atomics.
 //
-// H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 13 + 8 us (80 MB),
-// 64 tokens 124 + 70 us (1.27 GB: 6.9 and 6.1 TB/s). The pooled path takes 120 and 375 us.
+// H 4096, I 1536, 128 experts, top-8 (h and out kernel, MXFP8 rows): one token 14 + 9 us (80 MB),
+// 64 tokens 124 + 79 us (1.27 GB: 6.8 and 5.4 TB/s). The pooled path takes 110 and 379 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -57,7 +57,7 @@ constexpr uint32_t kNowhere = 0x7fffff00u;   // past every buffer: reads 0
 // the codes as they are, but it lines its 128 products up on the largest and drops what is too small beside it, up to 2e-4 of
 // the sum of their magnitudes. h's sums decide between neighbouring e4m3 codes, and 4 in 10000 went to the wrong one; out's
 // can be small beside their terms, and then that is far more than out's rounding to bf16. It costs 24 conversions a
-// tile for h and 32 for out (both kernels, one token 21.2 -> 23.1 us, 13 tokens at H 7168 48 -> 52, 64 tokens 194 -> 199).
+// tile for h and 32 for out (the call, one token 21.2 -> 23.1 us, 13 tokens at H 7168 48 -> 52, 64 tokens 194 -> 199).
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 struct Bf16Block {
@@ -333,8 +333,8 @@ struct TokenPairs {
 // A weight tile is one load, and what belongs to it must not cost several: the address unit
 // takes as long for a scattered load of 16 bytes a lane as for a weight tile, and with two of
 // those for h, one for its scale and one for the weight's it was busy 77% of the time (64 tokens:
-// 96 us). So h comes in whole lines, several K blocks a load, and goes to the lanes that want it
-// by way of LDS, and the scales of four K blocks come as words (80 us with the latter alone).
+// 96 us, products and all). So h comes in whole lines, several K blocks a load, and goes to the lanes that want it by way
+// of LDS, and the scales of four K blocks come as words (70 us then; 80 with the latter alone).
 // ---------------------------------------------------------------------------------------
 // 4 waves a SIMD: two workgroups of 8 waves a CU, or one of 16 (13 tokens at H 7168: 26 us; 35 with 2)
 template <int NW, int TOK>

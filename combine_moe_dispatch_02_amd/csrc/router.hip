@@ -10,8 +10,8 @@
 // token and, with the scores' 64-bit arithmetic, the grouped choice; a large batch by logits is
 // half latency, half its one read of them.
 //
-// 16384 tokens, 128 experts by logits 7.8 us (8.4 MB) and its backward 5.3; 8192 tokens, 256
-// experts by scores in groups 16 and 5; one token 3.2.
+// 16384 tokens, 128 experts by logits 7.9 us (8.4 MB) and its backward 5.4; 8192 tokens, 256
+// experts by scores in groups 16.5 and 4.8; one token 3.1.
 //
 // Keys are the logits (32 bits) where their order is the scores'. With a bias or with groups
 // ranked by two keys the scores themselves are compared: in 64 bits, since a 32-bit sum would
@@ -66,8 +66,10 @@ __device__ inline float load_logit(const RouterArgs& a, int64_t at) {
 }
 
 // The logits of `rows` tokens from t0 on, expert j * L + l of token `sub` in v[j]. Buffer loads,
-// whatever lies past the last expert or token masked afterwards: all are in flight at once (a
-// load behind a condition waits for the one before, 0.6 us each).
+// whatever lies past the last expert or token masked afterwards, so that they can be in flight at once (a
+// load behind a condition waits for the one before, 0.6 us each). The compiler does not know that t0 is the
+// wave's: it puts a loop over the lanes' different buffers around each load, which runs once (a sixth of the code of
+// the kernel by scores with 16 experts a lane).
 template <int L, int EPL>
 __device__ inline void load_logits(const RouterArgs& a, int64_t t0, int sub, int l, float (&v)[EPL]) {
   const int rows = (int)min((int64_t)(64 / L), a.T - t0);
