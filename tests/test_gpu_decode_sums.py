@@ -94,10 +94,12 @@ def test_every_code_of_h(T, H, I, E):
     assert differs <= 2e-4 * T * I + 2                          # the comparison leaves hardly any code open
 
 
-# W1's rows differ by up to 2^9, so that h's codes are of all sizes; then ordinary rows and more of everything
+# W1's rows differ by up to 2^9, so that h's codes are of all sizes; then ordinary rows and more of everything, the last two by
+# workgroups of 16 waves
 @pytest.mark.parametrize("T,H,I,E,K,spread", [(1, 256, 128, 2, 1, 9), (5, 512, 128, 3, 1, 9), (16, 256, 256, 4, 2, 9), (33, 384, 128, 2, 2, 9),
                                               (64, 256, 128, 6, 1, 9), (64, 2048, 384, 5, 3, 9), (64, 4096, 640, 8, 4, 5),
-                                              (3, 128, 1536, 6, 4, 0), (24, 512, 512, 40, 8, 0)])
+                                              (3, 128, 1536, 6, 4, 0), (24, 512, 512, 40, 8, 0),
+                                              (16, 128, 1536, 30, 8, 0), (64, 256, 1536, 16, 4, 0)])
 def test_out_is_summed_in_fp32(T, H, I, E, K, spread):
     say("decode out's sums", T, H, I, E, K, spread)
     g = torch.Generator().manual_seed(T + H + I)
