@@ -496,7 +496,8 @@ class StreamMoE:
         scales) as moe_rmsnorm quantises them, through the same prepared weights but without plan and
         pool (moe_expert_ffn_decode), on the current stream. y is not rounded to bf16 before
         combine, so the results differ from forward()'s by that rounding. Returns the first rows
-        of the layer's ``out``."""
+        of the layer's ``out``, which x may not overlap. Calls on one layer share its buffers, as
+        forward()'s do: one at a time, in graphs too."""
         from .block import moe_expert_ffn_decode
 
         if self.dtype != "mxfp4":
