@@ -22,6 +22,9 @@ MOE_F32 = 16                  # the norm's weight and the router's logits (moe35
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 
+MOE_GATE_NONE, MOE_GATE_ROW, MOE_GATE_CHANNEL, MOE_GATE_FULL = 0, 1, 2, 3
+MOE_GATE_IDENTITY, MOE_GATE_SIGMOID, MOE_GATE_TANH = 0, 1, 2
+
 MOE_WEIGHTS_ROW_MAJOR = 0
 MOE_WEIGHTS_MFMA_TILED = 1
 
@@ -82,6 +85,18 @@ class RouterConfigT(ctypes.Structure):
     ]
 
 
+class SandwichConfigT(ctypes.Structure):
+    _fields_ = [
+        ("post_eps", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("res_scale", ctypes.c_float),
+        ("branch_scale", ctypes.c_float),
+        ("gate", ctypes.c_int32),
+        ("gate_act", ctypes.c_int32),
+        ("gate_dtype", ctypes.c_int32),
+    ]
+
+
 # (name, restype, argtypes) of every function of moe355.h
 _I32, _U32, _SZ, _VP = ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t, ctypes.c_void_p
 _PP = ctypes.POINTER(PlanT)
@@ -118,11 +133,17 @@ SIGNATURES = [
 
 # the same for moe355_block.h, the operators around the layer
 _RP = ctypes.POINTER(RouterConfigT)
+_SP = ctypes.POINTER(SandwichConfigT)
 BLOCK_SIGNATURES = [
     ("moe_rmsnorm", ctypes.c_int,
      [_VP, _VP, _VP, _I32, _I32, _I32, ctypes.c_double, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
     ("moe_rmsnorm_backward_workspace_bytes", _SZ, [_I32, _I32]),
     ("moe_rmsnorm_backward", ctypes.c_int, [_VP, _VP, _VP, _I32, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _SZ, _VP]),
+    ("moe_sandwich_norm", ctypes.c_int,
+     [_VP, _VP, _VP, _VP, _I32, _VP, _SP, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
+    ("moe_sandwich_norm_backward_workspace_bytes", _SZ, [_I32, _I32]),
+    ("moe_sandwich_norm_backward", ctypes.c_int,
+     [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SP, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     ("moe_router_topk", ctypes.c_int, [_VP, _I32, _VP, _I32, _I32, _I32, _RP, _VP, _VP, _VP]),
     ("moe_router_topk_backward", ctypes.c_int, [_VP, _VP, _I32, _VP, _I32, _I32, _I32, _RP, _VP, _VP]),
     ("moe_dispatch_quantized", ctypes.c_int,

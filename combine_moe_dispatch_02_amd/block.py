@@ -21,7 +21,8 @@ from .layer import Plan, Workspace, _dtype_code, _need_cuda
 __all__ = [
     "RouterConfig", "moe_rmsnorm", "moe_rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "moe_router_topk",
     "moe_router_topk_backward", "moe_dispatch_quantized", "moe_expert_ffn_decode",
-    "expert_ffn_decode_workspace_bytes", "quantized_scales",
+    "expert_ffn_decode_workspace_bytes", "quantized_scales", "moe_sandwich_norm", "moe_sandwich_norm_backward",
+    "sandwich_norm_backward_workspace_bytes",
 ]
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -150,6 +151,100 @@ def moe_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
             _ptr(weight, "weight", dev, (H,), weight.dtype), wcode, _ptr(rstd, "rstd", dev, (T,), _F32),
             _ptr(d_res, "d_res", dev, shape, _BF16), T, H, _ptr(dx, "dx", dev, shape, _BF16),
             _ptr(dweight, "dweight", dev, (H,), _F32), ws_ptr, ws_bytes)
+
+
+_GATE_ACTS = {"none": _abi.MOE_GATE_IDENTITY, "sigmoid": _abi.MOE_GATE_SIGMOID, "tanh": _abi.MOE_GATE_TANH}
+
+
+def _gate(gate: Optional[torch.Tensor], act: str, dev: int, T: int, H: int):
+    """(kind, activation, type, shape, address) of a block's gate: [T, 1] a row, [H] a channel, [T, H] a value."""
+    if act not in _GATE_ACTS:
+        raise ValueError(f"gate_act {act!r}")
+    if gate is None:
+        return _abi.MOE_GATE_NONE, _GATE_ACTS[act], MOE_BF16, None, None
+    dt = _real_dtype(gate, "gate")
+    shape = tuple(gate.shape)
+    kind = {(T, 1): _abi.MOE_GATE_ROW, (H,): _abi.MOE_GATE_CHANNEL, (T, H): _abi.MOE_GATE_FULL}.get(shape)
+    if kind is None:
+        raise ValueError(f"gate has shape {shape}, expected [T, 1], [H] or [T, H]")
+    return kind, _GATE_ACTS[act], dt, shape, _ptr(gate, "gate", dev, shape, gate.dtype)
+
+
+def _both_weights(post_weight, weight, dev: int, H: int):
+    """(type, post_weight's address, weight's) of two norm weights of one type, either of them None."""
+    some = weight if weight is not None else post_weight
+    if some is None:
+        return MOE_BF16, None, None
+    return (_real_dtype(some, "weight" if weight is not None else "post_weight"),
+            _ptr(post_weight, "post_weight", dev, (H,), some.dtype), _ptr(weight, "weight", dev, (H,), some.dtype))
+
+
+def moe_sandwich_norm(x: torch.Tensor, res: Optional[torch.Tensor], weight: Optional[torch.Tensor], eps: float,
+                      s_out: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                      post_weight: Optional[torch.Tensor] = None, post_eps: Optional[float] = None,
+                      gate: Optional[torch.Tensor] = None, gate_act: str = "none", res_scale: float = 1.0,
+                      branch_scale: float = 1.0, post_rstd: Optional[torch.Tensor] = None,
+                      rstd: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                      q_s: Optional[torch.Tensor] = None, dtype="bf16", stream=None) -> None:
+    """Between two blocks: s = res * res_scale + rms_norm(x) * post_weight * (act(gate) * branch_scale), then
+    y = rms_norm(s) * weight and its copy (q, q_s) in the activation format ``dtype``. x is the block's output,
+    s (to ``s_out``) the residual stream. Without post_weight x is taken as it is, without weight
+    only s is made. gate: bf16 or fp32, [T, 1] (a factor a row), [H] (a column) or [T, H];
+    gate_act: "none", "sigmoid" or "tanh". post_eps is eps unless given; post_rstd and rstd for the backward pass."""
+    dev = _device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    shape = x.shape
+    T, H = shape
+    _i32(T, H)
+    code = MOE_BF16 if dtype == "bf16" else _dtype_code(dtype)
+    wcode, wp_ptr, w_ptr = _both_weights(post_weight, weight, dev, H)
+    kind, act, gcode, _, g_ptr = _gate(gate, gate_act, dev, T, H)
+    cfg = _abi.SandwichConfigT(eps if post_eps is None else post_eps, eps, res_scale, branch_scale, kind, act, gcode)
+    _launch("moe_sandwich_norm", dev, stream,
+            _ptr(x, "x", dev, shape, _BF16), _ptr(res, "res", dev, shape, _BF16), wp_ptr, w_ptr, wcode, g_ptr, cfg, T, H,
+            _ptr(s_out, "s_out", dev, shape, _BF16), _ptr(y, "y", dev, shape, _BF16),
+            _ptr(post_rstd, "post_rstd", dev, (T,), _F32), _ptr(rstd, "rstd", dev, (T,), _F32), code,
+            _ptr(q, "q", dev, shape, _CODES), _scales(q_s, "q_s", dev, T, H, code))
+
+
+def sandwich_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    _i32(T, H)
+    return int(load().moe_sandwich_norm_backward_workspace_bytes(T, H))
+
+
+def moe_sandwich_norm_backward(dy: Optional[torch.Tensor], d_s: Optional[torch.Tensor], x: Optional[torch.Tensor],
+                               s: Optional[torch.Tensor], weight: Optional[torch.Tensor],
+                               rstd: Optional[torch.Tensor], dx: torch.Tensor, d_res: Optional[torch.Tensor] = None,
+                               dweight: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, *,
+                               post_weight: Optional[torch.Tensor] = None, post_rstd: Optional[torch.Tensor] = None,
+                               gate: Optional[torch.Tensor] = None, gate_act: str = "none", res_scale: float = 1.0,
+                               branch_scale: float = 1.0, d_post_weight: Optional[torch.Tensor] = None,
+                               d_gate: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_sandwich_norm from dy (of y; with weight) and d_s (of the stream behind it): dx, d_res,
+    dweight and d_post_weight (fp32 [H]) and d_gate (as the gate; of a channel gate fp32 [H]), written, not
+    added to. x, s, rstd and post_rstd are the forward's. ws is a byte tensor of
+    sandwich_norm_backward_workspace_bytes(T, H), needed for the sums over rows."""
+    dev = _device(dx, "dx")
+    if dx.dim() != 2:
+        raise ValueError("dx must be [T, H]")
+    shape = dx.shape
+    T, H = shape
+    _i32(T, H)
+    wcode, wp_ptr, w_ptr = _both_weights(post_weight, weight, dev, H)
+    kind, act, gcode, gshape, g_ptr = _gate(gate, gate_act, dev, T, H)
+    if d_gate is not None and gate is None:
+        raise ValueError("d_gate without a gate")
+    cfg = _abi.SandwichConfigT(0.0, 0.0, res_scale, branch_scale, kind, act, gcode)
+    ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
+    _launch("moe_sandwich_norm_backward", dev, stream,
+            _ptr(dy, "dy", dev, shape, _BF16), _ptr(d_s, "d_s", dev, shape, _BF16), _ptr(x, "x", dev, shape, _BF16),
+            _ptr(s, "s", dev, shape, _BF16), wp_ptr, w_ptr, wcode, g_ptr, cfg, _ptr(post_rstd, "post_rstd", dev, (T,), _F32),
+            _ptr(rstd, "rstd", dev, (T,), _F32), T, H, _ptr(dx, "dx", dev, shape, _BF16),
+            _ptr(d_res, "d_res", dev, shape, _BF16), _ptr(dweight, "dweight", dev, (H,), _F32),
+            _ptr(d_post_weight, "d_post_weight", dev, (H,), _F32),
+            _ptr(d_gate, "d_gate", dev, gshape, _F32 if kind == _abi.MOE_GATE_CHANNEL else gate.dtype if gate is not None else None),
+            ws_ptr, ws_bytes)
 
 
 @dataclass(frozen=True)

@@ -33,6 +33,22 @@ static int check_norm(const void* weight, int32_t weight_dtype, int32_t T, int32
   return MOE_OK;
 }
 
+// the two norms around the residual's addition, their gate and scales
+static int check_sandwich(const void* post_weight, const void* weight, int32_t weight_dtype, const void* gate,
+                          const moe_sandwich_config* c, int32_t T, int32_t H) {
+  if (!c || T < 0 || H < 8 || (weight_dtype != MOE_BF16 && weight_dtype != MOE_F32)) return MOE_ERR_INVALID;
+  if (misaligned({post_weight, weight}, 16)) return MOE_ERR_INVALID;
+  if (!(c->eps >= 0.0) || !std::isfinite(c->eps) || !(c->post_eps >= 0.0) || !std::isfinite(c->post_eps)) return MOE_ERR_INVALID;
+  if (!std::isfinite(c->res_scale) || !std::isfinite(c->branch_scale)) return MOE_ERR_INVALID;
+  if (c->gate < MOE_GATE_NONE || c->gate > MOE_GATE_FULL) return MOE_ERR_INVALID;
+  if (c->gate_act < MOE_GATE_IDENTITY || c->gate_act > MOE_GATE_TANH) return MOE_ERR_INVALID;
+  if (c->gate_dtype != MOE_BF16 && c->gate_dtype != MOE_F32) return MOE_ERR_INVALID;
+  if (c->gate == MOE_GATE_NONE ? gate != nullptr : (!gate && (T > 0 || c->gate == MOE_GATE_CHANNEL))) return MOE_ERR_INVALID;
+  if (misaligned({gate}, c->gate != MOE_GATE_ROW ? 16 : c->gate_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID;
+  if (H % 8 != 0 || H > kMaxWidth) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 static int check_router(int32_t logits_dtype, int32_t T, int32_t E, int32_t K, const moe_router_config* c) {
   if (!c || T < 0 || E < 1 || E > 1024 || K < 1 || K > 16) return MOE_ERR_INVALID;
   if (logits_dtype != MOE_BF16 && logits_dtype != MOE_F32) return MOE_ERR_INVALID;
@@ -96,6 +112,64 @@ MOE355_API int moe_rmsnorm_backward(const void* dy, const void* s, const void* w
     return MOE_ERR_INVALID;
   return launch_rmsnorm_backward(dy, s, weight, weight_dtype == MOE_F32, rstd, d_res, T, H, dx, dweight, ws,
                                  static_cast<hipStream_t>(stream));
+}
+
+MOE355_API int moe_sandwich_norm(const void* x, const void* res, const void* post_weight, const void* weight,
+                                 int32_t weight_dtype, const void* gate, const moe_sandwich_config* cfg, int32_t T,
+                                 int32_t H, void* s_out, void* y, float* post_rstd, float* rstd, int32_t q_dtype,
+                                 void* q, void* q_s, void* stream) {
+  BlockRange trace("moe_sandwich_norm");
+  const int rc = check_sandwich(post_weight, weight, weight_dtype, gate, cfg, T, H);
+  if (rc == MOE_ERR_INVALID) return rc;
+  if (q_dtype != MOE_BF16 && q_dtype != MOE_FP8_E4M3_G128 && q_dtype != MOE_MXFP4) return MOE_ERR_INVALID;
+  if (T > 0) {
+    if (!x || !s_out || s_out == y) return MOE_ERR_INVALID;
+    if (weight ? (!y && !q) : (y || rstd)) return MOE_ERR_INVALID;
+    if (!post_weight && post_rstd) return MOE_ERR_INVALID;
+    if (q_dtype == MOE_BF16 ? (q || q_s) : (!q || !q_s || !weight)) return MOE_ERR_INVALID;
+    if (misaligned({x, res, s_out, y, q}, 16) || misaligned({post_rstd, rstd, q_s}, 4)) return MOE_ERR_INVALID;
+  }
+  if (rc != MOE_OK) return rc;
+  if ((q_dtype == MOE_FP8_E4M3_G128 && H % 128 != 0) || (q_dtype == MOE_MXFP4 && H % 32 != 0))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  return launch_sandwich_norm({x, res, post_weight, weight, weight_dtype == MOE_F32, gate, *cfg, T, H, s_out, y, post_rstd, rstd,
+                               q_dtype, q, q_s},
+                              static_cast<hipStream_t>(stream));
+}
+
+MOE355_API size_t moe_sandwich_norm_backward_workspace_bytes(int32_t T, int32_t H) {
+  if (T < 1 || H < 8 || H % 8 != 0 || H > kMaxWidth) return 0;
+  return (size_t)3 * sandwich_backward_blocks(T, H) * H * sizeof(float);   // two weights and a channel gate
+}
+
+MOE355_API int moe_sandwich_norm_backward(const void* dy, const void* d_s, const void* x, const void* s,
+                                          const void* post_weight, const void* weight, int32_t weight_dtype,
+                                          const void* gate, const moe_sandwich_config* cfg, const float* post_rstd,
+                                          const float* rstd, int32_t T, int32_t H, void* dx, void* d_res,
+                                          float* dweight, float* d_post_weight, void* d_gate, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  BlockRange trace("moe_sandwich_norm_backward");
+  const int rc = check_sandwich(post_weight, weight, weight_dtype, gate, cfg, T, H);
+  if (rc == MOE_ERR_INVALID) return rc;
+  if ((dweight && !weight) || (d_post_weight && !post_weight) || (d_gate && cfg->gate == MOE_GATE_NONE)) return MOE_ERR_INVALID;
+  const bool channel = cfg->gate == MOE_GATE_CHANNEL;
+  if (misaligned({dweight, d_post_weight}, 4)) return MOE_ERR_INVALID;
+  if (misaligned({d_gate}, channel ? 4 : cfg->gate == MOE_GATE_FULL ? 16 : cfg->gate_dtype == MOE_F32 ? 4 : 2)) return MOE_ERR_INVALID;
+  const bool sums = dweight || d_post_weight || (channel && d_gate);
+  if (T > 0) {
+    if (!dx || dx == d_res) return MOE_ERR_INVALID;
+    if (weight ? (!dy || !s || !rstd) : (dy || !d_s)) return MOE_ERR_INVALID;
+    if ((post_weight || d_gate) && !x) return MOE_ERR_INVALID;
+    if (post_weight && !post_rstd) return MOE_ERR_INVALID;
+    if (misaligned({dy, d_s, x, s, dx, d_res}, 16) || misaligned({post_rstd, rstd}, 4)) return MOE_ERR_INVALID;
+  }
+  if (rc != MOE_OK) return rc;
+  if (T > 0 && sums && (!ws || misaligned({ws}, 16) || ws_bytes < moe_sandwich_norm_backward_workspace_bytes(T, H)))
+    return MOE_ERR_INVALID;
+  return launch_sandwich_norm_backward({dy, d_s, x, s, post_weight, weight, weight_dtype == MOE_F32, gate, *cfg, post_rstd, rstd, T, H,
+                                        dx, d_res, dweight, d_post_weight, d_gate, ws},
+                                       static_cast<hipStream_t>(stream));
 }
 
 MOE355_API int moe_router_topk(const void* logits, int32_t logits_dtype, const float* bias, int32_t T, int32_t E,

@@ -149,4 +149,47 @@ int launch_calibrate_mfma(int32_t iters, float* sink, int32_t workgroups, hipStr
 int launch_calibrate_stream(const void* src, void* dst, int64_t bytes, int32_t mode, uint32_t* sink,
                             int32_t workgroups, hipStream_t stream);
 
+// sandwich.hip
+struct SandwichLaunch {
+  const void* x;
+  const void* res;
+  const void* post_weight;
+  const void* weight;
+  bool w_f32;
+  const void* gate;
+  moe_sandwich_config cfg;
+  int32_t T, H;
+  void* s;
+  void* y;
+  float* post_rstd;
+  float* rstd;
+  int32_t q_dtype;
+  void* q;
+  void* q_s;
+};
+int launch_sandwich_norm(const SandwichLaunch& l, hipStream_t stream);
+
+struct SandwichBwdLaunch {
+  const void* dy;
+  const void* d_s;
+  const void* x;
+  const void* s;
+  const void* post_weight;
+  const void* weight;
+  bool w_f32;
+  const void* gate;
+  moe_sandwich_config cfg;
+  const float* post_rstd;
+  const float* rstd;
+  int32_t T, H;
+  void* dx;
+  void* d_res;
+  float* dweight;
+  float* d_post_weight;
+  void* d_gate;
+  void* ws;
+};
+int32_t sandwich_backward_blocks(int32_t T, int32_t H);
+int launch_sandwich_norm_backward(const SandwichBwdLaunch& l, hipStream_t stream);
+
 }  // namespace moe

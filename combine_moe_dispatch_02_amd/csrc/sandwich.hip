@@ -1,0 +1,563 @@
+// The norms behind a block and in front of the next one, with the block's gate, the scales of both
+// branches and the residual's addition between them, and the backward pass.
+//
+//   r1 = fp32(1 / sqrt(mean(x^2) + eps1)), p = (x r1) wp      (without a post-norm: p = x)
+//   f = act(gate) branch_scale, s = bf16(res_scale res + p f)
+//   r2 = fp32(1 / sqrt(mean(s^2) + eps2)), y = bf16((s r2) w), (q, q_s) = y in 8 bits;
+//   backward, with xs = s r2, xh = x r1, g = dy w:
+//   ds = d_s + r2 (g - xs mean(g xs)), d_res = res_scale ds, dp = f ds,
+//   dx = r1 (dp wp - xh mean(dp wp xh)), d_gate = branch_scale act'(gate) ds p, summed over what
+//   the gate is broadcast to, dw = sum over rows of dy xs, dwp = sum over rows of dp xh.
+//
+// Both passes move a few bytes for every value and compute some tens of operations on it: the memory's
+// rate bounds them, and for one row the launch. As in the single norm a row lives in the registers
+// of the W waves that share it, and only sums cross lanes. The two sums of squares are in 64
+// bits, so that both statistics are the same fp32 numbers in whatever order they are summed, and
+// products and sums are rounded one by one (no contraction), so that the stream, y and the codes do
+// not hang on how the compiler pairs them.
+#include "norm.h"
+
+#include <algorithm>
+
+#include "kernels.h"
+
+namespace moe {
+
+// the gate's factor without branch_scale, and its slope
+__device__ inline float gate_act(int act, float z) {
+  if (act == MOE_GATE_SIGMOID) return 1.0f / (1.0f + expf(-z));
+  if (act == MOE_GATE_TANH) return tanhf(z);
+  return z;
+}
+__device__ inline float gate_slope(int act, float f) {
+  if (act == MOE_GATE_SIGMOID) return f * (1.0f - f);
+  if (act == MOE_GATE_TANH) return 1.0f - f * f;
+  return 1.0f;
+}
+__device__ inline float load_scalar(const void* p, bool f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : bf16_lo(static_cast<const uint16_t*>(p)[i]);
+}
+__device__ inline uint32_t val_bytes(bool f32, int H) { return (uint32_t)H * (f32 ? 4u : 2u); }
+
+struct SandwichArgs {
+  const uint16_t* x;
+  const uint16_t* res;
+  const void* wp;      // null: no post-norm
+  const void* w;       // null: no norm behind the addition
+  const void* gate;
+  int32_t w_f32, gate_f32, gate_kind, act;
+  float res_scale, branch_scale;
+  int32_t T, H;
+  double eps1, eps2;
+  uint16_t* s;
+  uint16_t* y;
+  float* r1;
+  float* r2;
+  uint8_t* q;
+  void* q_s;
+};
+
+__device__ inline float inverse_rms(double ss, int H, double eps) { return (float)(1.0 / __builtin_sqrt(ss / (double)H + eps)); }
+
+// W waves a row, W = 1: four rows a workgroup; CPL chunks of 8 values a lane. With an 8-bit output the
+// rows in 16 bits pass the caches by, as in the single norm.
+template <int W, int CPL, int QF>
+__global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_kernel(SandwichArgs a) {
+#pragma clang fp contract(off)
+  constexpr int ROWS = W == 1 ? 4 : 1;
+  constexpr bool NT = QF != 0;
+  __shared__ double red[2 * W];
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = W == 1 ? 0 : wave;
+  const int H = a.H, nch = H >> 3, words = (H + 127) >> 7;
+  const int c0 = sub * (kWave * CPL) + lane;
+  const uint32_t row_bytes = (uint32_t)H * 2u;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, a.w ? val_bytes(a.w_f32, H) : 0u);
+  const __amdgpu_buffer_rsrc_t wpr = make_rsrc(a.wp, a.wp ? val_bytes(a.w_f32, H) : 0u);
+  const bool columns = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
+  int odd = 0;
+  for (int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
+    const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + t * H, row_bytes);
+    const __amdgpu_buffer_rsrc_t rr = make_rsrc(a.res ? a.res + t * H : nullptr, a.res ? row_bytes : 0u);
+    u32x4 v[CPL], r[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) v[i] = load_row<NT>(xr, (uint32_t)(c0 + i * kWave) * 16u);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) r[i] = load_row<NT>(rr, (uint32_t)(c0 + i * kWave) * 16u);
+    float row_f = a.branch_scale;
+    if (a.gate_kind == MOE_GATE_ROW) row_f = gate_act(a.act, load_scalar(a.gate, a.gate_f32, t)) * a.branch_scale;
+    const uint32_t gb = val_bytes(a.gate_f32, H);
+    const __amdgpu_buffer_rsrc_t gr =
+        make_rsrc(columns ? static_cast<const char*>(a.gate) + (a.gate_kind == MOE_GATE_FULL ? t * gb : 0) : nullptr, columns ? gb : 0u);
+    float r1 = 0.f;
+    if (a.wp) {
+      double ss = 0.0;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        float f[8];
+        unpack8(v[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)f[j], (double)f[j], ss);
+      }
+      ss = row_sum<W>(ss, red, sub, odd);
+      odd ^= 1;
+      r1 = inverse_rms(ss, H, a.eps1);
+      if (a.r1 && sub == 0 && lane == 0) a.r1[t] = r1;
+    }
+    const __amdgpu_buffer_rsrc_t sr = make_rsrc(a.s + t * H, row_bytes);
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = c0 + i * kWave;
+      float p[8], b[8];
+      unpack8(v[i], p);
+      unpack8(r[i], b);
+      if (a.wp) {
+        float w[8];
+        load_weight(wpr, a.w_f32, c, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = (p[j] * r1) * w[j];
+      }
+      if (columns) {
+        float z[8];
+        load_weight(gr, a.gate_f32, c, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = p[j] * (gate_act(a.act, z[j]) * a.branch_scale);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = p[j] * row_f;
+      }
+      if (a.res) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = b[j] * a.res_scale + p[j];
+      }
+      v[i] = pack8(p);
+      store_row<NT>(v[i], sr, (uint32_t)c * 16u);
+      if (c < nch) {       // chunks past the row: a gate of theirs may have made anything of their zeros
+        unpack8(v[i], p);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)p[j], (double)p[j], ss);
+      }
+    }
+    if (!a.w) continue;
+    ss = row_sum<W>(ss, red, sub, odd);
+    odd ^= 1;
+    const float r2 = inverse_rms(ss, H, a.eps2);
+    if (a.r2 && sub == 0 && lane == 0) a.r2[t] = r2;
+    const __amdgpu_buffer_rsrc_t yr = make_rsrc(a.y ? a.y + t * H : nullptr, a.y ? row_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t qr = make_rsrc(QF ? a.q + t * H : nullptr, QF ? (uint32_t)H : 0u);
+    uint8_t* q_s = static_cast<uint8_t*>(a.q_s) + t * words * 4;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = c0 + i * kWave;
+      float f[8], w[8];
+      unpack8(v[i], f);
+      load_weight(wr, a.w_f32, c, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = (f[j] * r2) * w[j];
+      u32x4 o = pack8(f);
+      if (QF == 2 && c >= nch) o = u32x4{0u, 0u, 0u, 0u};
+      store_row<NT>(o, yr, (uint32_t)c * 16u);
+      if constexpr (QF != 0) store_quantised<QF>(o, c, nch, words, qr, q_s);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------------------
+struct SandwichBwdArgs {
+  const uint16_t* dy;
+  const uint16_t* d_s;
+  const uint16_t* x;
+  const uint16_t* s;
+  const void* wp;
+  const void* w;
+  const void* gate;
+  int32_t w_f32, gate_f32, gate_kind, act;
+  float res_scale, branch_scale;
+  const float* r1;
+  const float* r2;
+  int32_t T, H;
+  uint16_t* dx;
+  uint16_t* d_res;
+  void* d_gate;          // row and full: in the gate's type (channel: through part_gate)
+  float* part_w;         // [gridDim.x][H] partial sums of dw, dwp and d_gate, or null
+  float* part_wp;
+  float* part_gate;
+};
+
+// three sums over a row at once
+template <int W>
+__device__ inline void row_sum3(float (&v)[3], float* red, int sub, int odd) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) v[k] = wave_sum(v[k]);
+  if constexpr (W > 1) {
+    float* r = red + odd * 3 * W;
+    if (lane_id() == 0) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) r[sub * 3 + k] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = r[k];
+#pragma unroll
+    for (int i = 1; i < W; ++i)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) v[k] += r[i * 3 + k];
+  }
+}
+
+// A row's two means need one exchange: with k = p f (its column sums over the row) the second mean is linear in
+// the first, mean(dp wp xh) = (sum k (d_s + r2 g) - r2 mean(g xs) sum k xs) / H. GK: 0 no gate or one a row (k = p:
+// f leaves the sums), 1 a gate for each column, 2 for each value.
+template <int W, int CPL, bool POST, int GK>
+__global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_backward_kernel(SandwichBwdArgs a) {
+  constexpr int ROWS = W == 1 ? 4 : 1;
+  constexpr bool HELD = CPL == 1;         // weights, gate and rows stay in registers
+  constexpr int NACC = 1 + (POST ? 1 : 0) + (GK == 1 ? 1 : 0);
+  __shared__ float red[2 * 3 * W];
+  __shared__ float s_acc[W == 1 ? 3 : 1][W == 1 ? 64 * 8 : 1];
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sub = W == 1 ? 0 : wave;
+  const int H = a.H;
+  const int c0 = sub * (kWave * CPL) + lane;
+  const uint32_t row_bytes = (uint32_t)H * 2u;
+  const bool pre = a.w != nullptr;
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, pre ? val_bytes(a.w_f32, H) : 0u);
+  const __amdgpu_buffer_rsrc_t wpr = make_rsrc(a.wp, POST ? val_bytes(a.w_f32, H) : 0u);
+  const uint32_t gb = val_bytes(a.gate_f32, H);
+  constexpr int NH = HELD ? CPL : 1;
+  float acc[NACC][CPL][8];
+  constexpr int AW = 0, AP = 1, AG = POST ? 2 : 1;
+#pragma unroll
+  for (int k = 0; k < NACC; ++k)
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[k][i][j] = 0.f;
+  float w[NH][8], wp[NH][8], z[NH][8];
+  const __amdgpu_buffer_rsrc_t gcr = make_rsrc(GK == 1 ? a.gate : nullptr, GK == 1 ? gb : 0u);
+  const auto weights = [&](int at, int c) {
+    load_weight(wr, a.w_f32, c, w[at]);
+    if constexpr (POST) load_weight(wpr, a.w_f32, c, wp[at]);
+    if constexpr (GK == 1) {
+      load_weight(gcr, a.gate_f32, c, z[at]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[at][j] = gate_act(a.act, z[at][j]);
+    }
+  };
+  if constexpr (HELD) weights(0, c0);
+  int odd = 0;
+  for (int64_t t = blockIdx.x + (W == 1 ? (int64_t)wave * gridDim.x : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
+    const auto row = [&](const uint16_t* p) { return make_rsrc(p ? p + t * H : nullptr, p ? row_bytes : 0u); };
+    const __amdgpu_buffer_rsrc_t dr = row(a.dy), er = row(a.d_s), xr = row(a.x), sr = row(a.s);
+    const __amdgpu_buffer_rsrc_t gr =
+        make_rsrc(GK == 2 ? static_cast<const char*>(a.gate) + t * gb : nullptr, GK == 2 ? gb : 0u);
+    u32x4 vd[NH], ve[NH], vx[NH], vs[NH];
+    const auto rows = [&](int at, int c) {
+      const uint32_t o = (uint32_t)c * 16u;
+      vd[at] = load_row<HELD>(dr, o);
+      ve[at] = load_row<HELD>(er, o);
+      vx[at] = load_row<HELD>(xr, o);
+      vs[at] = load_row<HELD>(sr, o);
+      if constexpr (GK == 2) {
+        load_weight(gr, a.gate_f32, c, z[at]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[at][j] = gate_act(a.act, z[at][j]);
+      }
+    };
+    if constexpr (HELD) rows(0, c0);
+    const float r2 = pre ? a.r2[t] : 0.f;
+    const float r1 = POST ? a.r1[t] : 0.f;
+    float zr = 1.f;
+    if (GK == 0 && a.gate_kind == MOE_GATE_ROW) zr = gate_act(a.act, load_scalar(a.gate, a.gate_f32, t));
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = c0 + i * kWave, h = HELD ? i : 0;
+      if constexpr (!HELD) {
+        rows(0, c);
+        weights(0, c);
+      }
+      float d[8], e[8], x[8], s[8];
+      unpack8(vd[h], d);
+      unpack8(ve[h], e);
+      unpack8(vx[h], x);
+      unpack8(vs[h], s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float k = x[j];
+        if constexpr (POST) k = (x[j] * r1) * wp[h][j];
+        if constexpr (GK != 0) k *= z[h][j];
+        float de = e[j];
+        if (pre) {
+          const float xs = s[j] * r2, dxs = d[j] * xs;
+          acc[AW][i][j] += dxs;
+          sum[0] += dxs * w[h][j];
+          sum[2] += k * xs;
+          de += r2 * (d[j] * w[h][j]);
+        }
+        sum[1] += k * de;
+      }
+    }
+    row_sum3<W>(sum, red, sub, odd);
+    odd ^= 1;
+    const float c2 = sum[0] / (float)H;
+    const float kds = sum[1] - (r2 * c2) * sum[2];       // of ds with p, times the gate where that is not one a row
+    const float c1 = a.branch_scale * (GK == 0 ? zr : 1.f) * kds / (float)H;
+    if (GK == 0 && a.gate_kind == MOE_GATE_ROW && a.d_gate && sub == 0 && lane == 0) {
+      const float dg = a.branch_scale * gate_slope(a.act, zr) * kds;
+      if (a.gate_f32) static_cast<float*>(a.d_gate)[t] = dg;
+      else static_cast<uint16_t*>(a.d_gate)[t] = (uint16_t)pack_bf16x2(dg, 0.f);
+    }
+    const __amdgpu_buffer_rsrc_t dxr = make_rsrc(a.dx + t * H, row_bytes);
+    const __amdgpu_buffer_rsrc_t drr = make_rsrc(a.d_res ? a.d_res + t * H : nullptr, a.d_res ? row_bytes : 0u);
+    const bool write_gate = GK == 2 && a.d_gate;
+    const __amdgpu_buffer_rsrc_t dgr =
+        make_rsrc(write_gate ? static_cast<char*>(a.d_gate) + t * gb : nullptr, write_gate ? gb : 0u);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const int c = c0 + i * kWave, h = HELD ? i : 0;
+      if constexpr (!HELD) {
+        rows(0, c);
+        weights(0, c);
+      }
+      float d[8], e[8], x[8], s[8], o[8], ro[8], dg[8];
+      unpack8(vd[h], d);
+      unpack8(ve[h], e);
+      unpack8(vx[h], x);
+      unpack8(vs[h], s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float ds = e[j];
+        if (pre) ds += r2 * (d[j] * w[h][j] - (s[j] * r2) * c2);
+        ro[j] = a.res_scale * ds;
+        const float f = a.branch_scale * (GK == 0 ? zr : z[h][j]);
+        const float dp = f * ds;
+        const float xh = POST ? x[j] * r1 : x[j];
+        if constexpr (GK != 0) {
+          const float g = a.branch_scale * gate_slope(a.act, z[h][j]) * ds * (POST ? xh * wp[h][j] : xh);
+          if constexpr (GK == 1) acc[AG][i][j] += g;
+          else dg[j] = g;
+        }
+        if constexpr (POST) {
+          acc[AP][i][j] += dp * xh;
+          o[j] = r1 * (dp * wp[h][j] - xh * c1);
+        } else {
+          o[j] = dp;
+        }
+      }
+      store_row<true>(pack8(o), dxr, (uint32_t)c * 16u);
+      store_row<true>(pack8(ro), drr, (uint32_t)c * 16u);
+      if constexpr (GK == 2) {
+        if (a.gate_f32) {
+          u32x4 lo, hi;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            lo[j] = __builtin_bit_cast(uint32_t, dg[j]);
+            hi[j] = __builtin_bit_cast(uint32_t, dg[4 + j]);
+          }
+          store_row<true>(lo, dgr, (uint32_t)c * 32u);
+          store_row<true>(hi, dgr, (uint32_t)c * 32u + 16u);
+        } else {
+          store_row<true>(pack8(dg), dgr, (uint32_t)c * 16u);
+        }
+      }
+    }
+  }
+  float* const parts[3] = {a.part_w, POST ? a.part_wp : a.part_gate, a.part_gate};
+#pragma unroll
+  for (int k = 0; k < NACC; ++k) {
+    if (!parts[k]) continue;
+    if constexpr (W == 1) {              // four waves' sums joined before they are written
+      __syncthreads();
+      if (wave > 0)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          s_acc[wave - 1][j * 64 + lane] = acc[k][0][j];
+      __syncthreads();
+      if (wave > 0) continue;
+#pragma unroll
+      for (int v = 0; v < 3; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[k][0][j] += s_acc[v][j * 64 + lane];
+    }
+    const __amdgpu_buffer_rsrc_t pr = make_rsrc(parts[k] + (int64_t)blockIdx.x * H, (uint32_t)H * 4u);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const uint32_t o = (uint32_t)(c0 + i * kWave) * 32u;
+      u32x4 p, q;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = __builtin_bit_cast(uint32_t, acc[k][i][j]);
+        q[j] = __builtin_bit_cast(uint32_t, acc[k][i][4 + j]);
+      }
+      buf_store16(p, pr, o);
+      buf_store16(q, pr, o + 16u);
+    }
+  }
+}
+
+struct ColumnSums {
+  const float* part[3];
+  float* out[3];
+  int32_t n, H;
+};
+// out[h] = sum of the n partial rows, always in the same order; as the single norm's (32 columns a workgroup)
+__global__ __launch_bounds__(1024) void sandwich_columns_kernel(ColumnSums a) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  __shared__ f32x4 red[16][8];
+  const float* part = a.part[blockIdx.y];
+  const int lane = lane_id(), wave = threadIdx.x >> 6;
+  const int c = lane & 7, r = lane >> 3;
+  const int h = blockIdx.x * 32 + c * 4;   // H % 8 == 0: four columns are in or out together
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (h < a.H)
+#pragma unroll 8
+    for (int i = wave * 8 + r; i < a.n; i += 128) v += *reinterpret_cast<const f32x4*>(part + (int64_t)i * a.H + h);
+#pragma unroll
+  for (int o = 8; o < 64; o *= 2)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += __shfl_xor(v[j], o, 64);
+  if (r == 0) red[wave][c] = v;
+  __syncthreads();
+  if (wave == 0 && r == 0 && h < a.H) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += red[i][c];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a.out[blockIdx.y][h + j] = v[j];
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------------------
+constexpr int kSandwichMaxBlocks = 1 << 16;
+
+template <int W, int CPL>
+static void launch_q(int qf, int64_t rows, hipStream_t s, const SandwichArgs& a) {
+  const dim3 block(64 * (W == 1 ? 4 : W));
+  const dim3 grid((unsigned)std::min<int64_t>((rows + (W == 1 ? 3 : 0)) / (W == 1 ? 4 : 1), kSandwichMaxBlocks));
+  if (qf == 1) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 1>), grid, block, 0, s, a);
+  else if (qf == 2) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 2>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((sandwich_kernel<W, CPL, 0>), grid, block, 0, s, a);
+}
+
+int launch_sandwich_norm(const SandwichLaunch& l, hipStream_t stream) {
+  SandwichArgs a;
+  a.x = static_cast<const uint16_t*>(l.x);
+  a.res = static_cast<const uint16_t*>(l.res);
+  a.wp = l.post_weight;
+  a.w = l.weight;
+  a.gate = l.gate;
+  a.w_f32 = l.w_f32;
+  a.gate_f32 = l.cfg.gate_dtype == MOE_F32;
+  a.gate_kind = l.cfg.gate;
+  a.act = l.cfg.gate_act;
+  a.res_scale = l.cfg.res_scale;
+  a.branch_scale = l.cfg.branch_scale;
+  a.T = l.T;
+  a.H = l.H;
+  a.eps1 = l.cfg.post_eps;
+  a.eps2 = l.cfg.eps;
+  a.s = static_cast<uint16_t*>(l.s);
+  a.y = static_cast<uint16_t*>(l.y);
+  a.r1 = l.post_rstd;
+  a.r2 = l.rstd;
+  a.q = static_cast<uint8_t*>(l.q);
+  a.q_s = l.q_s;
+  const int qf = l.q_dtype == MOE_FP8_E4M3_G128 ? 1 : l.q_dtype == MOE_MXFP4 ? 2 : 0;
+  const int nch = ((l.H + 127) / 128) * 16;   // chunks, the last scale word's whole
+  if (nch <= 64) launch_q<1, 1>(qf, l.T, stream, a);
+  else if (nch <= 128) launch_q<1, 2>(qf, l.T, stream, a);
+  else if (nch <= 256) launch_q<4, 1>(qf, l.T, stream, a);
+  else if (nch <= 512) launch_q<4, 2>(qf, l.T, stream, a);
+  else if (nch <= 1024) launch_q<4, 4>(qf, l.T, stream, a);
+  else if (nch <= 2048) launch_q<16, 2>(qf, l.T, stream, a);
+  else launch_q<16, 4>(qf, l.T, stream, a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+// Waves that share a row of the backward pass, and its workgroups (4096 waves, 16 a CU): rows of
+// partial sums that the workspace holds. Both depend on T and H alone, and so does the order of the sums.
+static int backward_waves(int32_t H) {
+  const int nch = H / 8;
+  return nch <= 64 ? 1 : nch <= 256 ? 4 : nch <= 512 ? 8 : 16;
+}
+int32_t sandwich_backward_blocks(int32_t T, int32_t H) { return std::min(T, 4096 / std::max(4, backward_waves(H))); }
+
+template <bool POST, int GK>
+static void launch_backward(const SandwichBwdArgs& a, int n, hipStream_t s) {
+  const int nch = a.H / 8;
+  const dim3 grid(n);
+  if (nch <= 64) hipLaunchKernelGGL((sandwich_backward_kernel<1, 1, POST, GK>), grid, dim3(256), 0, s, a);
+  else if (nch <= 256) hipLaunchKernelGGL((sandwich_backward_kernel<4, 1, POST, GK>), grid, dim3(256), 0, s, a);
+  else if (nch <= 512) hipLaunchKernelGGL((sandwich_backward_kernel<8, 1, POST, GK>), grid, dim3(512), 0, s, a);
+  else if (nch <= 1024) hipLaunchKernelGGL((sandwich_backward_kernel<16, 1, POST, GK>), grid, dim3(1024), 0, s, a);
+  else if (nch <= 2048) hipLaunchKernelGGL((sandwich_backward_kernel<16, 2, POST, GK>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((sandwich_backward_kernel<16, 4, POST, GK>), grid, dim3(1024), 0, s, a);
+}
+
+int launch_sandwich_norm_backward(const SandwichBwdLaunch& l, hipStream_t stream) {
+  SandwichBwdArgs a;
+  a.dy = static_cast<const uint16_t*>(l.dy);
+  a.d_s = static_cast<const uint16_t*>(l.d_s);
+  a.x = static_cast<const uint16_t*>(l.x);
+  a.s = static_cast<const uint16_t*>(l.s);
+  a.wp = l.post_weight;
+  a.w = l.weight;
+  a.gate = l.gate;
+  a.w_f32 = l.w_f32;
+  a.gate_f32 = l.cfg.gate_dtype == MOE_F32;
+  a.gate_kind = l.cfg.gate;
+  a.act = l.cfg.gate_act;
+  a.res_scale = l.cfg.res_scale;
+  a.branch_scale = l.cfg.branch_scale;
+  a.r1 = l.post_rstd;
+  a.r2 = l.rstd;
+  a.T = l.T;
+  a.H = l.H;
+  a.dx = static_cast<uint16_t*>(l.dx);
+  a.d_res = static_cast<uint16_t*>(l.d_res);
+  const bool channel = l.cfg.gate == MOE_GATE_CHANNEL;
+  a.d_gate = channel ? nullptr : l.d_gate;
+  const int n = l.T > 0 ? sandwich_backward_blocks(l.T, l.H) : 0;
+  // the sums over rows that the caller wants, their partial rows one array behind another
+  ColumnSums c{};
+  c.n = n;
+  c.H = l.H;
+  int arrays = 0;
+  const auto sums = [&](void* out) -> float* {
+    if (!out) return nullptr;
+    float* part = static_cast<float*>(l.ws) + (int64_t)arrays * n * l.H;
+    c.part[arrays] = part;
+    c.out[arrays++] = static_cast<float*>(out);
+    return part;
+  };
+  a.part_w = sums(l.dweight);
+  a.part_wp = sums(l.d_post_weight);
+  a.part_gate = channel ? sums(l.d_gate) : nullptr;
+  if (n > 0) {
+    const int gk = channel ? 1 : l.cfg.gate == MOE_GATE_FULL ? 2 : 0;
+    if (a.wp) {
+      if (gk == 1) launch_backward<true, 1>(a, n, stream);
+      else if (gk == 2) launch_backward<true, 2>(a, n, stream);
+      else launch_backward<true, 0>(a, n, stream);
+    } else {
+      if (gk == 1) launch_backward<false, 1>(a, n, stream);
+      else if (gk == 2) launch_backward<false, 2>(a, n, stream);
+      else launch_backward<false, 0>(a, n, stream);
+    }
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+  }
+  if (arrays > 0) {
+    hipLaunchKernelGGL(sandwich_columns_kernel, dim3((l.H + 31) / 32, arrays), dim3(1024), 0, stream, c);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -2,7 +2,8 @@
  * moe355_block.h -- C ABI of the operators that stand around the MoE layer of moe355.h in a
  * transformer block, in the same library (libmoe355.so): the residual's addition with the
  * RMS norm and its 8-bit output, the router's choice of experts, the dispatch of rows that
- * are 8-bit codes already, and the expert FFN of a few tokens with MXFP4 weights.
+ * are 8-bit codes already, and the expert FFN of a few tokens with MXFP4 weights; behind the layer the norm of a
+ * block's output with its gate and residual scales, and low-rank adapters of many requests.
  *
  *   serving, one token:  moe_rmsnorm -> (router logits) -> moe_router_topk -> moe_expert_ffn_decode
  *   serving, a prompt:   moe_rmsnorm -> (router logits) -> moe_router_topk -> moe_plan ->
@@ -79,6 +80,83 @@ MOE355_API size_t moe_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H);
 MOE355_API int moe_rmsnorm_backward(const void* dy, const void* s, const void* weight, int32_t weight_dtype,
                                     const float* rstd, const void* d_res, int32_t T, int32_t H, void* dx,
                                     float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* How a block's output is gated (moe_sandwich_config.gate) ... */
+enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_ROW = 1,     /* gate [T]: one for each row */
+  MOE_GATE_CHANNEL = 2, /* gate [H]: one for each column, the same for all rows */
+  MOE_GATE_FULL = 3     /* gate [T][H] */
+};
+/* ... and what of the gate is the factor (gate_act). */
+enum { MOE_GATE_IDENTITY = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_TANH = 2 };
+
+typedef struct moe_sandwich_config {
+  double post_eps;      /* of the norm behind the block */
+  double eps;           /* of the norm in front of the next one */
+  float res_scale;      /* factor of the residual */
+  float branch_scale;   /* factor of the block's output, beside its gate */
+  int32_t gate;         /* MOE_GATE_NONE, _ROW, _CHANNEL or _FULL */
+  int32_t gate_act;     /* MOE_GATE_IDENTITY, _SIGMOID or _TANH */
+  int32_t gate_dtype;   /* MOE_BF16 or MOE_F32 */
+} moe_sandwich_config;
+
+/*
+ * Between two blocks: the norm of the block's output x, its gate, the residual's addition with
+ * a scale for either, the norm in front of the next block, and its 8-bit copy:
+ *   post_rstd[t] = fp32(1 / sqrt(mean(x[t]^2) + post_eps))      sums and root in 64 bits
+ *   p[t]    = (x[t] * post_rstd[t]) * post_weight               (post_weight null: p = x)
+ *   f       = act(gate) * branch_scale                          (no gate: branch_scale)
+ *   s[t]    = bf16(res[t] * res_scale + p[t] * f)               (res null: bf16(p * f))
+ *   rstd[t] = fp32(1 / sqrt(mean(s[t]^2) + eps)),  y[t] = bf16((s[t] * rstd[t]) * weight)
+ *   q, q_s  = the quantised row y[t], as moe_rmsnorm has it
+ * fp32 products and sums, rounded one by one. x, res, s_out, y: bf16 [T][H]; post_weight,
+ * weight: bf16 or fp32 [H] (weight_dtype, both), either may be null; gate as cfg says (null
+ * without one), a channel or full gate 16-byte aligned. s_out receives s, always. With weight
+ * one of y and q is there, without it y, q, q_s and rstd are null. post_rstd and rstd (fp32
+ * [T], for the backward pass) may be null. s_out and y may be x or res (not both the same
+ * one): a row is read before it is written.
+ * Errors: MOE_ERR_INVALID (null or misaligned pointers, T < 0, H < 8, eps negative or not
+ * finite, scales not finite, unknown types, gate kinds or activations, outputs that need a
+ * weight that is not there, s_out the same array as y), MOE_ERR_UNSUPPORTED (H % 8 != 0 or
+ * H > 32768; fp8 with H % 128 != 0; MXFP8 with H % 32 != 0).
+ */
+MOE355_API int moe_sandwich_norm(const void* x, const void* res, const void* post_weight, const void* weight,
+                                 int32_t weight_dtype, const void* gate, const moe_sandwich_config* cfg, int32_t T,
+                                 int32_t H, void* s_out, void* y, float* post_rstd, float* rstd, int32_t q_dtype,
+                                 void* q, void* q_s, void* stream);
+
+/* Bytes of moe_sandwich_norm_backward's workspace (0 for invalid sizes or T = 0). */
+MOE355_API size_t moe_sandwich_norm_backward_workspace_bytes(int32_t T, int32_t H);
+
+/*
+ * Backward of moe_sandwich_norm's bf16 output y, with the gradient d_s of the stream behind it:
+ *   xs = s[t] * rstd[t], g = dy[t] * weight, xh = x[t] * post_rstd[t]
+ *   ds      = d_s[t] + rstd[t] * (g - xs * mean(g * xs))
+ *   d_res[t] = bf16(res_scale * ds),  dp = f * ds
+ *   dx[t]   = bf16(post_rstd[t] * (dp * post_weight - xh * mean(dp * post_weight * xh)))
+ *             (without a post-norm: bf16(dp))
+ *   d_gate  = branch_scale * act'(gate) * ds * p[t]: summed over the columns for a gate a row, over
+ *             the rows for a channel gate
+ *   dweight = sum over t of dy[t] * xs,  d_post_weight = sum over t of dp * xh
+ * Sums in fp32, in orders that T and H fix: results do not change from run to run. dy, d_s, x, s, dx,
+ * d_res: bf16 [T][H]; dy, s and rstd are there with weight; d_s may be null with weight;
+ * x is there with post_weight or a wanted d_gate, post_rstd with post_weight. dx is written
+ * always; d_res, dweight, d_post_weight (fp32 [H]) and d_gate (row and full: the gate's shape
+ * and type; channel: fp32 [H]) may be null. Everything is written, not added to; with T = 0
+ * the sums over rows are zero-filled. dx and d_res may be dy, d_s, x or s (not both the same
+ * one), a full gate's d_gate may be the gate. ws: the workspace, used for the sums over rows
+ * (null if none is wanted).
+ * Errors: MOE_ERR_INVALID (null or misaligned pointers, sizes, cfg as in moe_sandwich_norm,
+ * gradients of what is not there, dx the same array as d_res, small workspace),
+ * MOE_ERR_UNSUPPORTED (H % 8 != 0 or H > 32768).
+ */
+MOE355_API int moe_sandwich_norm_backward(const void* dy, const void* d_s, const void* x, const void* s,
+                                          const void* post_weight, const void* weight, int32_t weight_dtype,
+                                          const void* gate, const moe_sandwich_config* cfg, const float* post_rstd,
+                                          const float* rstd, int32_t T, int32_t H, void* dx, void* d_res,
+                                          float* dweight, float* d_post_weight, void* d_gate, void* ws,
+                                          size_t ws_bytes, void* stream);
 
 /* How the router scores experts. */
 enum {
