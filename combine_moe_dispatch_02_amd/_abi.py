@@ -146,6 +146,13 @@ BLOCK_SIGNATURES = [
      [_VP, _VP, _VP, _VP, _VP, _VP, _I32, _VP, _SP, _VP, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     ("moe_router_topk", ctypes.c_int, [_VP, _I32, _VP, _I32, _I32, _I32, _RP, _VP, _VP, _VP]),
     ("moe_router_topk_backward", ctypes.c_int, [_VP, _VP, _I32, _VP, _I32, _I32, _I32, _RP, _VP, _VP]),
+    ("moe_adapter_workspace_bytes", _SZ, [_I32, _I32, _I32]),
+    ("moe_adapter", ctypes.c_int,
+     [_VP, _I32, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _VP, _I32, _PP, _VP, _I32, _VP, _I32, _VP, _VP, _SZ, _VP]),
+    ("moe_adapter_backward_workspace_bytes", _SZ, [_I32, _I32, _I32, _I32, _I32]),
+    ("moe_adapter_backward", ctypes.c_int,
+     [_VP, _I32, _VP, _I32, _VP, _VP, _VP, _VP, _VP, _I32, _I32, _I32, _I32, _I32, _PP, _VP, _I32, _VP, _I32, _VP, _VP, _VP,
+      _SZ, _VP]),
     ("moe_dispatch_quantized", ctypes.c_int,
      [_VP, _VP, _I32, _I32, _PP, _I32, _VP, _VP, _U32, _VP, _SZ, _VP]),
     ("moe_expert_ffn_decode_workspace_bytes", _SZ, [_I32, _I32, _I32]),

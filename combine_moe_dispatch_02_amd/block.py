@@ -1,8 +1,8 @@
 """Python binding of the operators around the MoE layer (include/moe355_block.h).
 
 The residual's addition with the RMS norm and its 8-bit output, the router's choice of
-experts, the dispatch of rows that are quantised already, and the expert FFN of a few
-tokens. Argument marshalling only, as in ``layer``: the caller owns every tensor and the
+experts, the dispatch of rows that are quantised already, the expert FFN of a few
+tokens; the norms around a block's gate and residual, and low-rank adapters. Argument marshalling only, as in ``layer``: the caller owns every tensor and the
 calls are asynchronous. All tensors of a call are on one device, which need not be the
 current one; ``stream`` defaults to that device's current stream.
 """
@@ -22,7 +22,8 @@ __all__ = [
     "RouterConfig", "moe_rmsnorm", "moe_rmsnorm_backward", "rmsnorm_backward_workspace_bytes", "moe_router_topk",
     "moe_router_topk_backward", "moe_dispatch_quantized", "moe_expert_ffn_decode",
     "expert_ffn_decode_workspace_bytes", "quantized_scales", "moe_sandwich_norm", "moe_sandwich_norm_backward",
-    "sandwich_norm_backward_workspace_bytes",
+    "sandwich_norm_backward_workspace_bytes", "moe_adapter", "moe_adapter_backward", "adapter_workspace_bytes",
+    "adapter_backward_workspace_bytes", "adapter_tile",
 ]
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
@@ -301,6 +302,106 @@ def moe_router_topk_backward(d_topk_weights: torch.Tensor, logits: torch.Tensor,
             _ptr(d_topk_weights, "d_topk_weights", dev, (T, K), _F32),
             _ptr(logits, "logits", dev, logits.shape, logits.dtype), lcode, _ptr(topk_idx, "topk_idx", dev, (T, K), _I32),
             T, E, K, cfg.c(), _ptr(d_logits, "d_logits", dev, logits.shape, logits.dtype))
+
+
+def _rows(t: Optional[torch.Tensor], name: str, dev: int, T: int, width: int):
+    """(address, row pitch) of a checked bf16 tensor [T, width] whose rows may be columns of wider ones."""
+    if t is None:
+        return None, 0
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected bf16")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the call's first tensor on {dev}")
+    if t.shape != (T, width):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, width)}")
+    if T > 1 and (t.stride(1) != 1 or t.stride(0) < width):
+        raise ValueError(f"{name} must have dense rows that do not overlap")
+    if T == 1 and width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    ld = t.stride(0) if T > 1 else width
+    _i32(ld)
+    return t.data_ptr(), ld
+
+
+def adapter_tile(T: int, n: int) -> int:
+    """The tile of a plan that groups T rows by n adapters: 16 where they have few rows each, else 32."""
+    return 16 if T < 32 * n else 32
+
+
+def adapter_workspace_bytes(T: int, K: int, R: int) -> int:
+    _i32(T, K, R)
+    return int(load().moe_adapter_workspace_bytes(T, K, R))
+
+
+def _adapters(a: torch.Tensor, b: torch.Tensor, scale, ranks, dev: int):
+    """(n, K, N, R) of the adapters' tables, and their four addresses."""
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [n, R, K], b [n, N, R]")
+    (n, R, K), N = a.shape, b.shape[1]
+    _i32(n, R, K, N)
+    return (n, K, N, R), (_ptr(a, "a", dev, (n, R, K), _BF16), _ptr(b, "b", dev, (n, N, R), _BF16),
+                          _ptr(scale, "scale", dev, (n,), _F32), _ptr(ranks, "ranks", dev, (n,), _I32))
+
+
+def _adapter_plan(plan: Optional[Plan], dev: int):
+    if plan is None:
+        return None
+    if plan.pos.get_device() != dev:
+        raise ValueError(f"the plan is on device {plan.pos.get_device()}, the call's first tensor on {dev}")
+    return plan.c()
+
+
+def moe_adapter(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, *,
+                base: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None, plan: Optional[Plan] = None,
+                id_begin: int = 0, scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
+                v: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out[t] = base[t] + scale[e] * b[e] @ (a[e] @ x[t]) with e the adapter of row t; base[t] (or zeros) for a row
+    without one. x [T, K], base and out [T, N]: bf16, their rows may be columns of wider tensors; out may be base.
+    a: bf16 [n, R, K], b: bf16 [n, N, R]; scale: fp32 [n]; ranks: int32 [n], the rows of a (columns of b)
+    that an adapter has. The rows' adapters: ids int32 [T] for up to 64 rows (less id_begin; outside
+    [0, n): none), or a Plan with K = 1 that moe_plan made of ids [T, 1] (see adapter_tile()). v: fp32 [T, R], kept for
+    moe_adapter_backward. ws: a byte tensor of adapter_workspace_bytes(T, K, R)."""
+    dev = _device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    (n, K, N, R), table = _adapters(a, b, scale, ranks, dev)
+    T = x.shape[0]
+    _i32(T, id_begin)
+    x_ptr, ldx = _rows(x, "x", dev, T, K)
+    base_ptr, ld_base = _rows(base, "base", dev, T, N)
+    out_ptr, ld_out = _rows(out, "out", dev, T, N)
+    ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
+    _launch("moe_adapter", dev, stream, x_ptr, ldx, *table, n, T, K, N, R, _ptr(ids, "ids", dev, (T,), _I32), id_begin,
+            _adapter_plan(plan, dev), base_ptr, ld_base, out_ptr, ld_out, _ptr(v, "v", dev, (T, R), _F32), ws_ptr, ws_bytes)
+
+
+def adapter_backward_workspace_bytes(T: int, n: int, K: int, N: int, R: int) -> int:
+    _i32(T, n, K, N, R)
+    return int(load().moe_adapter_backward_workspace_bytes(T, n, K, N, R))
+
+
+def moe_adapter_backward(dout: torch.Tensor, x: Optional[torch.Tensor], v: Optional[torch.Tensor], a: torch.Tensor,
+                         b: torch.Tensor, plan: Optional[Plan], ws: Optional[torch.Tensor],
+                         da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None,
+                         dx: Optional[torch.Tensor] = None, *, dx_base: Optional[torch.Tensor] = None,
+                         scale: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of moe_adapter for rows grouped by ``plan``: da fp32 [n, R, K] and db fp32 [n, N, R], written, not
+    added to, and dx = dx_base (the shared projection's own, or zeros) + the adapters', which may be
+    dx_base itself. v is what moe_adapter kept. ws: a byte tensor of adapter_backward_workspace_bytes(T, n, K, N, R)."""
+    dev = _device(dout, "dout")
+    if dout.dim() != 2:
+        raise ValueError("dout must be [T, N]")
+    (n, K, N, R), table = _adapters(a, b, scale, ranks, dev)
+    T = dout.shape[0]
+    _i32(T)
+    d_ptr, ld_dout = _rows(dout, "dout", dev, T, N)
+    x_ptr, ldx = _rows(x, "x", dev, T, K)
+    base_ptr, ld_base = _rows(dx_base, "dx_base", dev, T, K)
+    dx_ptr, ld_dx = _rows(dx, "dx", dev, T, K)
+    ws_ptr, ws_bytes = _bytes(ws, "ws", dev)
+    _launch("moe_adapter_backward", dev, stream, d_ptr, ld_dout, x_ptr, ldx, _ptr(v, "v", dev, (T, R), _F32), *table, n, T, K, N,
+            R, _adapter_plan(plan, dev), base_ptr, ld_base, dx_ptr, ld_dx, _ptr(da, "da", dev, (n, R, K), _F32),
+            _ptr(db, "db", dev, (n, N, R), _F32), ws_ptr, ws_bytes)
 
 
 def moe_dispatch_quantized(q: torch.Tensor, q_s: torch.Tensor, plan: Plan, pool: torch.Tensor, pool_s: torch.Tensor,

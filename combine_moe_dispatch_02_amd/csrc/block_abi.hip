@@ -49,6 +49,21 @@ static int check_sandwich(const void* post_weight, const void* weight, int32_t w
   return MOE_OK;
 }
 
+// adapters of a call: their table, the rows' grouping, and the pitches of its row arrays (in elements)
+static int check_adapter(const void* a, const void* b, const float* scale, const int32_t* ranks, int32_t n, int32_t T,
+                         int32_t K, int32_t N, int32_t R) {
+  if (!a || !b || n < 1 || n > 1024 || T < 0 || K < 8 || N < 8 || R < 8) return MOE_ERR_INVALID;
+  if (misaligned({a, b}, 16) || misaligned({scale, ranks}, 4)) return MOE_ERR_INVALID;
+  if (K % 8 != 0 || N % 8 != 0 || R % 8 != 0 || K > kMaxWidth || N > kMaxWidth || R > 256) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+static int check_adapter_plan(const moe_plan_t* p, int32_t n, int32_t T) {
+  const int rc = check_plan(p);
+  if (rc != MOE_OK) return rc;
+  return p->T == T && p->K == 1 && p->E_local == n ? MOE_OK : MOE_ERR_INVALID;
+}
+static bool bad_pitch(int32_t ld, int32_t width) { return ld < width || ld % 8 != 0; }
+
 static int check_router(int32_t logits_dtype, int32_t T, int32_t E, int32_t K, const moe_router_config* c) {
   if (!c || T < 0 || E < 1 || E > 1024 || K < 1 || K > 16) return MOE_ERR_INVALID;
   if (logits_dtype != MOE_BF16 && logits_dtype != MOE_F32) return MOE_ERR_INVALID;
@@ -200,6 +215,76 @@ MOE355_API int moe_router_topk_backward(const float* d_topk_weights, const void*
     return MOE_ERR_INVALID;
   return launch_router_topk_backward(d_topk_weights, logits, logits_dtype == MOE_BF16, topk_idx, T, E, K, *cfg,
                                      d_logits, static_cast<hipStream_t>(stream));
+}
+
+MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R) {
+  if (T < 1 || K < 8 || K % 8 != 0 || K > kMaxWidth || R < 8 || R % 8 != 0 || R > 256) return 0;
+  return (size_t)adapter_splits(T, K) * T * R * sizeof(float);
+}
+
+MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void* b, const float* scale,
+                           const int32_t* ranks, int32_t n, int32_t T, int32_t K, int32_t N, int32_t R,
+                           const int32_t* ids, int32_t id_begin, const moe_plan_t* plan, const void* base,
+                           int32_t ld_base, void* out, int32_t ld_out, float* v, void* ws, size_t ws_bytes,
+                           void* stream) {
+  BlockRange trace("moe_adapter");
+  const int rc = check_adapter(a, b, scale, ranks, n, T, K, N, R);
+  if (rc == MOE_ERR_INVALID) return rc;
+  if (T > 0) {
+    if (!x || !out || !ws || (ids == nullptr) == (plan == nullptr) || id_begin < 0) return MOE_ERR_INVALID;
+    if (misaligned({x, base, out, v, ws}, 16) || misaligned({ids}, 4)) return MOE_ERR_INVALID;
+    if (bad_pitch(ldx, K) || bad_pitch(ld_out, N) || (base && bad_pitch(ld_base, N))) return MOE_ERR_INVALID;
+    if (base == out && ld_base != ld_out) return MOE_ERR_INVALID;
+    if (plan && check_adapter_plan(plan, n, T) != MOE_OK) return MOE_ERR_INVALID;
+  }
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  if (ids && T > 64) return MOE_ERR_UNSUPPORTED;
+  if (ws_bytes < moe_adapter_workspace_bytes(T, K, R)) return MOE_ERR_INVALID;
+  return launch_adapter({x, ldx, a, b, scale, ranks, n, T, K, N, R, ids, id_begin, plan, base, ld_base, out, ld_out, v, ws},
+                        static_cast<hipStream_t>(stream));
+}
+
+MOE355_API size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t n, int32_t K, int32_t N, int32_t R) {
+  if (n < 1 || n > 1024 || N < 8 || N % 8 != 0 || N > kMaxWidth || moe_adapter_workspace_bytes(T, K, R) == 0) return 0;
+  return moe_adapter_workspace_bytes(T, N, R) + (size_t)adapter_grad_slots(T) * R * (K + N) * sizeof(float);
+}
+
+MOE355_API int moe_adapter_backward(const void* dout, int32_t ld_dout, const void* x, int32_t ldx, const float* v,
+                                    const void* a, const void* b, const float* scale, const int32_t* ranks, int32_t n,
+                                    int32_t T, int32_t K, int32_t N, int32_t R, const moe_plan_t* plan,
+                                    const void* dx_base, int32_t ld_base, void* dx, int32_t ld_dx, float* da, float* db,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  BlockRange trace("moe_adapter_backward");
+  const int rc = check_adapter(a, b, scale, ranks, n, T, K, N, R);
+  if (rc == MOE_ERR_INVALID) return rc;
+  if (misaligned({da, db}, 16)) return MOE_ERR_INVALID;
+  if (T > 0) {
+    if (!dout || !ws || (!dx && !da && !db)) return MOE_ERR_INVALID;
+    if ((da && !x) || (db && !v)) return MOE_ERR_INVALID;
+    if (misaligned({dout, x, v, dx_base, dx, ws}, 16)) return MOE_ERR_INVALID;
+    if (bad_pitch(ld_dout, N) || (da && bad_pitch(ldx, K)) || (dx && bad_pitch(ld_dx, K))) return MOE_ERR_INVALID;
+    if (dx_base && (!dx || bad_pitch(ld_base, K) || (dx_base == dx && ld_base != ld_dx))) return MOE_ERR_INVALID;
+    if (check_adapter_plan(plan, n, T) != MOE_OK) return MOE_ERR_INVALID;
+  }
+  if (rc != MOE_OK) return rc;
+  if (T > 0 && ws_bytes < moe_adapter_backward_workspace_bytes(T, n, K, N, R)) return MOE_ERR_INVALID;
+  AdapterLaunch l{};
+  l.x = x;
+  l.ldx = ldx;
+  l.a = a;
+  l.b = b;
+  l.scale = scale;
+  l.ranks = ranks;
+  l.n = n;
+  l.T = T;
+  l.K = K;
+  l.N = N;
+  l.R = R;
+  l.plan = plan;
+  l.v = const_cast<float*>(v);
+  l.ws = ws;
+  return launch_adapter_backward(l, {dout, ld_dout, dx_base, ld_base, dx, ld_dx, da, db}, static_cast<hipStream_t>(stream));
 }
 
 MOE355_API int moe_dispatch_quantized(const void* q, const void* q_s, int32_t H, int32_t act_dtype,

@@ -192,4 +192,38 @@ struct SandwichBwdLaunch {
 int32_t sandwich_backward_blocks(int32_t T, int32_t H);
 int launch_sandwich_norm_backward(const SandwichBwdLaunch& l, hipStream_t stream);
 
+// adapter.hip
+struct AdapterLaunch {
+  const void* x;
+  int64_t ldx;
+  const void* a;
+  const void* b;
+  const float* scale;
+  const int32_t* ranks;
+  int32_t n, T, K, N, R;
+  const int32_t* ids;       // or plan
+  int32_t begin;
+  const moe_plan_t* plan;
+  const void* base;
+  int64_t ld_base;
+  void* out;
+  int64_t ld_out;
+  float* v;
+  void* ws;
+};
+struct AdapterGrads {
+  const void* dout;
+  int64_t ld_dout;
+  const void* dx_base;
+  int64_t ld_base;
+  void* dx;
+  int64_t ld_dx;
+  float* da;
+  float* db;
+};
+int32_t adapter_splits(int32_t T, int32_t K);   // partial results of v (K: the contraction's length)
+int32_t adapter_grad_slots(int32_t T);          // partial results of dA and dB
+int launch_adapter(const AdapterLaunch& l, hipStream_t stream);
+int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream);
+
 }  // namespace moe

@@ -213,6 +213,62 @@ MOE355_API int moe_router_topk_backward(const float* d_topk_weights, const void*
                                         const int32_t* topk_idx, int32_t T, int32_t E, int32_t K,
                                         const moe_router_config* cfg, void* d_logits, void* stream);
 
+/* Bytes of moe_adapter's workspace (0 for invalid sizes or T = 0). */
+MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R);
+
+/*
+ * Low-rank adapters of many requests at once, beside a projection that all of them share:
+ *   v[t]   = A[e] x[t]                                  fp32 sums, kept in fp32
+ *   out[t] = bf16(base[t] + scale[e] * (B[e] v[t]))     fp32
+ * with e the adapter of row t; a row without one has out[t] = base[t] (base null: zeros for both). base is what the
+ * shared projection made of x. a: bf16 [n][R][K], b: bf16 [n][N][R], scale: fp32 [n] or null
+ * (ones), ranks: int32 [n] or null: adapter e has the first ranks[e] rows of a[e] and columns
+ * of b[e] (taken into [0, R]), the others are not looked at and may hold anything.
+ * x: bf16 [T][K], base and out: bf16 [T][N], with row pitches ldx, ld_base, ld_out in elements
+ * (multiples of 8), so that they may be columns of wider arrays. out may be base (same
+ * pitch): rows without an adapter then stay as they are.
+ * The rows' adapters: either ids, int32 [T], e = ids[t] - id_begin, for up to 64 rows; or plan,
+ * made by moe_plan with K = 1 from such ids ([T][1]), E_local = n and expert_begin in
+ * id_begin's place, for any number: one plan serves all projections of a batch. Of
+ * its tile only the speed depends: 16 where adapters have few rows each, else 32 or more. Ids
+ * outside [0, n) are rows without an adapter.
+ * v: fp32 [T][R] or null: receives v of rows with an adapter (0 past its rank), for
+ * moe_adapter_backward. ws: the workspace.
+ * Products are exact and summed in fp32, in an order that sizes, and the plan or the ids, fix; v
+ * enters the second product as a sum of two bf16 numbers (off by 2^-18 at most).
+ * Errors: MOE_ERR_INVALID (null or misaligned pointers, n not in [1,1024], T < 0, K, N or R <
+ * 8, pitches below the width or no multiples of 8, both or neither of ids and plan, id_begin <
+ * 0, a plan of other sizes, small workspace), MOE_ERR_UNSUPPORTED (K, N or R no multiple of 8,
+ * K or N > 32768, R > 256, ids with T > 64, more than 2^24 - 1 workgroups).
+ */
+MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void* b, const float* scale,
+                           const int32_t* ranks, int32_t n, int32_t T, int32_t K, int32_t N, int32_t R,
+                           const int32_t* ids, int32_t id_begin, const moe_plan_t* plan, const void* base,
+                           int32_t ld_base, void* out, int32_t ld_out, float* v, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Bytes of moe_adapter_backward's workspace (0 for invalid sizes or T = 0). */
+MOE355_API size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t n, int32_t K, int32_t N, int32_t R);
+
+/*
+ * Backward of moe_adapter, of rows grouped by a plan:
+ *   dv[t] = scale[e] * (B[e]^T dout[t]),  dx[t] = bf16(dx_base[t] + A[e]^T dv[t])
+ *   da[e] = sum over the adapter's rows of dv[t] x[t]^T          fp32 [n][R][K]
+ *   db[e] = scale[e] * sum over its rows of dout[t] v[t]^T       fp32 [n][N][R]
+ * dout: bf16 [T][N], the gradient of out (and, as it is, of base); v as moe_adapter wrote it;
+ * dx_base: the shared projection's own dx, or null (zeros); dx may be dx_base (same pitch; rows
+ * without an adapter then stay as they are). dx, da and db may each be null, not all; x is needed
+ * for da, v for db. da and db are written, not added to, zeros past an adapter's rank and for
+ * adapters without rows; with T = 0 (plan null) they are zero-filled. Sums run in orders that sizes and
+ * plan fix. ids, ranks, scale and pitches as in moe_adapter.
+ * Errors: those of moe_adapter.
+ */
+MOE355_API int moe_adapter_backward(const void* dout, int32_t ld_dout, const void* x, int32_t ldx, const float* v,
+                                    const void* a, const void* b, const float* scale, const int32_t* ranks, int32_t n,
+                                    int32_t T, int32_t K, int32_t N, int32_t R, const moe_plan_t* plan,
+                                    const void* dx_base, int32_t ld_base, void* dx, int32_t ld_dx, float* da, float* db,
+                                    void* ws, size_t ws_bytes, void* stream);
+
 /*
  * moe_dispatch for rows that are quantised already: pool[pos[t,k]] = q[t] with its scale
  * words, moved to their tile-major places. Epoch, workspace, pool_rows, what is left alone and
