@@ -324,8 +324,8 @@ def _rows(t: Optional[torch.Tensor], name: str, dev: int, T: int, width: int):
 
 
 def adapter_tile(T: int, n: int) -> int:
-    """The tile of a plan that groups T rows by n adapters: 16 where they have few rows each, else 32."""
-    return 16 if T < 32 * n else 32
+    """The tile of a plan that groups T rows by n adapters: 16, 32 or 128 by how many rows they have each."""
+    return 16 if T < 32 * n else 32 if T < 256 * n else 128
 
 
 def adapter_workspace_bytes(T: int, K: int, R: int) -> int:

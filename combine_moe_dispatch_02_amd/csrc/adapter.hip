@@ -34,10 +34,12 @@ __device__ inline f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amd
 
 // A 16 x 32 operand out of a row-major LDS tile whose rows are the contraction: lane l receives column l % 16
 // (columns in fours, the lanes' own addresses choose which), rows 8 (l / 16) .. + 8. Each lane passes the address
-// of row 8 (l / 16) + (l % 16) / 4, four columns l % 4; `pitch4` is four rows in bytes.
-__device__ inline bf16x8 read_transposed(const uint8_t* at, uint32_t pitch4) {
-  const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)at);
-  const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(at + pitch4));
+// of row 8 (l / 16) + (l % 16) / 4, four columns l % 4, in bytes of the tile; `pitch4` is four rows.
+// The offset is one number: through a longer chain of sums the compiler loses whose LDS it is, and waits for every
+// load in flight.
+__device__ inline bf16x8 read_transposed(const uint8_t* tile, uint32_t at, uint32_t pitch4) {
+  const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(tile + at));
+  const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(tile + at + pitch4));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -55,7 +57,6 @@ __device__ inline void split(float v, __bf16 (&o)[P]) {
 struct RowArgs {
   const int32_t* src;          // plan
   const int32_t* tile_expert;
-  const int32_t* num_tiles;
   const int32_t* pos;
   int32_t tile_shift;
   const int32_t* ids;          // or the rows' ids (at most 64), less `begin`
@@ -70,17 +71,14 @@ template <int MB>
 __device__ inline bool block_rows(const RowArgs& r, int mb, int& e, int* rows) {
   const int tid = threadIdx.x;
   if (!r.ids) {
-    const int tile = (int)(((int64_t)mb * MB) >> r.tile_shift);
-    if (tile >= r.num_tiles[0]) return false;
-    e = r.tile_expert[tile];
-    const int32_t* src = r.src + (int64_t)mb * MB;
-    if ((uint32_t)e >= (uint32_t)r.n || src[0] < 0) return false;   // a tile's rows come first, its padding behind
-    if (tid < MB) {
-      const int t = src[tid];
-      rows[tid] = (uint32_t)t < (uint32_t)r.T ? t : -1;
-    }
+    // tiles past the last have no expert, src ends with its padding: both are loaded at once
+    const int64_t at = (int64_t)mb * MB;
+    e = r.tile_expert[at >> r.tile_shift];
+    const int t = tid < MB ? r.src[at + tid] : -1;
+    if ((uint32_t)e >= (uint32_t)r.n) return false;
+    if (tid < MB) rows[tid] = (uint32_t)t < (uint32_t)r.T ? t : -1;
     __syncthreads();
-    return true;
+    return rows[0] >= 0;                         // a tile's rows come first, its padding behind
   }
   // every wave for itself: a lane a row, the rows of one adapter one group, groups in order of their first rows
   const int lane = lane_id();
@@ -118,140 +116,217 @@ struct DownArgs {
   const float* scale;      // of the result, or null
   const int32_t* ranks;
   int32_t K, R;
+  int32_t blocks;          // blocks of rows
   int32_t splits;          // slices of K, whole groups of chunks each
   float* part;             // [splits][T][R]
 };
 
-constexpr int kChunk = 64;       // k of a wave's step: a 128-byte line of a row of z
-constexpr int kDownWaves = 4;
+// Both operands come by LDS-DMA, so that every load is of whole 128-byte lines (straight into MFMA registers a load
+// would touch 16 rows, 64 bytes of each, and a CU gets 10 bytes a clock that way). A stage is kc columns of the
+// block's rows and of m; three stages, two of them in flight while one is multiplied, its steps of 32 columns by a wave
+// each. In a stage, 16-byte pieces are permuted within their rows so that fragments are read without bank conflicts;
+// the DMA writes lane after lane, so the permutation is in the source addresses.
+constexpr int kDownWaves = 8;
+constexpr int down_kc(int mb, int rf) { return mb > 32 || rf > 4 ? 128 : 256; }
+
+__device__ u32x4 adapter_zeros[1];              // never written: what is loaded for columns and rows that are not there
+
+typedef const __attribute__((address_space(1))) void* global_ptr;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// 16 bytes a lane from anywhere to LDS, lane after lane from `to` on. (The host's pass, which has no use for it, refuses 16.)
+__device__ inline void load_to_lds(const void* from, void* to) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
+#endif
+}
+__device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t at, void* to) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_ptr)to, 16, at, 0, 0, 0);
+#endif
+}
+
+// A barrier behind which the wave's LDS reads are done, and all but its last N loads to LDS. (A __syncthreads
+// would wait for all of them.)
+template <int N>
+__device__ inline void stage_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(vmcnt_enc(N) & kLgkm0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// permutation of the 16-byte pieces of row k of transposed m, RP / 8 of them: the rows that a transposing read
+// touches at once (4 neighbours of two groups of 8) land on distinct banks
+template <int RP>
+__device__ inline int piece_swz(int k) {
+  if constexpr (RP == 32) return ((k >> 3) & 1) << 1;
+  if constexpr (RP == 64) return (((k >> 1) & 1) | (((k >> 3) & 1) << 1)) << 1;
+  if constexpr (RP == 128) return ((k & 3) | (((k >> 3) & 1) << 2)) << 1;
+  return 0;
+}
 
 template <int MB, int RF, bool TRANS>
 __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(DownArgs a) {
-  constexpr int MF = MB / 16;
-  constexpr int RP = RF * 16;
-  constexpr int PITCH = RP * 2 + 16;         // bytes of a row of k in LDS (TRANS)
-  constexpr int LOADS = RP / 8;              // 16-byte pieces of a chunk of m for each lane (TRANS)
-  constexpr int SUMS = (kDownWaves - 1) * MB * RP * 4;
-  constexpr int TILES = TRANS ? kDownWaves * kChunk * PITCH : 16;
-  __shared__ __attribute__((aligned(16))) uint8_t s_mem[SUMS > TILES ? SUMS : TILES];
+  constexpr int MF = MB / 16, RP = RF * 16, KC = down_kc(MB, RF), PIECES = KC / 8;
+  constexpr int KS = KC / 32;                    // steps of a stage
+  // Few rows: a wave has a step of the stage (two waves half the rows, or half the ranks, of one), and the waves' sums
+  // are added at the end. Many: a wave has rows and ranks of its own, and all steps.
+  constexpr int KG = MB > 32 ? 1 : KS;           // waves among which the steps are dealt
+  constexpr int JW = kDownWaves / KG;            // waves that share a step
+  constexpr int IW = JW == 8 ? (RF > 1 ? 4 : 8) : MF % JW == 0 ? JW : 1;     // of them by rows
+  constexpr int MW = MF / IW, RW = RF / (JW / IW);                           // fragments of z and of m of a wave
+  constexpr int ZB = MB * KC * 2 / 1024, MBK = RP * KC * 2 / 1024;   // DMA blocks of 1 KiB
+  constexpr int ZN = (ZB + kDownWaves - 1) / kDownWaves, MN = (MBK + kDownWaves - 1) / kDownWaves;
+  constexpr int STAGE = (MB + RP) * KC * 2;
+  constexpr int JG = RW < 4 ? RW : 4;            // fragments that are summed over the waves at a time
+  // every wave has the same number of loads; with fewer blocks than waves some load the same
+  static_assert((ZB % kDownWaves == 0 || kDownWaves % ZB == 0) && (MBK % kDownWaves == 0 || kDownWaves % MBK == 0));
+  static_assert(KG == 1 || kDownWaves / 2 * MW * JG * 1024 <= STAGE, "sums fit a stage");
+  __shared__ __attribute__((aligned(16))) uint8_t s_t0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t2[STAGE];
   __shared__ int s_rows[MB];
   const int slice = blockIdx.x % (uint32_t)a.splits;
+  // one slice: neighbouring blocks, which mostly share an adapter, on one XCD
+  const int block = a.splits > 1 ? blockIdx.x / (uint32_t)a.splits : (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   int e;
-  if (!block_rows<MB>(a.rows, blockIdx.x / (uint32_t)a.splits, e, s_rows)) return;
+  if (block >= a.blocks || !block_rows<MB>(a.rows, block, e, s_rows)) return;
+  e = __builtin_amdgcn_readfirstlane(e);
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, lhi = lane >> 4;
   const int r0 = blockIdx.y * RP;
   const int rank = adapter_rank(a.ranks, e, a.R) - r0;       // ranks from r0 on
-  const int nrf = rank <= 0 ? 0 : min(RF, (rank + 15) / 16);
   const int K = a.K;
-  const int chunks = (K + kChunk - 1) / kChunk;
+  const int chunks = rank > 0 ? (K + KC - 1) / KC : 0;
   const int per = (chunks + a.splits - 1) / a.splits;
-  const int c1 = min(chunks, (slice + 1) * per);
-  const uint16_t* mb = a.m + (int64_t)e * a.R * K;
-  const __amdgpu_buffer_rsrc_t mr = make_rsrc(mb, (uint32_t)a.R * (uint32_t)K * 2u);
-  const uint16_t* zp[MF];
+  const int c0 = slice * per, c1 = min(chunks, c0 + per), n = c1 - c0, k1 = min(K, c1 * KC);
+  const __amdgpu_buffer_rsrc_t mr = make_rsrc(a.m + (int64_t)e * a.R * K, (uint32_t)a.R * (uint32_t)K * 2u);
+  // this lane's piece of each of its wave's blocks: of z a pointer to its row and the column, of m an offset
+  const uint16_t* zrow[ZN];
+  int zcol[ZN], zend[ZN], mcol[MN];
+  uint32_t moff[MN];
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int t = s_rows[i * 16 + l16];
-    zp[i] = a.z + (int64_t)(t < 0 ? max(s_rows[0], 0) : t) * a.ldz;   // rows that are not there: any, not written
+  for (int i = 0; i < ZN; ++i) {
+    const int at = (wave + i * kDownWaves) % ZB * 64 + lane, row = at / PIECES;
+    const int t = s_rows[row];
+    zcol[i] = ((at % PIECES) ^ (row & 15)) * 8;
+    zrow[i] = a.z + max(t, 0) * a.ldz;
+    zend[i] = t < 0 ? 0 : k1 - zcol[i];          // stages that begin before have the column
   }
-  f32x4 acc[MF][RF];
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int j = 0; j < RF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint8_t* tile = s_mem + (TRANS ? wave * kChunk * PITCH : 0);
-
-  u32x4 zv[2][MF];
-  u32x4 mv[TRANS ? LOADS : 2 * RF];
-  const auto load = [&](int c) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int k = c * kChunk + s * 32 + lhi * 8;
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        zv[s][i] = *reinterpret_cast<const u32x4*>(zp[i] + min(k, K - 8));
-        if (k >= K) zv[s][i] = u32x4{0u, 0u, 0u, 0u};
-      }
-    }
+  for (int i = 0; i < MN; ++i) {
+    const int at = (wave + i * kDownWaves) % MBK * 64 + lane;
     if constexpr (TRANS) {
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int at = lane + i * 64, row = c * kChunk + at / (RP / 8), col = (at % (RP / 8)) * 8;
-        mv[i] = buf_load16(mr, row < K && col < rank ? ((uint32_t)row * (uint32_t)a.R + (uint32_t)(r0 + col)) * 2u : kOutside);
-      }
+      const int k = at / (RP / 8), col = ((at % (RP / 8)) ^ piece_swz<RP>(k)) * 8;
+      mcol[i] = col < rank ? k : K;
+      moff[i] = ((uint32_t)k * (uint32_t)a.R + (uint32_t)(r0 + col)) * 2u;
     } else {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int k = c * kChunk + s * 32 + lhi * 8;
-#pragma unroll
-        for (int j = 0; j < RF; ++j)
-          if (j < nrf) {
-            const int r = j * 16 + l16;
-            mv[s * RF + j] = buf_load16(mr, k < K && r < rank ? ((uint32_t)(r0 + r) * (uint32_t)K + (uint32_t)k) * 2u : kOutside);
-          }
-      }
+      const int r = at / PIECES;
+      mcol[i] = r < rank ? ((at % PIECES) ^ (r & 15)) * 8 : K;
+      moff[i] = ((uint32_t)(r0 + r) * (uint32_t)K + (uint32_t)mcol[i]) * 2u;
     }
+  }
+  const auto dma = [&](int c, uint8_t* stage) {
+    const int k0 = (c0 + c) * KC;
+#pragma unroll
+    for (int i = 0; i < ZN; ++i) {
+      const uint64_t there = reinterpret_cast<uint64_t>(zrow[i] + k0 + zcol[i]), none = reinterpret_cast<uint64_t>(adapter_zeros);
+      load_to_lds(reinterpret_cast<const void*>(k0 < zend[i] ? there : none), stage + (wave + i * kDownWaves) % ZB * 1024);
+    }
+    const uint32_t step = (uint32_t)k0 * (TRANS ? (uint32_t)a.R : 1u) * 2u;
+#pragma unroll
+    for (int i = 0; i < MN; ++i)
+      load_to_lds(mr, k0 + mcol[i] < k1 ? moff[i] + step : kOutside, stage + MB * KC * 2 + (wave + i * kDownWaves) % MBK * 1024);
   };
-  int c = slice * per + wave;
-  if (nrf > 0 && c < c1) load(c);
-  if (nrf > 0)
-    for (; c < c1; c += kDownWaves) {
-      bf16x8 zf[2][MF], mf[2][RF];
+  f32x4 acc[MW][RW];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+  for (int i = 0; i < MW; ++i)
 #pragma unroll
-        for (int i = 0; i < MF; ++i) zf[s][i] = __builtin_bit_cast(bf16x8, zv[s][i]);
-      if constexpr (TRANS) {
+    for (int j = 0; j < RW; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int kg = wave % KG, i0 = wave / KG % IW * MW, j0 = wave / KG / IW * RW;
+  // where m begins in a stage: not to be known, else the compiler sees that reads of m miss the stage's first load, which
+  // it takes for all of them, and waits for every load in flight
+  int m_at = MB * KC * 2;
+  asm volatile("" : "+s"(m_at));
+  const auto step = [&](int c, const uint8_t* cur, uint8_t* next) {
+    dma(c + 2, next);      // the stage that everybody was done with at the last barrier
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-          const int at = lane + i * 64;
-          *reinterpret_cast<u32x4*>(tile + (at / (RP / 8)) * PITCH + (at % (RP / 8)) * 16) = mv[i];
+    for (int q = 0; q < KS / KG; ++q) {
+      const int ks = KG == 1 ? q : kg;
+      bf16x8 zf[MW];
+#pragma unroll
+      for (int i = 0; i < MW; ++i)
+        zf[i] = *reinterpret_cast<const bf16x8*>(cur + (((i0 + i) * 16 + l16) * (KC * 2) + (((ks * 4 + lhi) ^ l16) << 4)));
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        bf16x8 mf;
+        if constexpr (TRANS) {
+          const int k = ks * 32 + 8 * lhi + (l16 >> 2);      // + 4 has the same permutation
+          const int piece = ((j0 + j) * 2 + ((l16 >> 1) & 1)) ^ piece_swz<RP>(k);
+          mf = read_transposed(cur, m_at + k * (RP * 2) + piece * 16 + (l16 & 1) * 8, 4 * RP * 2);
+        } else {
+          mf = *reinterpret_cast<const bf16x8*>(cur + (m_at + ((j0 + j) * 16 + l16) * (KC * 2) + (((ks * 4 + lhi) ^ l16) << 4)));
         }
-        wave_sync();
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int j = 0; j < RF; ++j)
-            mf[s][j] = read_transposed(tile + (s * 32 + 8 * lhi + (l16 >> 2)) * PITCH + j * 32 + (l16 & 3) * 8, 4 * PITCH);
-        wave_sync();
-      } else {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int j = 0; j < RF; ++j) mf[s][j] = __builtin_bit_cast(bf16x8, mv[s * RF + j]);
+        for (int i = 0; i < MW; ++i) acc[i][j] = mfma(mf, zf[i], acc[i][j]);
       }
-      if (c + kDownWaves < c1) load(c + kDownWaves);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < RF; ++j)
-          if (j < nrf)
-#pragma unroll
-            for (int i = 0; i < MF; ++i) acc[i][j] = mfma(mf[s][j], zf[s][i], acc[i][j]);
     }
-  // the waves' sums, in order; lane (l16, lhi) has row l16 and four ranks 4 lhi .. of each fragment
-  __syncthreads();
-  float* sums = reinterpret_cast<float*>(s_mem);
-  if (wave > 0)
+    // this wave's loads of stage c + 1 have landed (those of c + 2 are behind them), then everybody's. Stages past the
+    // last are loaded as zeros, without traffic, so that the counts hold.
+    stage_barrier<ZN + MN>();
+  };
+  if (n > 0) {
+    dma(0, s_t0);
+    dma(1, s_t1);
+    stage_barrier<ZN + MN>();
+    int c = 0;
+    for (; c + 3 <= n; c += 3) {
+      step(c, s_t0, s_t2);
+      step(c + 1, s_t1, s_t0);
+      step(c + 2, s_t2, s_t1);
+    }
+    if (c < n) step(c, s_t0, s_t2);
+    if (c + 1 < n) step(c + 1, s_t1, s_t0);
+    wait_vm0();
+  }
+  // Lane (l16, lhi) has row l16 and four ranks 4 lhi .. of each fragment. The waves' sums of a step each are halved until
+  // one wave has them.
+  if constexpr (KG > 1) {
+    float* sums = reinterpret_cast<float*>(s_t0);
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
+    for (int g = 0; g < RW; g += JG)
 #pragma unroll
-      for (int j = 0; j < RF; ++j)
-        *reinterpret_cast<f32x4*>(sums + (((wave - 1) * MF + i) * RF + j) * 256 + lane * 4) = acc[i][j];
-  __syncthreads();
-  if (wave > 0) return;
+      for (int half = KG / 2; half > 0; half /= 2) {
+        __syncthreads();
+        const int at = wave / KG * half;
+        if (kg >= half && kg < 2 * half)
+#pragma unroll
+          for (int i = 0; i < MW; ++i)
+#pragma unroll
+            for (int j = 0; j < JG; ++j)
+              *reinterpret_cast<f32x4*>(sums + (((at + kg - half) * MW + i) * JG + j) * 256 + lane * 4) = acc[i][g + j];
+        __syncthreads();
+        if (kg < half)
+#pragma unroll
+          for (int i = 0; i < MW; ++i)
+#pragma unroll
+            for (int j = 0; j < JG; ++j)
+              acc[i][g + j] += *reinterpret_cast<const f32x4*>(sums + (((at + kg) * MW + i) * JG + j) * 256 + lane * 4);
+      }
+    if (kg > 0) return;
+  }
   const float f = a.scale ? a.scale[e] : 1.f;
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
-    const int t = s_rows[i * 16 + l16];
+  for (int i = 0; i < MW; ++i) {
+    const int t = s_rows[(i0 + i) * 16 + l16];
 #pragma unroll
-    for (int j = 0; j < RF; ++j) {
+    for (int j = 0; j < RW; ++j) {
       f32x4 v = acc[i][j];
-#pragma unroll
-      for (int w = 0; w < kDownWaves - 1; ++w) v += *reinterpret_cast<const f32x4*>(sums + ((w * MF + i) * RF + j) * 256 + lane * 4);
-      const int r = j * 16 + lhi * 4;
+      const int r = (j0 + j) * 16 + lhi * 4;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = r + q < rank ? v[q] * f : 0.f;
       if (t >= 0 && r0 + r < a.R)
@@ -266,8 +341,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(DownArgs 
 // ---------------------------------------------------------------------------------------
 struct UpArgs {
   RowArgs rows;
-  const float* part;
+  const float* part;       // u as partial results,
   int32_t splits;
+  const uint16_t* parts;   // or (not null) as two bf16 numbers: the first [T][R], the second behind them
   const uint16_t* m;
   const float* scale;
   const int32_t* ranks;
@@ -278,20 +354,30 @@ struct UpArgs {
   int64_t ld_out;
   float* u_out;            // the sums themselves, where there are several partial results, or null
   int32_t blocks;          // blocks of rows; workgroups behind them copy rows without an adapter
-  int32_t slab;            // columns of a workgroup, a multiple of 128
+  int32_t slab;            // columns of a workgroup, a multiple of 256
 };
 
-constexpr int kUpWaves = 4;
 constexpr int kCopyRows = 64;
+constexpr int kUpWaves = 4;
 
-template <int MB, bool TRANS>
+// A wave makes CW columns of the block's rows, 32 rows at a time, in LDS of its own: m goes there as whole lines come,
+// then the sums, from where base and out are read and written in whole lines too. The next rows of base are in
+// flight meanwhile, and the next columns of m, the first ones while u is summed. RS: steps of 32 ranks that u has at most.
+template <int MB, int RS, bool TRANS>
 __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
-  constexpr int MF = MB / 16;
-  constexpr int MAXR = 256;
-  constexpr int UP = MAXR * 2 + 16;            // bytes of a row of u in LDS
-  constexpr int AP = 64 + 16;                  // bytes of a row of 32 columns of m in LDS (TRANS)
+  constexpr int NW = kUpWaves;
+  constexpr int RB = MB < 32 ? MB : 32, MF = RB / 16;    // rows at a time
+  constexpr int CW = RS > 4 ? 32 : 64, CF = CW / 16;
+  constexpr int UP = RS * 64 + 16;                       // bytes of a row of u in LDS,
+  constexpr int MP = (TRANS ? CW * 2 : RS * 64) + 16;    // of m (TRANS: a rank's columns, else a column's ranks),
+  constexpr int DP = CW * 4 + 16;                        // and of the sums
+  constexpr int MROWS = TRANS ? RS * 32 : CW, MPIECES = TRANS ? CW / 8 : RS * 4;
+  constexpr int MN = MROWS * MPIECES / 64;               // 16-byte pieces of m for each lane
+  constexpr int LPR = CW / 8, RPL = 64 / LPR;            // lanes that share a row of base and out, rows of a load
+  constexpr int BN = RB / RPL;                           // pieces of base for each lane
+  constexpr int TILE = MROWS * MP > RB * DP ? MROWS * MP : RB * DP;
   __shared__ __attribute__((aligned(16))) uint8_t s_u[2][MB * UP];
-  __shared__ __attribute__((aligned(16))) uint8_t s_m[TRANS ? kUpWaves * 32 * AP : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_tile[NW][TILE];
   __shared__ int s_rows[MB];
   const int tid = threadIdx.x;
   const int lane = lane_id();
@@ -301,7 +387,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
   const int n0 = slab * a.slab, n1 = min(a.N, n0 + a.slab);
   if (block >= a.blocks) {                     // rows without an adapter
     const int t0 = (block - a.blocks) * kCopyRows;
-    for (int t = t0 + wave; t < min(a.rows.T, t0 + kCopyRows); t += kUpWaves) {
+    for (int t = t0 + wave; t < min(a.rows.T, t0 + kCopyRows); t += NW) {
       const bool has = a.rows.ids ? (uint32_t)(a.rows.ids[t] - a.rows.begin) < (uint32_t)a.rows.n : a.rows.pos[t] >= 0;
       if (has) continue;
       for (int c = n0 + lane * 8; c < n1; c += 512)
@@ -312,109 +398,148 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
   }
   int e;
   if (!block_rows<MB>(a.rows, block, e, s_rows)) return;
+  e = __builtin_amdgcn_readfirstlane(e);
   const int l16 = lane & 15, lhi = lane >> 4;
   const int R = a.R, rank = adapter_rank(a.ranks, e, R);
   const int steps = (rank + 31) / 32;
-  // u: partial results added in order, as two bf16 numbers each
-  for (int at = tid; at < MB * steps * 8; at += 64 * kUpWaves) {
-    const int row = at / (steps * 8), r = (at % (steps * 8)) * 4, t = s_rows[row];
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (t >= 0 && r < R) {
-      const float* p = a.part + (int64_t)t * R + r;
-      v = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll 4
-      for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + (int64_t)s * a.rows.T * R);
-      if (a.u_out && slab == 0) *reinterpret_cast<f32x4*>(a.u_out + (int64_t)t * R + r) = v;
-    }
-    bf16x4 hi, lo;
+  const __amdgpu_buffer_rsrc_t mr = make_rsrc(a.m + (int64_t)e * a.N * R, (uint32_t)R * (uint32_t)a.N * 2u);
+  const int brow = lane / LPR, bcol = lane % LPR * 8;      // this lane's row and 8 columns of base and out
+
+  u32x4 mv[MN], b[BN];
+  const auto load_m = [&](int c0) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      __bf16 b[2];
-      split<2>(v[q], b);
-      hi[q] = b[0];
-      lo[q] = b[1];
+    for (int i = 0; i < MN; ++i) {
+      const int at = lane + i * 64, row = at / MPIECES, piece = at % MPIECES;
+      const int r = TRANS ? row : piece * 8, col = c0 + (TRANS ? piece * 8 : row);
+      const uint32_t off = TRANS ? (uint32_t)r * (uint32_t)a.N + (uint32_t)col : (uint32_t)col * (uint32_t)R + (uint32_t)r;
+      mv[i] = buf_load16(mr, r < rank && col < a.N ? off * 2u : kOutside);
     }
-    *reinterpret_cast<bf16x4*>(&s_u[0][row * UP + r * 2]) = hi;
-    *reinterpret_cast<bf16x4*>(&s_u[1][row * UP + r * 2]) = lo;
+  };
+  const auto load_base = [&](int c0, int rb) {
+#pragma unroll
+    for (int i = 0; i < BN; ++i) {
+      const uint16_t* p = a.base + max(s_rows[rb + i * RPL + brow], 0) * a.ld_base + min(c0 + bcol, a.N - 8);
+      b[i] = a.base ? *reinterpret_cast<const u32x4*>(p) : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  int c0 = n0 + wave * CW;
+  if (c0 < n1) {
+    load_m(c0);
+    load_base(c0, 0);
   }
-  // ranks past the adapter's own are zeros in u's sums as well
-  if (a.u_out && slab == 0)
-    for (int at = tid; at < MB * (R / 4); at += 64 * kUpWaves) {
-      const int row = at / (R / 4), r = (at % (R / 4)) * 4, t = s_rows[row];
-      if (t >= 0 && r >= steps * 32) *reinterpret_cast<f32x4*>(a.u_out + (int64_t)t * R + r) = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // u as two bf16 numbers each: as they are, or of partial results added in order
+  if (a.parts) {
+    for (int at = tid; at < MB * RS * 4; at += 64 * NW) {
+      const int row = at / (RS * 4), r = (at % (RS * 4)) * 8, t = s_rows[row];
+      u32x4 v[2] = {};
+      if (t >= 0 && r < R) {
+        const uint16_t* p = a.parts + (int64_t)t * R + r;
+        v[0] = *reinterpret_cast<const u32x4*>(p);
+        v[1] = *reinterpret_cast<const u32x4*>(p + (int64_t)a.rows.T * R);
+      }
+      *reinterpret_cast<u32x4*>(&s_u[0][row * UP + r * 2]) = v[0];
+      *reinterpret_cast<u32x4*>(&s_u[1][row * UP + r * 2]) = v[1];
     }
+  } else {
+    for (int at = tid; at < MB * RS * 8; at += 64 * NW) {
+      const int row = at / (RS * 8), r = (at % (RS * 8)) * 4, t = s_rows[row];
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      if (t >= 0 && r < R) {
+        const float* p = a.part + (int64_t)t * R + r;
+        v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll 8
+        for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(p + (int64_t)s * a.rows.T * R);
+        if (a.u_out && slab == 0) *reinterpret_cast<f32x4*>(a.u_out + (int64_t)t * R + r) = v;
+      }
+      bf16x4 hi, lo;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        __bf16 o[2];
+        split<2>(v[q], o);
+        hi[q] = o[0];
+        lo[q] = o[1];
+      }
+      *reinterpret_cast<bf16x4*>(&s_u[0][row * UP + r * 2]) = hi;
+      *reinterpret_cast<bf16x4*>(&s_u[1][row * UP + r * 2]) = lo;
+    }
+  }
   __syncthreads();
   const float f = a.scale ? a.scale[e] : 1.f;
-  const uint16_t* mb = a.m + (int64_t)e * a.N * R;
-  const __amdgpu_buffer_rsrc_t mr = make_rsrc(mb, (TRANS ? (uint32_t)rank : (uint32_t)R) * (uint32_t)a.N * 2u);
-  uint8_t* tile = s_m + (TRANS ? wave * 32 * AP : 0);
-  int tok[MF];
+  uint8_t* tile = s_tile[wave];
+  for (; c0 < n1; c0 += CW * NW) {
 #pragma unroll
-  for (int i = 0; i < MF; ++i) tok[i] = s_rows[i * 16 + l16];
-  for (int c0 = n0 + wave * 32; c0 < n1; c0 += 32 * kUpWaves) {
-    const int c = c0 + lhi * 8;                // this lane's 8 columns of the result
-    u32x4 b[MF];
+    for (int i = 0; i < MN; ++i) {
+      const int at = lane + i * 64, row = at / MPIECES, piece = at % MPIECES;
+      u32x4 v = mv[i];
+      if (!TRANS && (rank & 7)) {      // columns past the adapter's rank hold anything
+        const int left = rank - piece * 8;
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      b[i] = u32x4{0u, 0u, 0u, 0u};
-      if (a.base && tok[i] >= 0 && c < n1) b[i] = *reinterpret_cast<const u32x4*>(a.base + tok[i] * a.ld_base + c);
+        for (int q = 0; q < 4; ++q) v[q] = left >= 2 * q + 2 ? v[q] : left == 2 * q + 1 ? v[q] & 0xffffu : 0u;
+      }
+      *reinterpret_cast<u32x4*>(tile + row * MP + piece * 16) = v;
     }
-    f32x4 acc[MF][2];
+    wave_sync();
+    bf16x8 mf[RS][CF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i) acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < steps; ++s) {
-      bf16x8 mf[2];
-      if constexpr (TRANS) {
-        // rows s 32 .. of m, this wave's 32 columns
+    for (int s = 0; s < RS; ++s)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = lane + i * 64, r = s * 32 + (at >> 2), col = c0 + (at & 3) * 8;
-          const u32x4 v = buf_load16(mr, r < rank && col < a.N ? ((uint32_t)r * (uint32_t)a.N + (uint32_t)col) * 2u : kOutside);
-          *reinterpret_cast<u32x4*>(tile + (at >> 2) * AP + (at & 3) * 16) = v;
-        }
-        wave_sync();
+      for (int j = 0; j < CF; ++j) {
+        if constexpr (TRANS) mf[s][j] = read_transposed(tile, (s * 32 + 8 * lhi + (l16 >> 2)) * MP + j * 32 + (l16 & 3) * 8, 4 * MP);
+        else mf[s][j] = *reinterpret_cast<const bf16x8*>(tile + (j * 16 + l16) * MP + s * 64 + lhi * 16);
+      }
+    wave_sync();
+    const int next = c0 + CW * NW;
+    if (next < n1) load_m(next);
+#pragma unroll 1
+    for (int rb = 0; rb < MB; rb += RB) {
+      if (MB > RB && s_rows[rb] < 0) {           // padding behind the adapter's rows
+        if (next < n1) load_base(next, 0);
+        break;
+      }
+      u32x4 base[BN];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) mf[h] = read_transposed(tile + (8 * lhi + (l16 >> 2)) * AP + (l16 & 3) * 16 + h * 8, 4 * AP);
-        wave_sync();
-      } else {
-        const int r = s * 32 + lhi * 8;
+      for (int i = 0; i < BN; ++i) base[i] = b[i];
+      if (rb + RB < MB) load_base(c0, rb + RB);
+      else if (next < n1) load_base(next, 0);
+      f32x4 acc[MF][CF];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int col = c0 + (l16 >> 2) * 8 + h * 4 + (l16 & 3);
-          u32x4 v = buf_load16(mr, r < rank && col < a.N ? ((uint32_t)col * (uint32_t)R + (uint32_t)r) * 2u : kOutside);
-          if (r + 8 > rank) {                  // columns past the adapter's rank hold anything
+      for (int i = 0; i < MF; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int left = rank - (r + 2 * q);
-              v[q] = left >= 2 ? v[q] : left == 1 ? v[q] & 0xffffu : 0u;
+        for (int j = 0; j < CF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < RS; ++s)
+        if (s < steps)
+#pragma unroll
+          for (int i = 0; i < MF; ++i) {
+            const int at = (rb + i * 16 + l16) * UP + (s * 32 + lhi * 8) * 2;
+            const bf16x8 hi = *reinterpret_cast<const bf16x8*>(&s_u[0][at]);
+            const bf16x8 lo = *reinterpret_cast<const bf16x8*>(&s_u[1][at]);
+#pragma unroll
+            for (int j = 0; j < CF; ++j) {
+              acc[i][j] = mfma(mf[s][j], lo, acc[i][j]);
+              acc[i][j] = mfma(mf[s][j], hi, acc[i][j]);
             }
           }
-          mf[h] = __builtin_bit_cast(bf16x8, v);
-        }
-      }
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const int at = (i * 16 + l16) * UP + (s * 32 + lhi * 8) * 2;
-        const bf16x8 hi = *reinterpret_cast<const bf16x8*>(&s_u[0][at]);
-        const bf16x8 lo = *reinterpret_cast<const bf16x8*>(&s_u[1][at]);
+      for (int i = 0; i < MF; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          acc[i][h] = mfma(mf[h], lo, acc[i][h]);
-          acc[i][h] = mfma(mf[h], hi, acc[i][h]);
-        }
-      }
-    }
-    if (c < n1)
+        for (int j = 0; j < CF; ++j) *reinterpret_cast<f32x4*>(tile + (i * 16 + l16) * DP + j * 64 + lhi * 16) = acc[i][j];
+      wave_sync();
 #pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        if (tok[i] < 0) continue;
+      for (int i = 0; i < BN; ++i) {
+        const uint8_t* p = tile + (i * RPL + brow) * DP + bcol * 4;
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 16);
+        const int t = s_rows[rb + i * RPL + brow];
         u32x4 o;
-        o.x = pack_bf16x2(bf16_lo(b[i].x) + f * acc[i][0][0], bf16_hi(b[i].x) + f * acc[i][0][1]);
-        o.y = pack_bf16x2(bf16_lo(b[i].y) + f * acc[i][0][2], bf16_hi(b[i].y) + f * acc[i][0][3]);
-        o.z = pack_bf16x2(bf16_lo(b[i].z) + f * acc[i][1][0], bf16_hi(b[i].z) + f * acc[i][1][1]);
-        o.w = pack_bf16x2(bf16_lo(b[i].w) + f * acc[i][1][2], bf16_hi(b[i].w) + f * acc[i][1][3]);
-        *reinterpret_cast<u32x4*>(a.out + tok[i] * a.ld_out + c) = o;
+        o.x = pack_bf16x2(bf16_lo(base[i].x) + f * lo[0], bf16_hi(base[i].x) + f * lo[1]);
+        o.y = pack_bf16x2(bf16_lo(base[i].y) + f * lo[2], bf16_hi(base[i].y) + f * lo[3]);
+        o.z = pack_bf16x2(bf16_lo(base[i].z) + f * hi[0], bf16_hi(base[i].z) + f * hi[1]);
+        o.w = pack_bf16x2(bf16_lo(base[i].w) + f * hi[2], bf16_hi(base[i].w) + f * hi[3]);
+        if (t >= 0 && c0 + bcol < n1) *reinterpret_cast<u32x4*>(a.out + t * a.ld_out + c0 + bcol) = o;
       }
+      wave_sync();
+    }
   }
 }
 
@@ -426,8 +551,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
 struct GradSide {
   const uint16_t* z;
   int64_t ldz;
-  const float* u;        // [splits][T][R]
-  int32_t splits;
+  const uint16_t* u;     // three bf16 numbers a value: [3][T][R]
   int32_t N;             // columns
   const float* scale;    // or null
   float* out;            // dA: [n][R][N], dB: [n][N][R]; null: not wanted
@@ -445,9 +569,10 @@ struct GradArgs {
   float* part;
 };
 
-constexpr int kGradCols = 128;
+constexpr int kGradCols = 256;
 constexpr int kGradStep = 32;
 constexpr int kGradMaxRows = 1024;
+constexpr int kGradWaves = 8;
 
 // Chunk c: its adapter and place in that; `slot` its place in part (-1: written straight). False past the last.
 __device__ inline bool find_chunk(const int32_t* counts, int n, int rows, int c, int& e, int& at, int& slot) {
@@ -472,13 +597,23 @@ __device__ inline bool find_chunk(const int32_t* counts, int n, int rows, int c,
   return false;
 }
 
+// A step is 32 rows: 512 bytes of each row of z and its three parts of u, by LDS-DMA as in the down kernel, four stages
+// of which three are in flight. The rows are the contraction, so both operands are read transposed. A wave
+// has 64 columns and half the ranks (32 columns with one fragment of ranks).
 template <int RF>
-__global__ __launch_bounds__(256) void adapter_grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs a) {
   constexpr int RP = RF * 16;
-  constexpr int ZP = kGradCols * 2 + 16, UP = RP * 2 + 16;
-  __shared__ __attribute__((aligned(16))) uint8_t s_z[2][kGradStep * ZP];
-  __shared__ __attribute__((aligned(16))) uint8_t s_u[2][3][kGradStep * UP];
-  __shared__ int s_src[kGradMaxRows];
+  constexpr int RG = RF > 1 ? 2 : 1, CG = kGradWaves / RG;   // waves by ranks and by columns
+  constexpr int CF = kGradCols / 16 / CG, RW = RF / RG;      // fragments of a wave
+  constexpr int ZBYTES = kGradStep * kGradCols * 2, UBYTES = kGradStep * RP * 2;
+  constexpr int ZN = ZBYTES / 1024 / kGradWaves;             // loads of a wave
+  constexpr int UB = 3 * UBYTES / 1024, UN = (UB + kGradWaves - 1) / kGradWaves;
+  constexpr int STAGE = ZBYTES + 3 * UBYTES;
+  __shared__ __attribute__((aligned(16))) uint8_t s_t0[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t1[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t2[STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t s_t3[STAGE];
+  __shared__ int s_src[kGradMaxRows + 8 * kGradStep];
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -493,108 +628,109 @@ __global__ __launch_bounds__(256) void adapter_grad_kernel(GradArgs a) {
   e = __builtin_amdgcn_readfirstlane(e);
   const int cnt = min(a.rows, a.counts[e] - at * a.rows);
   const int rank = adapter_rank(a.ranks, e, a.R) - r0;
+  const int steps = (cnt + kGradStep - 1) / kGradStep;
   const int32_t* src = a.src + a.offsets[e] + (int64_t)at * a.rows;
-  for (int i = tid; i < cnt; i += 256) {
-    const int t = src[i];
+  for (int i = tid; i < (steps + 8) * kGradStep; i += 64 * kGradWaves) {      // steps past the last: no rows
+    const int t = i < cnt ? src[i] : -1;
     s_src[i] = (uint32_t)t < (uint32_t)a.T ? t : -1;
   }
   __syncthreads();
-  const int steps = (cnt + kGradStep - 1) / kGradStep;
-  // a thread's part of a step: two 16-byte pieces of z, 8 values of u
-  u32x4 zv[2];
-  f32x4 uv[2];
-  const int urow = tid / (RP / 8), ucol = (tid % (RP / 8)) * 8;
-  const auto load = [&](int s) {
+  // this lane's pieces of a step: row and column. The 16-byte pieces of a row of z are permuted so that the 16 rows
+  // of a transposing read land on distinct banks (u: piece_swz).
+  const uint16_t* zc[ZN];
+  const uint16_t* uc[UN];
+  int urow[UN];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = tid + i * 256, row = s * kGradStep + (p >> 4), col = n0 + (p & 15) * 8;
-      const int t = row < cnt ? s_src[row] : -1;
-      zv[i] = u32x4{0u, 0u, 0u, 0u};
-      if (t >= 0 && col < g.N) zv[i] = *reinterpret_cast<const u32x4*>(g.z + t * g.ldz + col);
+  for (int i = 0; i < ZN; ++i) {
+    const int p = (wave + i * kGradWaves) * 64 + lane, row = p >> 5;
+    const int swz = ((row & 3) | (((row >> 3) & 3) << 2)) << 1;
+    zc[i] = g.z + min(n0 + ((p & 31) ^ swz) * 8, g.N - 8);     // columns past the last are never written
+  }
+#pragma unroll
+  for (int i = 0; i < UN; ++i) {
+    const int p = (wave + i * kGradWaves) % UB * 64 + lane, plane = p / (UBYTES / 16), q = p % (UBYTES / 16);
+    urow[i] = q / (RP / 8);
+    const int r = r0 + ((q % (RP / 8)) ^ piece_swz<RP>(urow[i])) * 8;
+    uc[i] = r < a.R ? g.u + (int64_t)plane * a.T * a.R + r : nullptr;
+  }
+  const int64_t ldz = g.ldz;
+  const auto dma = [&](int s, uint8_t* stage) {
+    const uint64_t none = reinterpret_cast<uint64_t>(adapter_zeros);
+#pragma unroll
+    for (int i = 0; i < ZN; ++i) {
+      const int t = s_src[s * kGradStep + (((wave + i * kGradWaves) * 64 + lane) >> 5)];
+      const uint64_t there = reinterpret_cast<uint64_t>(zc[i] + t * ldz);
+      load_to_lds(reinterpret_cast<const void*>(t >= 0 ? there : none), stage + (wave + i * kGradWaves) * 1024);
     }
-    uv[0] = uv[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (urow < kGradStep) {
-      const int row = s * kGradStep + urow;
-      const int t = row < cnt ? s_src[row] : -1;
-      if (t >= 0 && ucol < rank && r0 + ucol < a.R) {
-        const float* p = g.u + (int64_t)t * a.R + r0 + ucol;
-        for (int q = 0; q < g.splits; ++q, p += (int64_t)a.T * a.R) {
-          uv[0] += *reinterpret_cast<const f32x4*>(p);
-          uv[1] += *reinterpret_cast<const f32x4*>(p + 4);
-        }
-      }
-    }
-  };
-  const auto store = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int p = tid + i * 256;
-      *reinterpret_cast<u32x4*>(&s_z[buf][(p >> 4) * ZP + (p & 15) * 16]) = zv[i];
-    }
-    if (urow < kGradStep) {
-      bf16x8 o[3];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        __bf16 b[3];
-        split<3>(uv[q >> 2][q & 3], b);
-#pragma unroll
-        for (int p = 0; p < 3; ++p) o[p][q] = b[p];
-      }
-#pragma unroll
-      for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(&s_u[buf][p][urow * UP + ucol * 2]) = o[p];
+    for (int i = 0; i < UN; ++i) {
+      const int t = s_src[s * kGradStep + urow[i]];
+      const uint64_t there = reinterpret_cast<uint64_t>(uc[i] + (int64_t)t * a.R);
+      load_to_lds(reinterpret_cast<const void*>(((t >= 0) & (uc[i] != nullptr)) ? there : none), stage + ZBYTES + (wave + i * kGradWaves) % UB * 1024);
     }
   };
-  f32x4 acc[2][RF];
+  f32x4 acc[CF][RW];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < CF; ++h)
 #pragma unroll
-    for (int j = 0; j < RF; ++j) acc[h][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load(0);
-  store(0);
-  if (steps > 1) load(1);
-  __syncthreads();
-  const int trow = 8 * lhi + (l16 >> 2), tcol = l16 & 3;
-  for (int s = 0; s < steps; ++s) {
-    const int buf = s & 1;
-    bf16x8 zf[2];
-    // dA: a lane's columns are to be 8 neighbours (over both fragments), dB: 16 neighbours a fragment
+    for (int j = 0; j < RW; ++j) acc[h][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int h0 = wave % CG * CF, j0 = wave / CG * RW;
+  // this lane's places in a stage (the rows of a fragment's second half have the same permutation)
+  const int trow = 8 * lhi + (l16 >> 2);
+  const int tswz = ((trow & 3) | (((trow >> 3) & 3) << 2)) << 1;
+  uint32_t zat[CF], uat[RW];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      zf[h] = read_transposed(&s_z[buf][trow * ZP + wave * 64 + (db ? h * 32 + tcol * 8 : tcol * 16 + h * 8)], 4 * ZP);
+  for (int h = 0; h < CF; ++h) zat[h] = trow * (kGradCols * 2) + ((((h0 + h) * 2 + ((l16 >> 1) & 1)) ^ tswz) << 4) + (l16 & 1) * 8;
 #pragma unroll
-    for (int j = 0; j < RF; ++j)
+  for (int j = 0; j < RW; ++j)
+    uat[j] = ZBYTES + trow * (RP * 2) + ((((j0 + j) * 2 + ((l16 >> 1) & 1)) ^ piece_swz<RP>(trow)) << 4) + (l16 & 1) * 8;
+  const auto step = [&](int s, const uint8_t* cur, uint8_t* next) {
+    dma(s + 3, next);      // the stage that everybody was done with at the last barrier
+    bf16x8 zf[CF];
+#pragma unroll
+    for (int h = 0; h < CF; ++h) zf[h] = read_transposed(cur, zat[h], 4 * kGradCols * 2);
+#pragma unroll
+    for (int j = 0; j < RW; ++j)
 #pragma unroll
       for (int p = 2; p >= 0; --p) {
-        const bf16x8 uf = read_transposed(&s_u[buf][p][trow * UP + j * 32 + tcol * 8], 4 * UP);
+        const bf16x8 uf = read_transposed(cur, uat[j] + p * UBYTES, 4 * RP * 2);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) acc[h][j] = db ? mfma(uf, zf[h], acc[h][j]) : mfma(zf[h], uf, acc[h][j]);
+        for (int h = 0; h < CF; ++h) acc[h][j] = mfma(zf[h], uf, acc[h][j]);
       }
-    if (s + 1 < steps) {
-      store(buf ^ 1);
-      if (s + 2 < steps) load(s + 2);
-    }
-    __syncthreads();
+    stage_barrier<2 * (ZN + UN)>();
+  };
+  dma(0, s_t0);
+  dma(1, s_t1);
+  dma(2, s_t2);
+  stage_barrier<2 * (ZN + UN)>();
+  for (int s = 0; s < steps; s += 4) {      // whole rounds: steps past the last add zeros
+    step(s, s_t0, s_t3);
+    step(s + 1, s_t1, s_t0);
+    step(s + 2, s_t2, s_t1);
+    step(s + 3, s_t3, s_t2);
   }
+  wait_vm0();
   const float f = g.scale ? g.scale[e] : 1.f;
   const int64_t size = (int64_t)a.R * g.N;
   float* out = slot < 0 ? g.out + e * size : a.part + g.part + slot * size;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < CF; ++h) {
+    const int col = n0 + (h0 + h) * 16 + lhi * 4;
 #pragma unroll
-    for (int j = 0; j < RF; ++j) {
+    for (int j = 0; j < RW; ++j) {
+      const int r = (j0 + j) * 16 + l16;
       f32x4 v = acc[h][j];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = r < rank ? v[q] * f : 0.f;
+      if (col >= g.N || r0 + r >= a.R) continue;
       if (db) {
-        const int col = n0 + wave * 32 + h * 16 + l16, r = j * 16 + lhi * 4;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = r + q < rank ? v[q] * f : 0.f;
-        if (col < g.N && r0 + r < a.R) *reinterpret_cast<f32x4*>(out + (int64_t)col * a.R + r0 + r) = v;
+        for (int q = 0; q < 4; ++q) out[(int64_t)(col + q) * a.R + r0 + r] = v[q];
       } else {
-        const int col = n0 + wave * 32 + lhi * 8 + h * 4, r = j * 16 + l16;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = r < rank ? v[q] * f : 0.f;
-        if (col < g.N && r0 + r < a.R) *reinterpret_cast<f32x4*>(out + (int64_t)(r0 + r) * g.N + col) = v;
+        *reinterpret_cast<f32x4*>(out + (int64_t)(r0 + r) * g.N + col) = v;
       }
     }
+  }
 }
 
 constexpr int kJoinValues = 2048;    // values of a workgroup of the join kernel
@@ -627,16 +763,47 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(GradArgs a) {
   }
 }
 
+// u[i], the sum of `splits` partial results in order, as three bf16 numbers n apart; of two arrays
+struct PartsArgs {
+  const float* part[2];
+  int32_t splits[2];
+  uint16_t* out[2];
+  int64_t n;
+};
+__global__ __launch_bounds__(256) void adapter_parts_kernel(PartsArgs a) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int k = blockIdx.y;
+  if (i >= a.n || !a.out[k]) return;
+  const float* part = a.part[k];
+  f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
+#pragma unroll 8
+  for (int s = 1; s < a.splits[k]; ++s) v += *reinterpret_cast<const f32x4*>(part + s * a.n + i);
+  bf16x4 o[3];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    __bf16 b[3];
+    split<3>(v[q], b);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) o[p][q] = b[p];
+  }
+#pragma unroll
+  for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x4*>(a.out[k] + p * a.n + i) = o[p];
+}
+
 // ---------------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------------
-constexpr int64_t kMaxGrid = (1 << 24) - 1;      // workgroups of 256 threads: fewer than 2^32 threads
+constexpr int64_t kMaxGrid = (1 << 23) - 8;      // workgroups of up to 512 threads: fewer than 2^32 threads
 
-// Slices of the long dimension: enough workgroups for few rows, each wave a chunk at least.
-int32_t adapter_splits(int32_t T, int32_t K) {
-  const int blocks = std::max(1, (T + 15) / 16), most = std::max(1, K / (kChunk * kDownWaves));
-  return std::max(1, std::min(most, 512 / blocks));
+// rows of a block: 128 for many rows in tiles of 128 (with at most 64 ranks), so that an adapter's factors are read for
+// more rows at once
+static int block_rows_of(int32_t T, int32_t tile, int32_t R) { return tile == 16 ? 16 : tile == 128 && R <= 64 && T >= 256 ? 128 : 32; }
+// Slices of the long dimension: so many that there are about as many workgroups as CUs.
+static int32_t splits_of(int32_t T, int32_t K, int mb) {
+  const int blocks = std::max(1, T <= 64 ? (T + 1) / 2 : mb == 128 ? (T + 127) / 128 : (T + 31) / 32);
+  return std::max(1, std::min((K + 255) / 256, (256 + blocks - 1) / blocks));
 }
+int32_t adapter_splits(int32_t T, int32_t K, int32_t R) { return splits_of(T, K, block_rows_of(T, 128, R)); }
 int32_t adapter_grad_rows(int32_t T) { return T <= 2048 ? 256 : 1024; }
 int32_t adapter_grad_slots(int32_t T) { return T <= adapter_grad_rows(T) ? 0 : 2 * (T / adapter_grad_rows(T)); }
 
@@ -649,7 +816,6 @@ static RowArgs row_args(const AdapterLaunch& l) {
   } else {
     r.src = l.plan->src;
     r.tile_expert = l.plan->tile_expert;
-    r.num_tiles = l.plan->num_tiles;
     r.pos = l.plan->pos;
     r.tile_shift = __builtin_ctz((unsigned)l.plan->tile);
   }
@@ -658,7 +824,7 @@ static RowArgs row_args(const AdapterLaunch& l) {
   return r;
 }
 // blocks of MB rows that a grouping can have: a tile of a plan has a row at least
-static int block_rows_of(const AdapterLaunch& l) { return l.ids || l.plan->tile == 16 ? 16 : 32; }
+static int block_rows_of(const AdapterLaunch& l) { return block_rows_of(l.T, l.ids ? 16 : l.plan->tile, l.R); }
 static int block_count(const AdapterLaunch& l, int mb) {
   if (l.ids) return l.T;
   const int64_t tiles = std::min<int64_t>(l.T, l.plan->rows_cap / l.plan->tile);
@@ -666,25 +832,39 @@ static int block_count(const AdapterLaunch& l, int mb) {
 }
 
 static int copy_blocks(int32_t T) { return (T + kCopyRows - 1) / kCopyRows; }
-static int up_slab(int32_t T) { return T <= 256 ? 128 : 512; }
+static int up_slab(int32_t T, int mb) { return T <= 256 ? 256 : mb == 128 ? 1024 : 512; }
 static int grad_chunks(int32_t T, int32_t n) { return T / adapter_grad_rows(T) + std::min(n, T); }
 
 // whether every launch of a forward (K to N) or backward pass has a grid that can be launched
 static bool fits(const AdapterLaunch& l, int32_t K, int32_t N, bool grads) {
   if (l.T == 0) return true;
-  const int64_t blocks = block_count(l, block_rows_of(l)), slab = up_slab(l.T);
-  if (blocks * adapter_splits(l.T, K) > kMaxGrid || (blocks + copy_blocks(l.T)) * ((N + slab - 1) / slab) > kMaxGrid) return false;
+  const int mb = block_rows_of(l);
+  const int64_t blocks = block_count(l, mb), slab = up_slab(l.T, mb);
+  if (blocks * splits_of(l.T, K, mb) > kMaxGrid || (blocks + copy_blocks(l.T)) * ((N + slab - 1) / slab) > kMaxGrid) return false;
+  if (grads && ((int64_t)l.T * l.R / 4 + 255) / 256 > kMaxGrid) return false;
   return !grads || (int64_t)((K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols) * grad_chunks(l.T, l.n) <= kMaxGrid;
 }
 
 template <int MB, bool TRANS>
-static void launch_down(const DownArgs& a, int blocks, hipStream_t s) {
+static void launch_down(const DownArgs& a, hipStream_t s) {
   const int rp = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : 128;
-  const dim3 grid((unsigned)(a.splits * blocks), (a.R + rp - 1) / rp), block(64 * kDownWaves);
+  const int x = a.splits > 1 ? a.splits * a.blocks : (a.blocks + 7) / 8 * 8;
+  const dim3 grid((unsigned)x, (a.R + rp - 1) / rp), block(64 * kDownWaves);
   if (rp == 16) hipLaunchKernelGGL((adapter_down_kernel<MB, 1, TRANS>), grid, block, 0, s, a);
   else if (rp == 32) hipLaunchKernelGGL((adapter_down_kernel<MB, 2, TRANS>), grid, block, 0, s, a);
   else if (rp == 64) hipLaunchKernelGGL((adapter_down_kernel<MB, 4, TRANS>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((adapter_down_kernel<MB, 8, TRANS>), grid, block, 0, s, a);
+  else if constexpr (MB <= 32) hipLaunchKernelGGL((adapter_down_kernel<MB, 8, TRANS>), grid, block, 0, s, a);
+}
+
+template <int MB, bool TRANS>
+static void launch_up(const UpArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 block(64 * kUpWaves);
+  if (a.R <= 32) hipLaunchKernelGGL((adapter_up_kernel<MB, 1, TRANS>), grid, block, 0, s, a);
+  else if (a.R <= 64) hipLaunchKernelGGL((adapter_up_kernel<MB, 2, TRANS>), grid, block, 0, s, a);
+  else if constexpr (MB <= 32) {
+    if (a.R <= 128) hipLaunchKernelGGL((adapter_up_kernel<MB, 4, TRANS>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((adapter_up_kernel<MB, 8, TRANS>), grid, block, 0, s, a);
+  }
 }
 
 template <bool TRANS>
@@ -699,21 +879,24 @@ static int down(const AdapterLaunch& l, const void* z, int64_t ldz, const void* 
   a.ranks = l.ranks;
   a.K = K;
   a.R = l.R;
-  a.splits = adapter_splits(l.T, K);
   a.part = part;
-  const int mb = block_rows_of(l), blocks = block_count(l, mb);
-  if (mb == 16) launch_down<16, TRANS>(a, blocks, stream);
-  else launch_down<32, TRANS>(a, blocks, stream);
+  const int mb = block_rows_of(l);
+  a.blocks = block_count(l, mb);
+  a.splits = splits_of(l.T, K, mb);
+  if (mb == 16) launch_down<16, TRANS>(a, stream);
+  else if (mb == 128) launch_down<128, TRANS>(a, stream);
+  else launch_down<32, TRANS>(a, stream);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 template <bool TRANS>
-static int up(const AdapterLaunch& l, const float* part, int32_t splits, const void* m, const float* scale, int32_t N,
+static int up(const AdapterLaunch& l, const float* part, int32_t splits, const uint16_t* parts, const void* m, const float* scale, int32_t N,
               const void* base, int64_t ld_base, void* out, int64_t ld_out, float* u_out, hipStream_t stream) {
   UpArgs a;
   a.rows = row_args(l);
   a.part = part;
   a.splits = splits;
+  a.parts = parts;
   a.m = static_cast<const uint16_t*>(m);
   a.scale = scale;
   a.ranks = l.ranks;
@@ -727,30 +910,39 @@ static int up(const AdapterLaunch& l, const float* part, int32_t splits, const v
   const int mb = block_rows_of(l);
   a.blocks = block_count(l, mb);
   const int copies = base == out ? 0 : copy_blocks(l.T);   // in place they stay as they are
-  a.slab = up_slab(l.T);
-  const dim3 grid((unsigned)((N + a.slab - 1) / a.slab * (a.blocks + copies))), block(64 * kUpWaves);
-  if (mb == 16) hipLaunchKernelGGL((adapter_up_kernel<16, TRANS>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((adapter_up_kernel<32, TRANS>), grid, block, 0, stream, a);
+  a.slab = up_slab(l.T, mb);
+  const dim3 grid((unsigned)((N + a.slab - 1) / a.slab * (a.blocks + copies)));
+  if (mb == 16) launch_up<16, TRANS>(a, grid, stream);
+  else if (mb == 128) launch_up<128, TRANS>(a, grid, stream);
+  else launch_up<32, TRANS>(a, grid, stream);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
   if (!fits(l, l.K, l.N, false)) return MOE_ERR_UNSUPPORTED;
-  const int splits = adapter_splits(l.T, l.K);
+  const int splits = splits_of(l.T, l.K, block_rows_of(l));
   float* part = splits == 1 && l.v ? l.v : static_cast<float*>(l.ws);
   int rc = down<false>(l, l.x, l.ldx, l.a, nullptr, l.K, part, stream);
   if (rc != MOE_OK) return rc;
-  return up<false>(l, part, splits, l.b, l.scale, l.N, l.base, l.ld_base, l.out, l.ld_out, splits > 1 ? l.v : nullptr, stream);
+  return up<false>(l, part, splits, nullptr, l.b, l.scale, l.N, l.base, l.ld_base, l.out, l.ld_out, splits > 1 ? l.v : nullptr, stream);
 }
 
 int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream) {
   if (!fits(l, l.N, l.K, true)) return MOE_ERR_UNSUPPORTED;
-  const int splits = adapter_splits(l.T, l.N);
-  float* dv = static_cast<float*>(l.ws);
-  if (l.T > 0 && (g.dx || g.da)) {
-    int rc = down<true>(l, g.dout, g.ld_dout, l.b, l.scale, l.N, dv, stream);
-    if (rc == MOE_OK && g.dx)
-      rc = up<true>(l, dv, splits, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
+  // dv's partial results, dv and v in three bf16 numbers each, partial results of dA and dB
+  const int splits = l.T > 0 ? splits_of(l.T, l.N, block_rows_of(l)) : 1;
+  const int64_t size = (int64_t)l.T * l.R;
+  float* const part = static_cast<float*>(l.ws);
+  uint16_t* const dv = reinterpret_cast<uint16_t*>(part + splits * size);
+  uint16_t* const v = dv + 3 * size;
+  if (l.T > 0) {
+    const bool rows = g.dx || g.da;
+    int rc = rows ? down<true>(l, g.dout, g.ld_dout, l.b, l.scale, l.N, part, stream) : MOE_OK;
+    if (rc != MOE_OK) return rc;
+    const PartsArgs p = {{part, l.v}, {splits, 1}, {rows ? dv : nullptr, g.db ? v : nullptr}, size};
+    hipLaunchKernelGGL(adapter_parts_kernel, dim3((unsigned)((size / 4 + 255) / 256), 2), dim3(256), 0, stream, p);
+    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+    if (g.dx) rc = up<true>(l, nullptr, 0, dv, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
     if (rc != MOE_OK) return rc;
   }
   if (!g.da && !g.db) return MOE_OK;
@@ -760,9 +952,9 @@ int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipSt
   a.T = l.T;
   a.R = l.R;
   a.rows = adapter_grad_rows(l.T);
-  a.part = dv + (int64_t)splits * l.T * l.R;
-  a.side[0] = {static_cast<const uint16_t*>(l.x), l.ldx, dv, splits, l.K, nullptr, g.da, 0};
-  a.side[1] = {static_cast<const uint16_t*>(g.dout), g.ld_dout, l.v, 1, l.N, l.scale, g.db,
+  a.part = reinterpret_cast<float*>(v + 3 * size);
+  a.side[0] = {static_cast<const uint16_t*>(l.x), l.ldx, dv, l.K, nullptr, g.da, 0};
+  a.side[1] = {static_cast<const uint16_t*>(g.dout), g.ld_dout, v, l.N, l.scale, g.db,
                (int64_t)adapter_grad_slots(l.T) * l.R * l.K};
   if (l.T > 0) {
     a.src = l.plan->src;
@@ -772,9 +964,9 @@ int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipSt
     a.slabs = a.slabs0 + (g.db ? (l.N + kGradCols - 1) / kGradCols : 0);
     const int rp = l.R <= 16 ? 16 : l.R <= 32 ? 32 : 64;
     const dim3 grid((unsigned)(a.slabs * grad_chunks(l.T, l.n)), (l.R + rp - 1) / rp);
-    if (rp == 16) hipLaunchKernelGGL(adapter_grad_kernel<1>, grid, dim3(256), 0, stream, a);
-    else if (rp == 32) hipLaunchKernelGGL(adapter_grad_kernel<2>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(adapter_grad_kernel<4>, grid, dim3(256), 0, stream, a);
+    if (rp == 16) hipLaunchKernelGGL(adapter_grad_kernel<1>, grid, dim3(64 * kGradWaves), 0, stream, a);
+    else if (rp == 32) hipLaunchKernelGGL(adapter_grad_kernel<2>, grid, dim3(64 * kGradWaves), 0, stream, a);
+    else hipLaunchKernelGGL(adapter_grad_kernel<4>, grid, dim3(64 * kGradWaves), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   }
   const int64_t most = (int64_t)l.R * std::max(g.da ? l.K : 0, g.db ? l.N : 0);

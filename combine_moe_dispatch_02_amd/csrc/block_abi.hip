@@ -219,7 +219,7 @@ MOE355_API int moe_router_topk_backward(const float* d_topk_weights, const void*
 
 MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R) {
   if (T < 1 || K < 8 || K % 8 != 0 || K > kMaxWidth || R < 8 || R % 8 != 0 || R > 256) return 0;
-  return (size_t)adapter_splits(T, K) * T * R * sizeof(float);
+  return (size_t)adapter_splits(T, K, R) * T * R * sizeof(float);
 }
 
 MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void* b, const float* scale,
@@ -247,7 +247,8 @@ MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void
 
 MOE355_API size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t n, int32_t K, int32_t N, int32_t R) {
   if (n < 1 || n > 1024 || N < 8 || N % 8 != 0 || N > kMaxWidth || moe_adapter_workspace_bytes(T, K, R) == 0) return 0;
-  return moe_adapter_workspace_bytes(T, N, R) + (size_t)adapter_grad_slots(T) * R * (K + N) * sizeof(float);
+  // dv's partial results, dv and v in three 2-byte parts each, partial results of da and db
+  return moe_adapter_workspace_bytes(T, N, R) + (size_t)T * R * 12 + (size_t)adapter_grad_slots(T) * R * (K + N) * sizeof(float);
 }
 
 MOE355_API int moe_adapter_backward(const void* dout, int32_t ld_dout, const void* x, int32_t ldx, const float* v,

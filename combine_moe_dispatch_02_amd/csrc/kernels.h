@@ -221,7 +221,7 @@ struct AdapterGrads {
   float* da;
   float* db;
 };
-int32_t adapter_splits(int32_t T, int32_t K);   // partial results of v (K: the contraction's length)
+int32_t adapter_splits(int32_t T, int32_t K, int32_t R);   // partial results of v at most (K: the contraction's length)
 int32_t adapter_grad_slots(int32_t T);          // partial results of dA and dB
 int launch_adapter(const AdapterLaunch& l, hipStream_t stream);
 int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream);

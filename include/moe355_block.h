@@ -239,7 +239,7 @@ MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R);
  * Errors: MOE_ERR_INVALID (null or misaligned pointers, n not in [1,1024], T < 0, K, N or R <
  * 8, pitches below the width or no multiples of 8, both or neither of ids and plan, id_begin <
  * 0, a plan of other sizes, small workspace), MOE_ERR_UNSUPPORTED (K, N or R no multiple of 8,
- * K or N > 32768, R > 256, ids with T > 64, more than 2^24 - 1 workgroups).
+ * K or N > 32768, R > 256, ids with T > 64, more than 2^23 - 8 workgroups).
  */
 MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void* b, const float* scale,
                            const int32_t* ranks, int32_t n, int32_t T, int32_t K, int32_t N, int32_t R,
