@@ -339,6 +339,29 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(DownArgs 
 // up: out[t][c] = bf16(base[t][c] + f sum over r of u[t][r] m(c, r)); TRANS: m is given as [r][c] (A for dx),
 // else [c][r] (B). u is the sum of the down kernel's partial results.
 // ---------------------------------------------------------------------------------------
+// Row t, one without an adapter: out = base. By a wave, a row's loads in flight together.
+struct CopyArgs {
+  const uint16_t* base;    // null: zeros
+  int64_t ld_base;
+  uint16_t* out;
+  int64_t ld_out;
+  int32_t N;
+};
+__device__ inline void copy_row(const CopyArgs& a, const RowArgs& rows, int t) {
+  if (rows.ids ? (uint32_t)(rows.ids[t] - rows.begin) < (uint32_t)rows.n : rows.pos[t] >= 0) return;
+  const uint16_t* from = a.base + t * a.ld_base;
+  uint16_t* to = a.out + t * a.ld_out;
+  for (int c = lane_id() * 8; c < a.N; c += 8 * 512) {
+    u32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = a.base ? *reinterpret_cast<const u32x4*>(from + min(c + i * 512, a.N - 8)) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i * 512 < a.N) *reinterpret_cast<u32x4*>(to + c + i * 512) = v[i];
+  }
+}
+
 struct UpArgs {
   RowArgs rows;
   const float* part;       // u as partial results,
@@ -348,54 +371,44 @@ struct UpArgs {
   const float* scale;
   const int32_t* ranks;
   int32_t N, R;
-  const uint16_t* base;    // null: zeros
-  int64_t ld_base;
-  uint16_t* out;
-  int64_t ld_out;
+  CopyArgs io;             // base and out
   float* u_out;            // the sums themselves, where there are several partial results, or null
-  int32_t blocks;          // blocks of rows; workgroups behind them copy rows without an adapter
-  int32_t slab;            // columns of a workgroup, a multiple of 256
+  int32_t copies;          // workgroups in front that copy rows without an adapter, kCopyRows each
 };
 
-constexpr int kCopyRows = 64;
+constexpr int kCopyRows = 4;     // of a workgroup, a row a wave
 constexpr int kUpWaves = 4;
+constexpr int up_cols(int rs) { return rs > 4 ? 32 : 64; }    // columns of a wave
+constexpr int kRowsAhead = 2;
 
-// A wave makes CW columns of the block's rows, 32 rows at a time, in LDS of its own: m goes there as whole lines come,
-// then the sums, from where base and out are read and written in whole lines too. The next rows of base are in
-// flight meanwhile, and the next columns of m, the first ones while u is summed. RS: steps of 32 ranks that u has at most.
+// A wave has CW columns of m in registers and makes them for the block's rows, 16 at a time, with base of the next ones
+// in flight. A CU's address unit takes 64 neighbouring bytes of neighbouring lanes a clock, so u is the first operand of
+// the product and fragment j has columns 4 i + j (CW = 64): a lane has 4 neighbours of a row, 16 lanes a whole line
+// (with the rows along the lanes, each lane's 16 bytes were a clock of their own: 44 us for 8192 x 4096 in bf16, rank 64).
+// RS: steps of 32 ranks that u has at most.
 template <int MB, int RS, bool TRANS>
-__global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
-  constexpr int NW = kUpWaves;
-  constexpr int RB = MB < 32 ? MB : 32, MF = RB / 16;    // rows at a time
-  constexpr int CW = RS > 4 ? 32 : 64, CF = CW / 16;
+__global__ __launch_bounds__(64 * kUpWaves, RS <= 2 ? 4 : 2) void adapter_up_kernel(UpArgs a) {
+  constexpr int NW = kUpWaves, CW = up_cols(RS), CF = CW / 16;
+  constexpr int CD = CF / 2;                             // 4-byte words of a row for each lane
+  typedef uint32_t words __attribute__((ext_vector_type(CD)));
   constexpr int UP = RS * 64 + 16;                       // bytes of a row of u in LDS,
-  constexpr int MP = (TRANS ? CW * 2 : RS * 64) + 16;    // of m (TRANS: a rank's columns, else a column's ranks),
-  constexpr int DP = CW * 4 + 16;                        // and of the sums
-  constexpr int MROWS = TRANS ? RS * 32 : CW, MPIECES = TRANS ? CW / 8 : RS * 4;
-  constexpr int MN = MROWS * MPIECES / 64;               // 16-byte pieces of m for each lane
-  constexpr int LPR = CW / 8, RPL = 64 / LPR;            // lanes that share a row of base and out, rows of a load
-  constexpr int BN = RB / RPL;                           // pieces of base for each lane
-  constexpr int TILE = MROWS * MP > RB * DP ? MROWS * MP : RB * DP;
-  __shared__ __attribute__((aligned(16))) uint8_t s_u[2][MB * UP];
-  __shared__ __attribute__((aligned(16))) uint8_t s_tile[NW][TILE];
-  __shared__ int s_rows[MB];
+  constexpr int MP = TRANS ? CW * 2 + 16 : 64 + 16;      // of 32 ranks of m: a rank's columns (TRANS), else a column's ranks
+  constexpr int MR = TRANS ? 32 : CW;                    // rows of that
+  constexpr int MPC = TRANS ? CW / 8 : 4;                // 16-byte pieces of such a row,
+  constexpr int MN = MR * MPC / 64;                      // of all of it for each lane
+  __shared__ __attribute__((aligned(16))) uint8_t s_mem[2 * MB * UP > NW * MR * MP ? 2 * MB * UP : NW * MR * MP];   // m, then u
+  __shared__ __attribute__((aligned(16))) int s_rows[MB];
   const int tid = threadIdx.x;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int slabs = (a.N + a.slab - 1) / a.slab;
-  const int slab = blockIdx.x % (uint32_t)slabs, block = blockIdx.x / (uint32_t)slabs;
-  const int n0 = slab * a.slab, n1 = min(a.N, n0 + a.slab);
-  if (block >= a.blocks) {                     // rows without an adapter
-    const int t0 = (block - a.blocks) * kCopyRows;
-    for (int t = t0 + wave; t < min(a.rows.T, t0 + kCopyRows); t += NW) {
-      const bool has = a.rows.ids ? (uint32_t)(a.rows.ids[t] - a.rows.begin) < (uint32_t)a.rows.n : a.rows.pos[t] >= 0;
-      if (has) continue;
-      for (int c = n0 + lane * 8; c < n1; c += 512)
-        *reinterpret_cast<u32x4*>(a.out + t * a.ld_out + c) =
-            a.base ? *reinterpret_cast<const u32x4*>(a.base + t * a.ld_base + c) : u32x4{0u, 0u, 0u, 0u};
-    }
+  if ((int)blockIdx.x < a.copies) {            // rows without an adapter
+    const int t = blockIdx.x * kCopyRows + wave;
+    if (t < a.rows.T) copy_row(a.io, a.rows, t);
     return;
   }
+  const int slabs = (a.N + CW * NW - 1) / (CW * NW);
+  const int slab = (blockIdx.x - a.copies) % (uint32_t)slabs, block = (blockIdx.x - a.copies) / (uint32_t)slabs;
+  const int n0 = slab * (CW * NW), n1 = min(a.N, n0 + CW * NW);
   int e;
   if (!block_rows<MB>(a.rows, block, e, s_rows)) return;
   e = __builtin_amdgcn_readfirstlane(e);
@@ -403,43 +416,94 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
   const int R = a.R, rank = adapter_rank(a.ranks, e, R);
   const int steps = (rank + 31) / 32;
   const __amdgpu_buffer_rsrc_t mr = make_rsrc(a.m + (int64_t)e * a.N * R, (uint32_t)R * (uint32_t)a.N * 2u);
-  const int brow = lane / LPR, bcol = lane % LPR * 8;      // this lane's row and 8 columns of base and out
+  const int c0 = n0 + wave * CW;               // this wave's columns,
+  const int lc = c0 + l16 * CF;                // this lane's CF of them
 
-  u32x4 mv[MN], b[BN];
-  const auto load_m = [&](int c0) {
+  u32x4 mv[RS][MN];
+#pragma unroll
+  for (int s = 0; s < RS; ++s)
 #pragma unroll
     for (int i = 0; i < MN; ++i) {
-      const int at = lane + i * 64, row = at / MPIECES, piece = at % MPIECES;
-      const int r = TRANS ? row : piece * 8, col = c0 + (TRANS ? piece * 8 : row);
+      const int at = lane + i * 64, row = at / MPC, piece = at % MPC;
+      const int r = s * 32 + (TRANS ? row : piece * 8), col = c0 + (TRANS ? piece * 8 : row);
       const uint32_t off = TRANS ? (uint32_t)r * (uint32_t)a.N + (uint32_t)col : (uint32_t)col * (uint32_t)R + (uint32_t)r;
-      mv[i] = buf_load16(mr, r < rank && col < a.N ? off * 2u : kOutside);
+      mv[s][i] = buf_load16(mr, r < rank && col < a.N ? off * 2u : kOutside);
     }
-  };
-  const auto load_base = [&](int c0, int rb) {
+  // u, where it is there in parts
+  constexpr int UN = MB * RS * 4 / (64 * NW) > 0 ? MB * RS * 4 / (64 * NW) : 1;     // 16-byte pieces of a part for each lane
+  u32x4 uv[UN][2];
+  if (a.parts) {
 #pragma unroll
-    for (int i = 0; i < BN; ++i) {
-      const uint16_t* p = a.base + max(s_rows[rb + i * RPL + brow], 0) * a.ld_base + min(c0 + bcol, a.N - 8);
-      b[i] = a.base ? *reinterpret_cast<const u32x4*>(p) : u32x4{0u, 0u, 0u, 0u};
+    for (int i = 0; i < UN; ++i) {
+      const int at = tid + i * 64 * NW, row = at / (RS * 4), r = (at % (RS * 4)) * 8, t = row < MB ? s_rows[row] : -1;
+      const bool has = t >= 0 && r < R;
+      const uint16_t* p = a.parts + (has ? (int64_t)t * R + r : 0);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uv[i][k] = *reinterpret_cast<const u32x4*>(p + k * (int64_t)a.rows.T * R);
+        if (!has) uv[i][k] = u32x4{0u, 0u, 0u, 0u};
+      }
     }
+  }
+  words base[kRowsAhead][4];
+  const auto load_base = [&](int i, words (&b)[4]) {
+    const int4 t = *reinterpret_cast<const int4*>(&s_rows[i * 16 + lhi * 4]);
+    const int ts[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      b[q] = a.io.base ? *reinterpret_cast<const words*>(a.io.base + max(ts[q], 0) * a.io.ld_base + min(lc, a.N - CF)) : words{};
   };
-  int c0 = n0 + wave * CW;
-  if (c0 < n1) {
-    load_m(c0);
-    load_base(c0, 0);
+#pragma unroll
+  for (int i = 0; i < kRowsAhead; ++i) load_base(min(i, MB / 16 - 1), base[i]);
+
+  // m's fragments: lane (l16, lhi) has ranks 8 lhi .. of column CF l16 + j. Transposed, the tile holds column CF i + j
+  // at place 16 j + i, which is where the transposing read looks for lane i's.
+  bf16x8 mf[RS][CF];
+  uint8_t* tile = s_mem + wave * (MR * MP);
+#pragma unroll
+  for (int s = 0; s < RS; ++s) {
+#pragma unroll
+    for (int i = 0; i < MN; ++i) {
+      const int at = lane + i * 64, row = at / MPC, piece = at % MPC;
+      u32x4 v = mv[s][i];
+      if constexpr (!TRANS) {
+        if (rank & 7) {                        // columns past the adapter's rank hold anything
+          const int left = rank - (s * 32 + piece * 8);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = left >= 2 * q + 2 ? v[q] : left == 2 * q + 1 ? v[q] & 0xffffu : 0u;
+        }
+        *reinterpret_cast<u32x4*>(tile + row * MP + piece * 16) = v;
+      } else if constexpr (CF == 4) {          // columns k and 4 + k of the piece are neighbours
+        uint8_t* to = tile + row * MP + piece * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint32_t*>(to + k * 32) = k & 1 ? (v[k >> 1] >> 16) | (v[2 + (k >> 1)] & 0xffff0000u)
+                                                            : (v[k >> 1] & 0xffffu) | (v[2 + (k >> 1)] << 16);
+      } else {                                 // columns k, 2 + k, 4 + k and 6 + k are
+        uint8_t* to = tile + row * MP + piece * 8;
+        *reinterpret_cast<u32x2*>(to) = u32x2{(v[0] & 0xffffu) | (v[1] << 16), (v[2] & 0xffffu) | (v[3] << 16)};
+        *reinterpret_cast<u32x2*>(to + 32) = u32x2{(v[0] >> 16) | (v[1] & 0xffff0000u), (v[2] >> 16) | (v[3] & 0xffff0000u)};
+      }
+    }
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < CF; ++j) {
+      if constexpr (TRANS) mf[s][j] = read_transposed(tile, (8 * lhi + (l16 >> 2)) * MP + j * 32 + (l16 & 3) * 8, 4 * MP);
+      else mf[s][j] = *reinterpret_cast<const bf16x8*>(tile + ((l16 * CF + j) * MP + lhi * 16));
+    }
+    wave_sync();
   }
 
   // u as two bf16 numbers each: as they are, or of partial results added in order
+  uint8_t* s_u = s_mem;
+  __syncthreads();
   if (a.parts) {
-    for (int at = tid; at < MB * RS * 4; at += 64 * NW) {
-      const int row = at / (RS * 4), r = (at % (RS * 4)) * 8, t = s_rows[row];
-      u32x4 v[2] = {};
-      if (t >= 0 && r < R) {
-        const uint16_t* p = a.parts + (int64_t)t * R + r;
-        v[0] = *reinterpret_cast<const u32x4*>(p);
-        v[1] = *reinterpret_cast<const u32x4*>(p + (int64_t)a.rows.T * R);
-      }
-      *reinterpret_cast<u32x4*>(&s_u[0][row * UP + r * 2]) = v[0];
-      *reinterpret_cast<u32x4*>(&s_u[1][row * UP + r * 2]) = v[1];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int at = tid + i * 64 * NW, row = at / (RS * 4), r = (at % (RS * 4)) * 8;
+      if (row >= MB) break;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) *reinterpret_cast<u32x4*>(&s_u[k * (MB * UP) + row * UP + r * 2]) = uv[i][k];
     }
   } else {
     for (int at = tid; at < MB * RS * 8; at += 64 * NW) {
@@ -460,86 +524,46 @@ __global__ __launch_bounds__(64 * kUpWaves) void adapter_up_kernel(UpArgs a) {
         hi[q] = o[0];
         lo[q] = o[1];
       }
-      *reinterpret_cast<bf16x4*>(&s_u[0][row * UP + r * 2]) = hi;
-      *reinterpret_cast<bf16x4*>(&s_u[1][row * UP + r * 2]) = lo;
+      *reinterpret_cast<bf16x4*>(&s_u[row * UP + r * 2]) = hi;
+      *reinterpret_cast<bf16x4*>(&s_u[MB * UP + row * UP + r * 2]) = lo;
     }
   }
   __syncthreads();
   const float f = a.scale ? a.scale[e] : 1.f;
-  uint8_t* tile = s_tile[wave];
-  for (; c0 < n1; c0 += CW * NW) {
+  const auto rows16 = [&](int i, words (&b)[4]) {
+    f32x4 acc[CF];
 #pragma unroll
-    for (int i = 0; i < MN; ++i) {
-      const int at = lane + i * 64, row = at / MPIECES, piece = at % MPIECES;
-      u32x4 v = mv[i];
-      if (!TRANS && (rank & 7)) {      // columns past the adapter's rank hold anything
-        const int left = rank - piece * 8;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = left >= 2 * q + 2 ? v[q] : left == 2 * q + 1 ? v[q] & 0xffffu : 0u;
-      }
-      *reinterpret_cast<u32x4*>(tile + row * MP + piece * 16) = v;
-    }
-    wave_sync();
-    bf16x8 mf[RS][CF];
+    for (int j = 0; j < CF; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < RS; ++s)
+      if (s < steps) {
+        const int at = (i * 16 + l16) * UP + (s * 32 + lhi * 8) * 2;
+        const bf16x8 hi = *reinterpret_cast<const bf16x8*>(&s_u[at]);
+        const bf16x8 lo = *reinterpret_cast<const bf16x8*>(&s_u[MB * UP + at]);
 #pragma unroll
-      for (int j = 0; j < CF; ++j) {
-        if constexpr (TRANS) mf[s][j] = read_transposed(tile, (s * 32 + 8 * lhi + (l16 >> 2)) * MP + j * 32 + (l16 & 3) * 8, 4 * MP);
-        else mf[s][j] = *reinterpret_cast<const bf16x8*>(tile + (j * 16 + l16) * MP + s * 64 + lhi * 16);
+        for (int j = 0; j < CF; ++j) acc[j] = mfma(lo, mf[s][j], acc[j]);
+#pragma unroll
+        for (int j = 0; j < CF; ++j) acc[j] = mfma(hi, mf[s][j], acc[j]);
       }
-    wave_sync();
-    const int next = c0 + CW * NW;
-    if (next < n1) load_m(next);
-#pragma unroll 1
-    for (int rb = 0; rb < MB; rb += RB) {
-      if (MB > RB && s_rows[rb] < 0) {           // padding behind the adapter's rows
-        if (next < n1) load_base(next, 0);
-        break;
+    words o[4];                                  // row 4 lhi + q
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int k = 0; k < CD; ++k) {
+        const uint32_t w = b[q][k];
+        o[q][k] = pack_bf16x2(bf16_lo(w) + f * acc[2 * k][q], bf16_hi(w) + f * acc[2 * k + 1][q]);
       }
-      u32x4 base[BN];
+    if (i + kRowsAhead < MB / 16) load_base(i + kRowsAhead, b);
+    const int4 t = *reinterpret_cast<const int4*>(&s_rows[i * 16 + lhi * 4]);
+    const int ts[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-      for (int i = 0; i < BN; ++i) base[i] = b[i];
-      if (rb + RB < MB) load_base(c0, rb + RB);
-      else if (next < n1) load_base(next, 0);
-      f32x4 acc[MF][CF];
+    for (int q = 0; q < 4; ++q)
+      if (ts[q] >= 0 && lc < n1) *reinterpret_cast<words*>(a.io.out + ts[q] * a.io.ld_out + lc) = o[q];
+  };
 #pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < CF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < RS; ++s)
-        if (s < steps)
-#pragma unroll
-          for (int i = 0; i < MF; ++i) {
-            const int at = (rb + i * 16 + l16) * UP + (s * 32 + lhi * 8) * 2;
-            const bf16x8 hi = *reinterpret_cast<const bf16x8*>(&s_u[0][at]);
-            const bf16x8 lo = *reinterpret_cast<const bf16x8*>(&s_u[1][at]);
-#pragma unroll
-            for (int j = 0; j < CF; ++j) {
-              acc[i][j] = mfma(mf[s][j], lo, acc[i][j]);
-              acc[i][j] = mfma(mf[s][j], hi, acc[i][j]);
-            }
-          }
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < CF; ++j) *reinterpret_cast<f32x4*>(tile + (i * 16 + l16) * DP + j * 64 + lhi * 16) = acc[i][j];
-      wave_sync();
-#pragma unroll
-      for (int i = 0; i < BN; ++i) {
-        const uint8_t* p = tile + (i * RPL + brow) * DP + bcol * 4;
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 16);
-        const int t = s_rows[rb + i * RPL + brow];
-        u32x4 o;
-        o.x = pack_bf16x2(bf16_lo(base[i].x) + f * lo[0], bf16_hi(base[i].x) + f * lo[1]);
-        o.y = pack_bf16x2(bf16_lo(base[i].y) + f * lo[2], bf16_hi(base[i].y) + f * lo[3]);
-        o.z = pack_bf16x2(bf16_lo(base[i].z) + f * hi[0], bf16_hi(base[i].z) + f * hi[1]);
-        o.w = pack_bf16x2(bf16_lo(base[i].w) + f * hi[2], bf16_hi(base[i].w) + f * hi[3]);
-        if (t >= 0 && c0 + bcol < n1) *reinterpret_cast<u32x4*>(a.out + t * a.ld_out + c0 + bcol) = o;
-      }
-      wave_sync();
-    }
+  for (int i = 0; i < MB / 16; ++i) {
+    if (i > 0 && s_rows[i * 16] < 0) break;      // padding behind the adapter's rows
+    rows16(i, base[i % kRowsAhead]);
   }
 }
 
@@ -769,8 +793,17 @@ struct PartsArgs {
   int32_t splits[2];
   uint16_t* out[2];
   int64_t n;
+  float* sum;            // the first array's sums themselves, or null
+  int32_t blocks;        // workgroups of that; those behind them copy rows without an adapter
+  RowArgs rows;
+  CopyArgs io;
 };
 __global__ __launch_bounds__(256) void adapter_parts_kernel(PartsArgs a) {
+  if ((int)blockIdx.x >= a.blocks) {
+    const int t = ((int)blockIdx.x - a.blocks) * kCopyRows + (threadIdx.x >> 6);
+    if (t < a.rows.T && blockIdx.y == 0) copy_row(a.io, a.rows, t);
+    return;
+  }
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int k = blockIdx.y;
   if (i >= a.n || !a.out[k]) return;
@@ -778,6 +811,7 @@ __global__ __launch_bounds__(256) void adapter_parts_kernel(PartsArgs a) {
   f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
 #pragma unroll 8
   for (int s = 1; s < a.splits[k]; ++s) v += *reinterpret_cast<const f32x4*>(part + s * a.n + i);
+  if (a.sum && k == 0) *reinterpret_cast<f32x4*>(a.sum + i) = v;
   bf16x4 o[3];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -832,16 +866,18 @@ static int block_count(const AdapterLaunch& l, int mb) {
 }
 
 static int copy_blocks(int32_t T) { return (T + kCopyRows - 1) / kCopyRows; }
-static int up_slab(int32_t T, int mb) { return T <= 256 ? 256 : mb == 128 ? 1024 : 512; }
+static int up_slabs(int32_t N, int32_t R) { const int c = up_cols(R > 128 ? 8 : 4) * kUpWaves; return (N + c - 1) / c; }
+// rows of a block of the up kernel
+static int up_rows_of(const AdapterLaunch& l) { return l.ids ? 16 : l.R > 64 ? std::min(l.plan->tile, 64) : l.plan->tile; }
 static int grad_chunks(int32_t T, int32_t n) { return T / adapter_grad_rows(T) + std::min(n, T); }
 
 // whether every launch of a forward (K to N) or backward pass has a grid that can be launched
 static bool fits(const AdapterLaunch& l, int32_t K, int32_t N, bool grads) {
   if (l.T == 0) return true;
   const int mb = block_rows_of(l);
-  const int64_t blocks = block_count(l, mb), slab = up_slab(l.T, mb);
-  if (blocks * splits_of(l.T, K, mb) > kMaxGrid || (blocks + copy_blocks(l.T)) * ((N + slab - 1) / slab) > kMaxGrid) return false;
-  if (grads && ((int64_t)l.T * l.R / 4 + 255) / 256 > kMaxGrid) return false;
+  if ((int64_t)block_count(l, mb) * splits_of(l.T, K, mb) > kMaxGrid) return false;
+  if ((int64_t)block_count(l, up_rows_of(l)) * up_slabs(N, l.R) + copy_blocks(l.T) > kMaxGrid) return false;
+  if (((int64_t)l.T * l.R / 4 + 255) / 256 + copy_blocks(l.T) > kMaxGrid) return false;
   return !grads || (int64_t)((K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols) * grad_chunks(l.T, l.n) <= kMaxGrid;
 }
 
@@ -861,7 +897,7 @@ static void launch_up(const UpArgs& a, dim3 grid, hipStream_t s) {
   const dim3 block(64 * kUpWaves);
   if (a.R <= 32) hipLaunchKernelGGL((adapter_up_kernel<MB, 1, TRANS>), grid, block, 0, s, a);
   else if (a.R <= 64) hipLaunchKernelGGL((adapter_up_kernel<MB, 2, TRANS>), grid, block, 0, s, a);
-  else if constexpr (MB <= 32) {
+  else if constexpr (MB <= 64) {
     if (a.R <= 128) hipLaunchKernelGGL((adapter_up_kernel<MB, 4, TRANS>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((adapter_up_kernel<MB, 8, TRANS>), grid, block, 0, s, a);
   }
@@ -902,29 +938,45 @@ static int up(const AdapterLaunch& l, const float* part, int32_t splits, const u
   a.ranks = l.ranks;
   a.N = N;
   a.R = l.R;
-  a.base = static_cast<const uint16_t*>(base);
-  a.ld_base = ld_base;
-  a.out = static_cast<uint16_t*>(out);
-  a.ld_out = ld_out;
+  a.io = {static_cast<const uint16_t*>(base), ld_base, static_cast<uint16_t*>(out), ld_out, N};
   a.u_out = u_out;
-  const int mb = block_rows_of(l);
-  a.blocks = block_count(l, mb);
-  const int copies = base == out ? 0 : copy_blocks(l.T);   // in place they stay as they are
-  a.slab = up_slab(l.T, mb);
-  const dim3 grid((unsigned)((N + a.slab - 1) / a.slab * (a.blocks + copies)));
+  const int mb = up_rows_of(l);
+  a.copies = parts || base == out ? 0 : copy_blocks(l.T);   // with parts they are copied already; in place they stay as they are
+  const dim3 grid((unsigned)(a.copies + up_slabs(N, l.R) * block_count(l, mb)));
   if (mb == 16) launch_up<16, TRANS>(a, grid, stream);
-  else if (mb == 128) launch_up<128, TRANS>(a, grid, stream);
-  else launch_up<32, TRANS>(a, grid, stream);
+  else if (mb == 32) launch_up<32, TRANS>(a, grid, stream);
+  else if (mb == 64) launch_up<64, TRANS>(a, grid, stream);
+  else launch_up<128, TRANS>(a, grid, stream);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+// u (and another array) in parts, and the rows without an adapter copied (unless nothing is written, or in place)
+static int make_parts(const AdapterLaunch& l, PartsArgs p, const CopyArgs& io, hipStream_t stream) {
+  p.blocks = (int)((p.n / 4 + 255) / 256);
+  p.rows = row_args(l);
+  p.io = io;
+  const int copies = io.out && io.out != io.base ? copy_blocks(l.T) : 0;
+  hipLaunchKernelGGL(adapter_parts_kernel, dim3((unsigned)(p.blocks + copies), p.out[1] ? 2 : 1), dim3(256), 0, stream, p);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
   if (!fits(l, l.K, l.N, false)) return MOE_ERR_UNSUPPORTED;
+  const int64_t size = (int64_t)l.T * l.R;
   const int splits = splits_of(l.T, l.K, block_rows_of(l));
   float* part = splits == 1 && l.v ? l.v : static_cast<float*>(l.ws);
   int rc = down<false>(l, l.x, l.ldx, l.a, nullptr, l.K, part, stream);
   if (rc != MOE_OK) return rc;
-  return up<false>(l, part, splits, nullptr, l.b, l.scale, l.N, l.base, l.ld_base, l.out, l.ld_out, splits > 1 ? l.v : nullptr, stream);
+  // many rows: v once, in parts, rather than the partial results by every workgroup
+  uint16_t* parts = nullptr;
+  if (block_rows_of(l) == 128) {
+    parts = reinterpret_cast<uint16_t*>(static_cast<float*>(l.ws) + splits * size);
+    const int rc = make_parts(l, {{part, nullptr}, {splits, 0}, {parts, nullptr}, size, splits > 1 ? l.v : nullptr},
+                              {static_cast<const uint16_t*>(l.base), l.ld_base, static_cast<uint16_t*>(l.out), l.ld_out, l.N}, stream);
+    if (rc != MOE_OK) return rc;
+  }
+  return up<false>(l, part, splits, parts, l.b, l.scale, l.N, l.base, l.ld_base, l.out, l.ld_out,
+                   splits > 1 && !parts ? l.v : nullptr, stream);
 }
 
 int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream) {
@@ -939,9 +991,9 @@ int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipSt
     const bool rows = g.dx || g.da;
     int rc = rows ? down<true>(l, g.dout, g.ld_dout, l.b, l.scale, l.N, part, stream) : MOE_OK;
     if (rc != MOE_OK) return rc;
-    const PartsArgs p = {{part, l.v}, {splits, 1}, {rows ? dv : nullptr, g.db ? v : nullptr}, size};
-    hipLaunchKernelGGL(adapter_parts_kernel, dim3((unsigned)((size / 4 + 255) / 256), 2), dim3(256), 0, stream, p);
-    if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
+    rc = make_parts(l, {{part, l.v}, {splits, 1}, {rows ? dv : nullptr, g.db ? v : nullptr}, size, nullptr},
+                    {static_cast<const uint16_t*>(g.dx_base), g.ld_base, static_cast<uint16_t*>(g.dx), g.ld_dx, l.K}, stream);
+    if (rc != MOE_OK) return rc;
     if (g.dx) rc = up<true>(l, nullptr, 0, dv, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
     if (rc != MOE_OK) return rc;
   }

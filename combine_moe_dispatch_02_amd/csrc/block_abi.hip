@@ -219,7 +219,7 @@ MOE355_API int moe_router_topk_backward(const float* d_topk_weights, const void*
 
 MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R) {
   if (T < 1 || K < 8 || K % 8 != 0 || K > kMaxWidth || R < 8 || R % 8 != 0 || R > 256) return 0;
-  return (size_t)adapter_splits(T, K, R) * T * R * sizeof(float);
+  return (size_t)adapter_splits(T, K, R) * T * R * sizeof(float) + (size_t)T * R * 6;   // v's partial results, v in 2-byte parts
 }
 
 MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void* b, const float* scale,
