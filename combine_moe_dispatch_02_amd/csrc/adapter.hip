@@ -832,12 +832,14 @@ constexpr int64_t kMaxGrid = (1 << 23) - 8;      // workgroups of up to 512 thre
 // rows of a block: 128 for many rows in tiles of 128 (with at most 64 ranks), so that an adapter's factors are read for
 // more rows at once
 static int block_rows_of(int32_t T, int32_t tile, int32_t R) { return tile == 16 ? 16 : tile == 128 && R <= 64 && T >= 256 ? 128 : 32; }
-// Slices of the long dimension: so many that there are about as many workgroups as CUs.
-static int32_t splits_of(int32_t T, int32_t K, int mb) {
-  const int blocks = std::max(1, T <= 64 ? (T + 1) / 2 : mb == 128 ? (T + 127) / 128 : (T + 31) / 32);
-  return std::max(1, std::min((K + 255) / 256, (256 + blocks - 1) / blocks));
+// Slices of the long dimension: so many that there are about as many workgroups as CUs, all in one round (64 rows of
+// nearly as many adapters: 8 slices 12.5 us, 4 slices 8.4; 1021 rows in tiles of 16: 11 and 8.5; 8192 rows of 16
+// adapters: 4 slices 31, 2 slices 27).
+static int32_t splits_of(int32_t T, int32_t K, int32_t n, int mb) {
+  const int blocks = std::max(1, T <= 64 ? T : (T + mb - 1) / mb + std::min(n, T) / 2);    // half a block more for each adapter
+  return std::max(1, std::min((K + 255) / 256, 256 / blocks));
 }
-int32_t adapter_splits(int32_t T, int32_t K, int32_t R) { return splits_of(T, K, block_rows_of(T, 128, R)); }
+int32_t adapter_splits(int32_t T, int32_t K, int32_t R) { return splits_of(T, K, 0, block_rows_of(T, 128, R)); }
 int32_t adapter_grad_rows(int32_t T) { return T <= 2048 ? 256 : 1024; }
 int32_t adapter_grad_slots(int32_t T) { return T <= adapter_grad_rows(T) ? 0 : 2 * (T / adapter_grad_rows(T)); }
 
@@ -875,7 +877,7 @@ static int grad_chunks(int32_t T, int32_t n) { return T / adapter_grad_rows(T) +
 static bool fits(const AdapterLaunch& l, int32_t K, int32_t N, bool grads) {
   if (l.T == 0) return true;
   const int mb = block_rows_of(l);
-  if ((int64_t)block_count(l, mb) * splits_of(l.T, K, mb) > kMaxGrid) return false;
+  if ((int64_t)block_count(l, mb) * splits_of(l.T, K, l.n, mb) > kMaxGrid) return false;
   if ((int64_t)block_count(l, up_rows_of(l)) * up_slabs(N, l.R) + copy_blocks(l.T) > kMaxGrid) return false;
   if (((int64_t)l.T * l.R / 4 + 255) / 256 + copy_blocks(l.T) > kMaxGrid) return false;
   return !grads || (int64_t)((K + kGradCols - 1) / kGradCols + (N + kGradCols - 1) / kGradCols) * grad_chunks(l.T, l.n) <= kMaxGrid;
@@ -918,7 +920,7 @@ static int down(const AdapterLaunch& l, const void* z, int64_t ldz, const void* 
   a.part = part;
   const int mb = block_rows_of(l);
   a.blocks = block_count(l, mb);
-  a.splits = splits_of(l.T, K, mb);
+  a.splits = splits_of(l.T, K, l.n, mb);
   if (mb == 16) launch_down<16, TRANS>(a, stream);
   else if (mb == 128) launch_down<128, TRANS>(a, stream);
   else launch_down<32, TRANS>(a, stream);
@@ -963,7 +965,7 @@ static int make_parts(const AdapterLaunch& l, PartsArgs p, const CopyArgs& io, h
 int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
   if (!fits(l, l.K, l.N, false)) return MOE_ERR_UNSUPPORTED;
   const int64_t size = (int64_t)l.T * l.R;
-  const int splits = splits_of(l.T, l.K, block_rows_of(l));
+  const int splits = splits_of(l.T, l.K, l.n, block_rows_of(l));
   float* part = splits == 1 && l.v ? l.v : static_cast<float*>(l.ws);
   int rc = down<false>(l, l.x, l.ldx, l.a, nullptr, l.K, part, stream);
   if (rc != MOE_OK) return rc;
@@ -982,7 +984,7 @@ int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
 int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream) {
   if (!fits(l, l.N, l.K, true)) return MOE_ERR_UNSUPPORTED;
   // dv's partial results, dv and v in three bf16 numbers each, partial results of dA and dB
-  const int splits = l.T > 0 ? splits_of(l.T, l.N, block_rows_of(l)) : 1;
+  const int splits = l.T > 0 ? splits_of(l.T, l.N, l.n, block_rows_of(l)) : 1;
   const int64_t size = (int64_t)l.T * l.R;
   float* const part = static_cast<float*>(l.ws);
   uint16_t* const dv = reinterpret_cast<uint16_t*>(part + splits * size);
