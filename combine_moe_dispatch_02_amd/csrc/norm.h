@@ -63,19 +63,32 @@ __device__ inline void unpack8(u32x4 v, float (&f)[8]) {
 __device__ inline u32x4 pack8(const float (&f)[8]) {
   return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
 }
-// the norm's weight, bf16 or fp32 (chunks past the row read as 0)
-__device__ inline void load_weight(__amdgpu_buffer_rsrc_t r, bool f32, int c, float (&w)[8]) {
+// 8 values, bf16 or fp32, as they are loaded (the second half for fp32 alone) ...
+struct Raw8 {
+  u32x4 lo, hi;
+};
+__device__ inline Raw8 load_raw(__amdgpu_buffer_rsrc_t r, bool f32, int c) {
+  Raw8 v;
+  v.lo = buf_load16(r, (uint32_t)c * (f32 ? 32u : 16u));
+  if (f32) v.hi = buf_load16(r, (uint32_t)c * 32u + 16u);
+  return v;
+}
+// ... and what they are
+__device__ inline void unpack_raw(const Raw8& v, bool f32, float (&w)[8]) {
   if (f32) {
-    const u32x4 a = buf_load16(r, (uint32_t)c * 32u), b = buf_load16(r, (uint32_t)c * 32u + 16u);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = a[j], hi = b[j];   // a bit cast of a vector's element would take its first
+      const uint32_t lo = v.lo[j], hi = v.hi[j];   // a bit cast of a vector's element would take its first
       w[j] = __builtin_bit_cast(float, lo);
       w[4 + j] = __builtin_bit_cast(float, hi);
     }
   } else {
-    unpack8(buf_load16(r, (uint32_t)c * 16u), w);
+    unpack8(v.lo, w);
   }
+}
+// the norm's weight, bf16 or fp32 (chunks past the row read as 0)
+__device__ inline void load_weight(__amdgpu_buffer_rsrc_t r, bool f32, int c, float (&w)[8]) {
+  unpack_raw(load_raw(r, f32, c), f32, w);
 }
 
 __device__ inline uint32_t umax_dpp(uint32_t v, uint32_t o) { return v > o ? v : o; }

@@ -23,9 +23,20 @@
 
 namespace moe {
 
+// 1 / (1 + e^-z) within 3 units in the last place: e^-z = 2^t (1 + ln 2 d) with t = -z log2 e as fp32 rounds it and d what
+// that leaves out, hardware exp2 and reciprocal (a unit each); 0 below 2^-125. expf and a division take 13 instructions more a value: 35 of 43 us
+// without any (1021 x 7168 backward, a gate for each value).
+__device__ inline float sigmoid(float z) {
+  const float c = -__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f);        // 2^t stays finite
+  const float t = c * 0x1.715476p+0f;
+  const float d = __builtin_fmaf(c, 0x1.4ae0bep-26f, __builtin_fmaf(c, 0x1.715476p+0f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float f = __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e * d, 0x1.62e430p-1f, e));
+  return z != z ? z : z < -87.0f ? 0.0f : f;
+}
 // the gate's factor without branch_scale, and its slope
 __device__ inline float gate_act(int act, float z) {
-  if (act == MOE_GATE_SIGMOID) return 1.0f / (1.0f + expf(-z));
+  if (act == MOE_GATE_SIGMOID) return sigmoid(z);
   if (act == MOE_GATE_TANH) return tanhf(z);
   return z;
 }
@@ -60,8 +71,9 @@ struct SandwichArgs {
 __device__ inline float inverse_rms(double ss, int H, double eps) { return (float)(1.0 / __builtin_sqrt(ss / (double)H + eps)); }
 
 // W waves a row, W = 1: four rows a workgroup; CPL chunks of 8 values a lane. With an 8-bit output the
-// rows in 16 bits pass the caches by, as in the single norm.
-template <int W, int CPL, int QF>
+// rows in 16 bits pass the caches by, as in the single norm. COLS: the gate is one for each column or value. Gate and weights
+// are loaded before the sums that they wait for.
+template <int W, int CPL, int QF, bool COLS>
 __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_kernel(SandwichArgs a) {
 #pragma clang fp contract(off)
   constexpr int ROWS = W == 1 ? 4 : 1;
@@ -75,7 +87,6 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
   const uint32_t row_bytes = (uint32_t)H * 2u;
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, a.w ? val_bytes(a.w_f32, H) : 0u);
   const __amdgpu_buffer_rsrc_t wpr = make_rsrc(a.wp, a.wp ? val_bytes(a.w_f32, H) : 0u);
-  const bool columns = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL;
   int odd = 0;
   for (int64_t t = (int64_t)blockIdx.x * ROWS + (W == 1 ? wave : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
     const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x + t * H, row_bytes);
@@ -89,7 +100,13 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     if (a.gate_kind == MOE_GATE_ROW) row_f = gate_act(a.act, load_scalar(a.gate, a.gate_f32, t)) * a.branch_scale;
     const uint32_t gb = val_bytes(a.gate_f32, H);
     const __amdgpu_buffer_rsrc_t gr =
-        make_rsrc(columns ? static_cast<const char*>(a.gate) + (a.gate_kind == MOE_GATE_FULL ? t * gb : 0) : nullptr, columns ? gb : 0u);
+        make_rsrc(COLS ? static_cast<const char*>(a.gate) + (a.gate_kind == MOE_GATE_FULL ? t * gb : 0) : nullptr, COLS ? gb : 0u);
+    Raw8 z[CPL], w[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      if constexpr (COLS) z[i] = load_raw(gr, a.gate_f32, c0 + i * kWave);
+      w[i] = load_raw(wpr, a.w_f32, c0 + i * kWave);
+    }
     float r1 = 0.f;
     if (a.wp) {
       double ss = 0.0;
@@ -114,16 +131,16 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       unpack8(v[i], p);
       unpack8(r[i], b);
       if (a.wp) {
-        float w[8];
-        load_weight(wpr, a.w_f32, c, w);
+        float wf[8];
+        unpack_raw(w[i], a.w_f32, wf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = (p[j] * r1) * w[j];
+        for (int j = 0; j < 8; ++j) p[j] = (p[j] * r1) * wf[j];
       }
-      if (columns) {
-        float z[8];
-        load_weight(gr, a.gate_f32, c, z);
+      if constexpr (COLS) {
+        float zf[8];
+        unpack_raw(z[i], a.gate_f32, zf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = p[j] * (gate_act(a.act, z[j]) * a.branch_scale);
+        for (int j = 0; j < 8; ++j) p[j] = p[j] * (gate_act(a.act, zf[j]) * a.branch_scale);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] = p[j] * row_f;
@@ -141,6 +158,8 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       }
     }
     if (!a.w) continue;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) w[i] = load_raw(wr, a.w_f32, c0 + i * kWave);
     ss = row_sum<W>(ss, red, sub, odd);
     odd ^= 1;
     const float r2 = inverse_rms(ss, H, a.eps2);
@@ -151,11 +170,11 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = c0 + i * kWave;
-      float f[8], w[8];
+      float f[8], wf[8];
       unpack8(v[i], f);
-      load_weight(wr, a.w_f32, c, w);
+      unpack_raw(w[i], a.w_f32, wf);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (f[j] * r2) * w[j];
+      for (int j = 0; j < 8; ++j) f[j] = (f[j] * r2) * wf[j];
       u32x4 o = pack8(f);
       if (QF == 2 && c >= nch) o = u32x4{0u, 0u, 0u, 0u};
       store_row<NT>(o, yr, (uint32_t)c * 16u);
@@ -188,6 +207,9 @@ struct SandwichBwdArgs {
   float* part_gate;
 };
 
+// value j of 8 bf16 values
+__device__ inline float value(u32x4 v, int j) { return j & 1 ? bf16_hi(v[j >> 1]) : bf16_lo(v[j >> 1]); }
+
 // three sums over a row at once
 template <int W>
 __device__ inline void row_sum3(float (&v)[3], float* red, int sub, int odd) {
@@ -211,7 +233,7 @@ __device__ inline void row_sum3(float (&v)[3], float* red, int sub, int odd) {
 
 // A row's two means need one exchange: with k = p f (its column sums over the row) the second mean is linear in
 // the first, mean(dp wp xh) = (sum k (d_s + r2 g) - r2 mean(g xs) sum k xs) / H. GK: 0 no gate or one a row (k = p:
-// f leaves the sums), 1 a gate for each column, 2 for each value.
+// f leaves the sums), 1 a gate for each column, 2 (bf16) and 3 (fp32) for each value.
 template <int W, int CPL, bool POST, int GK>
 __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_backward_kernel(SandwichBwdArgs a) {
   constexpr int ROWS = W == 1 ? 4 : 1;
@@ -250,55 +272,80 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     }
   };
   if constexpr (HELD) weights(0, c0);
-  int odd = 0;
-  for (int64_t t = blockIdx.x + (W == 1 ? (int64_t)wave * gridDim.x : 0); t < a.T; t += (int64_t)gridDim.x * ROWS) {
-    const auto row = [&](const uint16_t* p) { return make_rsrc(p ? p + t * H : nullptr, p ? row_bytes : 0u); };
-    const __amdgpu_buffer_rsrc_t dr = row(a.dy), er = row(a.d_s), xr = row(a.x), sr = row(a.s);
-    const __amdgpu_buffer_rsrc_t gr =
-        make_rsrc(GK == 2 ? static_cast<const char*>(a.gate) + t * gb : nullptr, GK == 2 ? gb : 0u);
-    u32x4 vd[NH], ve[NH], vx[NH], vs[NH];
-    const auto rows = [&](int at, int c) {
-      const uint32_t o = (uint32_t)c * 16u;
-      vd[at] = load_row<HELD>(dr, o);
-      ve[at] = load_row<HELD>(er, o);
-      vx[at] = load_row<HELD>(xr, o);
-      vs[at] = load_row<HELD>(sr, o);
-      if constexpr (GK == 2) {
-        load_weight(gr, a.gate_f32, c, z[at]);
+  struct Chunk {
+    u32x4 d, e, x, s;
+    Raw8 z;
+  };
+  struct Stats {
+    float r1, r2, z;
+  };
+  const auto load = [&](int64_t t, int c) {
+    const auto row = [&](const uint16_t* p) { return make_rsrc(p ? p + t * H : nullptr, p && t < a.T ? row_bytes : 0u); };
+    const uint32_t o = (uint32_t)c * 16u;
+    Chunk k;
+    k.d = load_row<HELD>(row(a.dy), o);
+    k.e = load_row<HELD>(row(a.d_s), o);
+    k.x = load_row<HELD>(row(a.x), o);
+    k.s = load_row<HELD>(row(a.s), o);
+    if constexpr (GK >= 2) k.z = load_raw(make_rsrc(static_cast<const char*>(a.gate) + t * gb, t < a.T ? gb : 0u), GK == 3, c);
+    return k;
+  };
+  const auto stats = [&](int64_t t) {
+    Stats r = {0.f, 0.f, 1.f};
+    if (t < a.T) {
+      if (pre) r.r2 = a.r2[t];
+      if (POST) r.r1 = a.r1[t];
+      if (GK == 0 && a.gate_kind == MOE_GATE_ROW) r.z = load_scalar(a.gate, a.gate_f32, t);
+    }
+    return r;
+  };
+  // the gate of a chunk's values
+  const auto gates = [&](const Chunk& k) {
+    if constexpr (GK >= 2) {
+      unpack_raw(k.z, GK == 3, z[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[at][j] = gate_act(a.act, z[at][j]);
-      }
-    };
-    if constexpr (HELD) rows(0, c0);
-    const float r2 = pre ? a.r2[t] : 0.f;
-    const float r1 = POST ? a.r1[t] : 0.f;
-    float zr = 1.f;
-    if (GK == 0 && a.gate_kind == MOE_GATE_ROW) zr = gate_act(a.act, load_scalar(a.gate, a.gate_f32, t));
+      for (int j = 0; j < 8; ++j) z[0][j] = gate_act(a.act, z[0][j]);
+    }
+  };
+  int odd = 0;
+  const int64_t stride = (int64_t)gridDim.x * ROWS;
+  int64_t t = blockIdx.x + (W == 1 ? (int64_t)wave * gridDim.x : 0);
+  // held rows are loaded while the one before is worked on
+  Chunk held;
+  if constexpr (HELD) held = load(t, c0);
+  Stats st = stats(t);
+  for (; t < a.T; t += stride) {
+    Chunk cur, ahead;
+    const Stats now = st;
+    if constexpr (HELD) {
+      cur = held;
+      ahead = load(t + stride, c0);
+    }
+    st = stats(t + stride);
+    const float r1 = now.r1, r2 = now.r2;
+    const float zr = GK == 0 && a.gate_kind == MOE_GATE_ROW ? gate_act(a.act, now.z) : 1.f;
     float sum[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
-      const int c = c0 + i * kWave, h = HELD ? i : 0;
+      const int c = c0 + i * kWave, h = 0;
       if constexpr (!HELD) {
-        rows(0, c);
+        cur = load(t, c);
         weights(0, c);
       }
-      float d[8], e[8], x[8], s[8];
-      unpack8(vd[h], d);
-      unpack8(ve[h], e);
-      unpack8(vx[h], x);
-      unpack8(vs[h], s);
+      gates(cur);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float k = x[j];
-        if constexpr (POST) k = (x[j] * r1) * wp[h][j];
+        const float d = value(cur.d, j), e = value(cur.e, j), x = value(cur.x, j), s = value(cur.s, j);
+        float k = x;
+        if constexpr (POST) k = (x * r1) * wp[h][j];
         if constexpr (GK != 0) k *= z[h][j];
-        float de = e[j];
+        float de = e;
         if (pre) {
-          const float xs = s[j] * r2, dxs = d[j] * xs;
+          const float xs = s * r2, dxs = d * xs;
           acc[AW][i][j] += dxs;
           sum[0] += dxs * w[h][j];
           sum[2] += k * xs;
-          de += r2 * (d[j] * w[h][j]);
+          de += r2 * (d * w[h][j]);
         }
         sum[1] += k * de;
       }
@@ -315,58 +362,59 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     }
     const __amdgpu_buffer_rsrc_t dxr = make_rsrc(a.dx + t * H, row_bytes);
     const __amdgpu_buffer_rsrc_t drr = make_rsrc(a.d_res ? a.d_res + t * H : nullptr, a.d_res ? row_bytes : 0u);
-    const bool write_gate = GK == 2 && a.d_gate;
+    const bool write_gate = GK >= 2 && a.d_gate;
     const __amdgpu_buffer_rsrc_t dgr =
         make_rsrc(write_gate ? static_cast<char*>(a.d_gate) + t * gb : nullptr, write_gate ? gb : 0u);
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
-      const int c = c0 + i * kWave, h = HELD ? i : 0;
+      const int c = c0 + i * kWave, h = 0;
       if constexpr (!HELD) {
-        rows(0, c);
+        cur = load(t, c);
         weights(0, c);
+        gates(cur);
+      } else {
+        // unpacked anew: what the first pass unpacked would not fit the registers
+        asm volatile("" : "+v"(cur.d), "+v"(cur.e), "+v"(cur.x), "+v"(cur.s));
       }
-      float d[8], e[8], x[8], s[8], o[8], ro[8], dg[8];
-      unpack8(vd[h], d);
-      unpack8(ve[h], e);
-      unpack8(vx[h], x);
-      unpack8(vs[h], s);
+      u32x4 o, ro, dg;
+      float odd_o = 0.f, odd_r = 0.f, odd_g = 0.f;      // values that wait for their neighbours
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float ds = e[j];
-        if (pre) ds += r2 * (d[j] * w[h][j] - (s[j] * r2) * c2);
-        ro[j] = a.res_scale * ds;
+        const float d = value(cur.d, j), e = value(cur.e, j), x = value(cur.x, j), s = value(cur.s, j);
+        float ds = e;
+        if (pre) ds += r2 * (d * w[h][j] - (s * r2) * c2);
+        const float r = a.res_scale * ds;
         const float f = a.branch_scale * (GK == 0 ? zr : z[h][j]);
         const float dp = f * ds;
-        const float xh = POST ? x[j] * r1 : x[j];
+        const float xh = POST ? x * r1 : x;
+        float g = 0.f, v = dp;
         if constexpr (GK != 0) {
-          const float g = a.branch_scale * gate_slope(a.act, z[h][j]) * ds * (POST ? xh * wp[h][j] : xh);
+          g = a.branch_scale * gate_slope(a.act, z[h][j]) * ds * (POST ? xh * wp[h][j] : xh);
           if constexpr (GK == 1) acc[AG][i][j] += g;
-          else dg[j] = g;
         }
         if constexpr (POST) {
           acc[AP][i][j] += dp * xh;
-          o[j] = r1 * (dp * wp[h][j] - xh * c1);
+          v = r1 * (dp * wp[h][j] - xh * c1);
+        }
+        if (j & 1) {
+          o[j >> 1] = pack_bf16x2(odd_o, v);
+          ro[j >> 1] = pack_bf16x2(odd_r, r);
+          if constexpr (GK == 2) dg[j >> 1] = pack_bf16x2(odd_g, g);
         } else {
-          o[j] = dp;
+          odd_o = v;
+          odd_r = r;
+          odd_g = g;
+        }
+        if constexpr (GK == 3) {
+          dg[j & 3] = __builtin_bit_cast(uint32_t, g);
+          if ((j & 3) == 3) store_row<true>(dg, dgr, (uint32_t)c * 32u + (j >> 2) * 16u);
         }
       }
-      store_row<true>(pack8(o), dxr, (uint32_t)c * 16u);
-      store_row<true>(pack8(ro), drr, (uint32_t)c * 16u);
-      if constexpr (GK == 2) {
-        if (a.gate_f32) {
-          u32x4 lo, hi;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            lo[j] = __builtin_bit_cast(uint32_t, dg[j]);
-            hi[j] = __builtin_bit_cast(uint32_t, dg[4 + j]);
-          }
-          store_row<true>(lo, dgr, (uint32_t)c * 32u);
-          store_row<true>(hi, dgr, (uint32_t)c * 32u + 16u);
-        } else {
-          store_row<true>(pack8(dg), dgr, (uint32_t)c * 16u);
-        }
-      }
+      store_row<true>(o, dxr, (uint32_t)c * 16u);
+      store_row<true>(ro, drr, (uint32_t)c * 16u);
+      if constexpr (GK == 2) store_row<true>(dg, dgr, (uint32_t)c * 16u);
     }
+    if constexpr (HELD) held = ahead;
   }
   float* const parts[3] = {a.part_w, POST ? a.part_wp : a.part_gate, a.part_gate};
 #pragma unroll
@@ -441,9 +489,15 @@ template <int W, int CPL>
 static void launch_q(int qf, int64_t rows, hipStream_t s, const SandwichArgs& a) {
   const dim3 block(64 * (W == 1 ? 4 : W));
   const dim3 grid((unsigned)std::min<int64_t>((rows + (W == 1 ? 3 : 0)) / (W == 1 ? 4 : 1), kSandwichMaxBlocks));
-  if (qf == 1) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 1>), grid, block, 0, s, a);
-  else if (qf == 2) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 2>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((sandwich_kernel<W, CPL, 0>), grid, block, 0, s, a);
+  if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_FULL) {
+    if (qf == 1) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 1, true>), grid, block, 0, s, a);
+    else if (qf == 2) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 2, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((sandwich_kernel<W, CPL, 0, true>), grid, block, 0, s, a);
+  } else {
+    if (qf == 1) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 1, false>), grid, block, 0, s, a);
+    else if (qf == 2) hipLaunchKernelGGL((sandwich_kernel<W, CPL, 2, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((sandwich_kernel<W, CPL, 0, false>), grid, block, 0, s, a);
+  }
 }
 
 int launch_sandwich_norm(const SandwichLaunch& l, hipStream_t stream) {
@@ -475,7 +529,7 @@ int launch_sandwich_norm(const SandwichLaunch& l, hipStream_t stream) {
   else if (nch <= 128) launch_q<1, 2>(qf, l.T, stream, a);
   else if (nch <= 256) launch_q<4, 1>(qf, l.T, stream, a);
   else if (nch <= 512) launch_q<4, 2>(qf, l.T, stream, a);
-  else if (nch <= 1024) launch_q<4, 4>(qf, l.T, stream, a);
+  else if (nch <= 1024) launch_q<8, 2>(qf, l.T, stream, a);
   else if (nch <= 2048) launch_q<16, 2>(qf, l.T, stream, a);
   else launch_q<16, 4>(qf, l.T, stream, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
@@ -499,6 +553,14 @@ static void launch_backward(const SandwichBwdArgs& a, int n, hipStream_t s) {
   else if (nch <= 1024) hipLaunchKernelGGL((sandwich_backward_kernel<16, 1, POST, GK>), grid, dim3(1024), 0, s, a);
   else if (nch <= 2048) hipLaunchKernelGGL((sandwich_backward_kernel<16, 2, POST, GK>), grid, dim3(1024), 0, s, a);
   else hipLaunchKernelGGL((sandwich_backward_kernel<16, 4, POST, GK>), grid, dim3(1024), 0, s, a);
+}
+
+template <bool POST>
+static void launch_backward(const SandwichBwdArgs& a, int gk, int n, hipStream_t s) {
+  if (gk == 1) launch_backward<POST, 1>(a, n, s);
+  else if (gk == 2) launch_backward<POST, 2>(a, n, s);
+  else if (gk == 3) launch_backward<POST, 3>(a, n, s);
+  else launch_backward<POST, 0>(a, n, s);
 }
 
 int launch_sandwich_norm_backward(const SandwichBwdLaunch& l, hipStream_t stream) {
@@ -541,16 +603,9 @@ int launch_sandwich_norm_backward(const SandwichBwdLaunch& l, hipStream_t stream
   a.part_wp = sums(l.d_post_weight);
   a.part_gate = channel ? sums(l.d_gate) : nullptr;
   if (n > 0) {
-    const int gk = channel ? 1 : l.cfg.gate == MOE_GATE_FULL ? 2 : 0;
-    if (a.wp) {
-      if (gk == 1) launch_backward<true, 1>(a, n, stream);
-      else if (gk == 2) launch_backward<true, 2>(a, n, stream);
-      else launch_backward<true, 0>(a, n, stream);
-    } else {
-      if (gk == 1) launch_backward<false, 1>(a, n, stream);
-      else if (gk == 2) launch_backward<false, 2>(a, n, stream);
-      else launch_backward<false, 0>(a, n, stream);
-    }
+    const int gk = channel ? 1 : l.cfg.gate == MOE_GATE_FULL ? (a.gate_f32 ? 3 : 2) : 0;
+    if (a.wp) launch_backward<true>(a, gk, n, stream);
+    else launch_backward<false>(a, gk, n, stream);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   }
   if (arrays > 0) {
