@@ -23,21 +23,34 @@
 
 namespace moe {
 
-// 1 / (1 + e^-z) within 3 units in the last place: e^-z = 2^t (1 + ln 2 d) with t = -z log2 e as fp32 rounds it and d what
-// that leaves out, hardware exp2 and reciprocal (a unit each); 0 below 2^-125. expf and a division take 13 instructions more a value: 35 of 43 us
-// without any (1021 x 7168 backward, a gate for each value).
-__device__ inline float sigmoid(float z) {
-  const float c = -__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f);        // 2^t stays finite
+// e^c for |c| <= 87, within 2 units in the last place: 2^t (1 + ln 2 d) with t = c log2 e as fp32 rounds it and d what that
+// leaves out; the hardware's exp2 is good to a unit.
+__device__ inline float exp_of(float c) {
   const float t = c * 0x1.715476p+0f;
   const float d = __builtin_fmaf(c, 0x1.4ae0bep-26f, __builtin_fmaf(c, 0x1.715476p+0f, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  const float f = __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e * d, 0x1.62e430p-1f, e));
+  return __builtin_fmaf(e * d, 0x1.62e430p-1f, e);
+}
+// 1 / (1 + e^-z) within 4 units in the last place, 0 below 2^-125. expf and a division take 13 instructions more a value:
+// 43 us instead of 34 (1021 x 7168 backward, a gate for each value).
+__device__ inline float sigmoid(float z) {
+  const float f = __builtin_amdgcn_rcpf(1.0f + exp_of(-__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f)));
   return z != z ? z : z < -87.0f ? 0.0f : f;
+}
+// tanh z within 4 units: (1 - e^-2|z|) / (1 + e^-2|z|), and below 0.6, where that cancels, five terms of its continued
+// fraction z / (1 + z^2 / (3 + z^2 / (5 + ...))), which leave out 1e-9 of it.
+__device__ inline float tanh_of(float z) {
+  const float u = exp_of(-2.0f * __builtin_fminf(__builtin_fabsf(z), 43.0f)), s = z * z;
+  const bool small = __builtin_fabsf(z) < 0.6f;
+  const float num = small ? z * __builtin_fmaf(s, s + 105.0f, 945.0f) : __builtin_copysignf(1.0f - u, z);
+  const float den = small ? __builtin_fmaf(s, __builtin_fmaf(15.0f, s, 420.0f), 945.0f) : 1.0f + u;
+  const float f = num * __builtin_amdgcn_rcpf(den);
+  return z != z ? z : f;
 }
 // the gate's factor without branch_scale, and its slope
 __device__ inline float gate_act(int act, float z) {
   if (act == MOE_GATE_SIGMOID) return sigmoid(z);
-  if (act == MOE_GATE_TANH) return tanhf(z);
+  if (act == MOE_GATE_TANH) return tanh_of(z);
   return z;
 }
 __device__ inline float gate_slope(int act, float f) {
@@ -72,12 +85,13 @@ __device__ inline float inverse_rms(double ss, int H, double eps) { return (floa
 
 // W waves a row, W = 1: four rows a workgroup; CPL chunks of 8 values a lane. With an 8-bit output the
 // rows in 16 bits pass the caches by, as in the single norm. COLS: the gate is one for each column or value. Gate and weights
-// are loaded before the sums that they wait for.
+// are loaded before the sums that they wait for (333 x 5120: 7.9 us without, 6.0 so), but with the widest rows, which have no
+// registers for them.
 template <int W, int CPL, int QF, bool COLS>
 __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_kernel(SandwichArgs a) {
 #pragma clang fp contract(off)
   constexpr int ROWS = W == 1 ? 4 : 1;
-  constexpr bool NT = QF != 0;
+  constexpr bool NT = QF != 0, EARLY = CPL < 4;
   __shared__ double red[2 * W];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -102,11 +116,12 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     const __amdgpu_buffer_rsrc_t gr =
         make_rsrc(COLS ? static_cast<const char*>(a.gate) + (a.gate_kind == MOE_GATE_FULL ? t * gb : 0) : nullptr, COLS ? gb : 0u);
     Raw8 z[CPL], w[CPL];
+    if constexpr (EARLY)
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) {
-      if constexpr (COLS) z[i] = load_raw(gr, a.gate_f32, c0 + i * kWave);
-      w[i] = load_raw(wpr, a.w_f32, c0 + i * kWave);
-    }
+      for (int i = 0; i < CPL; ++i) {
+        if constexpr (COLS) z[i] = load_raw(gr, a.gate_f32, c0 + i * kWave);
+        w[i] = load_raw(wpr, a.w_f32, c0 + i * kWave);
+      }
     float r1 = 0.f;
     if (a.wp) {
       double ss = 0.0;
@@ -127,6 +142,10 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = c0 + i * kWave;
+      if constexpr (!EARLY) {
+        if constexpr (COLS) z[i] = load_raw(gr, a.gate_f32, c);
+        w[i] = load_raw(wpr, a.w_f32, c);
+      }
       float p[8], b[8];
       unpack8(v[i], p);
       unpack8(r[i], b);
@@ -158,8 +177,9 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       }
     }
     if (!a.w) continue;
+    if constexpr (EARLY)
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) w[i] = load_raw(wr, a.w_f32, c0 + i * kWave);
+      for (int i = 0; i < CPL; ++i) w[i] = load_raw(wr, a.w_f32, c0 + i * kWave);
     ss = row_sum<W>(ss, red, sub, odd);
     odd ^= 1;
     const float r2 = inverse_rms(ss, H, a.eps2);
@@ -170,6 +190,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
       const int c = c0 + i * kWave;
+      if constexpr (!EARLY) w[i] = load_raw(wr, a.w_f32, c);
       float f[8], wf[8];
       unpack8(v[i], f);
       unpack_raw(w[i], a.w_f32, wf);
@@ -222,12 +243,16 @@ __device__ inline void row_sum3(float (&v)[3], float* red, int sub, int odd) {
       for (int k = 0; k < 3; ++k) r[sub * 3 + k] = v[k];
     }
     __syncthreads();
+    // a wave's sum a lane, and 16 lanes' by rotations: read one after another by every lane, 16 waves' would take 48 registers
+    const int w = lane_id() & 15;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] = r[k];
-#pragma unroll
-    for (int i = 1; i < W; ++i)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) v[k] += r[i * 3 + k];
+    for (int k = 0; k < 3; ++k) {
+      float s = w < W ? r[w * 3 + k] : 0.f;
+      s = row_add<0x128>(s);
+      s = row_add<0x124>(s);
+      s = row_add<0x122>(s);
+      v[k] = row_add<0x121>(s);
+    }
   }
 }
 
@@ -237,7 +262,10 @@ __device__ inline void row_sum3(float (&v)[3], float* red, int sub, int odd) {
 template <int W, int CPL, bool POST, int GK>
 __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_backward_kernel(SandwichBwdArgs a) {
   constexpr int ROWS = W == 1 ? 4 : 1;
-  constexpr bool HELD = CPL == 1;         // weights, gate and rows stay in registers
+  constexpr bool HELD = CPL == 1;         // weights, a channel gate and rows stay in registers
+  // The next row is loaded while one is worked on where a CU has but one workgroup (1021 x 7168, a gate a value: 30.4 us
+  // with, 31.7 without; workgroups of 8 waves, 16384 x 4096: 149 and 140)
+  constexpr bool AHEAD = HELD && W == 16;
   constexpr int NACC = 1 + (POST ? 1 : 0) + (GK == 1 ? 1 : 0);
   __shared__ float red[2 * 3 * W];
   __shared__ float s_acc[W == 1 ? 3 : 1][W == 1 ? 64 * 8 : 1];
@@ -251,7 +279,6 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
   const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w, pre ? val_bytes(a.w_f32, H) : 0u);
   const __amdgpu_buffer_rsrc_t wpr = make_rsrc(a.wp, POST ? val_bytes(a.w_f32, H) : 0u);
   const uint32_t gb = val_bytes(a.gate_f32, H);
-  constexpr int NH = HELD ? CPL : 1;
   float acc[NACC][CPL][8];
   constexpr int AW = 0, AP = 1, AG = POST ? 2 : 1;
 #pragma unroll
@@ -260,18 +287,23 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     for (int i = 0; i < CPL; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[k][i][j] = 0.f;
-  float w[NH][8], wp[NH][8], z[NH][8];
+  float w[8], wp[8], z[8];
   const __amdgpu_buffer_rsrc_t gcr = make_rsrc(GK == 1 ? a.gate : nullptr, GK == 1 ? gb : 0u);
-  const auto weights = [&](int at, int c) {
-    load_weight(wr, a.w_f32, c, w[at]);
-    if constexpr (POST) load_weight(wpr, a.w_f32, c, wp[at]);
+  const auto weights = [&](int c) {
+    load_weight(wr, a.w_f32, c, w);
+    if constexpr (POST) load_weight(wpr, a.w_f32, c, wp);
+  };
+  const auto channel = [&](int c) {
     if constexpr (GK == 1) {
-      load_weight(gcr, a.gate_f32, c, z[at]);
+      load_weight(gcr, a.gate_f32, c, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[at][j] = gate_act(a.act, z[at][j]);
+      for (int j = 0; j < 8; ++j) z[j] = gate_act(a.act, z[j]);
     }
   };
-  if constexpr (HELD) weights(0, c0);
+  if constexpr (HELD) {
+    channel(c0);
+    weights(c0);
+  }
   struct Chunk {
     u32x4 d, e, x, s;
     Raw8 z;
@@ -302,50 +334,57 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
   // the gate of a chunk's values
   const auto gates = [&](const Chunk& k) {
     if constexpr (GK >= 2) {
-      unpack_raw(k.z, GK == 3, z[0]);
+      unpack_raw(k.z, GK == 3, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[0][j] = gate_act(a.act, z[0][j]);
+      for (int j = 0; j < 8; ++j) z[j] = gate_act(a.act, z[j]);
     }
   };
   int odd = 0;
   const int64_t stride = (int64_t)gridDim.x * ROWS;
   int64_t t = blockIdx.x + (W == 1 ? (int64_t)wave * gridDim.x : 0);
-  // held rows are loaded while the one before is worked on
-  Chunk held;
-  if constexpr (HELD) held = load(t, c0);
-  Stats st = stats(t);
+  Chunk next;
+  Stats st;
+  if constexpr (AHEAD) {
+    next = load(t, c0);
+    st = stats(t);
+  }
   for (; t < a.T; t += stride) {
     Chunk cur, ahead;
-    const Stats now = st;
-    if constexpr (HELD) {
-      cur = held;
+    Stats now;
+    if constexpr (AHEAD) {
+      cur = next;
       ahead = load(t + stride, c0);
+      now = st;
+      st = stats(t + stride);
+    } else {
+      if constexpr (HELD) cur = load(t, c0);
+      now = stats(t);
     }
-    st = stats(t + stride);
     const float r1 = now.r1, r2 = now.r2;
     const float zr = GK == 0 && a.gate_kind == MOE_GATE_ROW ? gate_act(a.act, now.z) : 1.f;
     float sum[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
-      const int c = c0 + i * kWave, h = 0;
+      const int c = c0 + i * kWave;
       if constexpr (!HELD) {
         cur = load(t, c);
-        weights(0, c);
+        channel(c);
+        weights(c);
       }
       gates(cur);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = value(cur.d, j), e = value(cur.e, j), x = value(cur.x, j), s = value(cur.s, j);
         float k = x;
-        if constexpr (POST) k = (x * r1) * wp[h][j];
-        if constexpr (GK != 0) k *= z[h][j];
+        if constexpr (POST) k = (x * r1) * wp[j];
+        if constexpr (GK != 0) k *= z[j];
         float de = e;
         if (pre) {
           const float xs = s * r2, dxs = d * xs;
           acc[AW][i][j] += dxs;
-          sum[0] += dxs * w[h][j];
+          sum[0] += dxs * w[j];
           sum[2] += k * xs;
-          de += r2 * (d * w[h][j]);
+          de += r2 * (d * w[j]);
         }
         sum[1] += k * de;
       }
@@ -367,10 +406,11 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
         make_rsrc(write_gate ? static_cast<char*>(a.d_gate) + t * gb : nullptr, write_gate ? gb : 0u);
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
-      const int c = c0 + i * kWave, h = 0;
+      const int c = c0 + i * kWave;
       if constexpr (!HELD) {
         cur = load(t, c);
-        weights(0, c);
+        channel(c);
+        weights(c);
         gates(cur);
       } else {
         // unpacked anew: what the first pass unpacked would not fit the registers
@@ -382,19 +422,19 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       for (int j = 0; j < 8; ++j) {
         const float d = value(cur.d, j), e = value(cur.e, j), x = value(cur.x, j), s = value(cur.s, j);
         float ds = e;
-        if (pre) ds += r2 * (d * w[h][j] - (s * r2) * c2);
+        if (pre) ds += r2 * (d * w[j] - (s * r2) * c2);
         const float r = a.res_scale * ds;
-        const float f = a.branch_scale * (GK == 0 ? zr : z[h][j]);
+        const float f = a.branch_scale * (GK == 0 ? zr : z[j]);
         const float dp = f * ds;
         const float xh = POST ? x * r1 : x;
         float g = 0.f, v = dp;
         if constexpr (GK != 0) {
-          g = a.branch_scale * gate_slope(a.act, z[h][j]) * ds * (POST ? xh * wp[h][j] : xh);
+          g = a.branch_scale * gate_slope(a.act, z[j]) * ds * (POST ? xh * wp[j] : xh);
           if constexpr (GK == 1) acc[AG][i][j] += g;
         }
         if constexpr (POST) {
           acc[AP][i][j] += dp * xh;
-          v = r1 * (dp * wp[h][j] - xh * c1);
+          v = r1 * (dp * wp[j] - xh * c1);
         }
         if (j & 1) {
           o[j >> 1] = pack_bf16x2(odd_o, v);
@@ -414,7 +454,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       store_row<true>(ro, drr, (uint32_t)c * 16u);
       if constexpr (GK == 2) store_row<true>(dg, dgr, (uint32_t)c * 16u);
     }
-    if constexpr (HELD) held = ahead;
+    if constexpr (AHEAD) next = ahead;
   }
   float* const parts[3] = {a.part_w, POST ? a.part_wp : a.part_gate, a.part_gate};
 #pragma unroll
