@@ -981,32 +981,16 @@ int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
                    splits > 1 && !parts ? l.v : nullptr, stream);
 }
 
-int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream) {
-  if (!fits(l, l.N, l.K, true)) return MOE_ERR_UNSUPPORTED;
-  // dv's partial results, dv and v in three bf16 numbers each, partial results of dA and dB
-  const int splits = l.T > 0 ? splits_of(l.T, l.N, l.n, block_rows_of(l)) : 1;
-  const int64_t size = (int64_t)l.T * l.R;
-  float* const part = static_cast<float*>(l.ws);
-  uint16_t* const dv = reinterpret_cast<uint16_t*>(part + splits * size);
-  uint16_t* const v = dv + 3 * size;
-  if (l.T > 0) {
-    const bool rows = g.dx || g.da;
-    int rc = rows ? down<true>(l, g.dout, g.ld_dout, l.b, l.scale, l.N, part, stream) : MOE_OK;
-    if (rc != MOE_OK) return rc;
-    rc = make_parts(l, {{part, l.v}, {splits, 1}, {rows ? dv : nullptr, g.db ? v : nullptr}, size, nullptr},
-                    {static_cast<const uint16_t*>(g.dx_base), g.ld_base, static_cast<uint16_t*>(g.dx), g.ld_dx, l.K}, stream);
-    if (rc != MOE_OK) return rc;
-    if (g.dx) rc = up<true>(l, nullptr, 0, dv, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
-    if (rc != MOE_OK) return rc;
-  }
-  if (!g.da && !g.db) return MOE_OK;
+// dA and dB; dv and v in three bf16 numbers each
+static int factor_grads(const AdapterLaunch& l, const AdapterGrads& g, const uint16_t* dv, const uint16_t* v, float* part,
+                        hipStream_t stream) {
   GradArgs a{};
   a.ranks = l.ranks;
   a.n = l.n;
   a.T = l.T;
   a.R = l.R;
   a.rows = adapter_grad_rows(l.T);
-  a.part = reinterpret_cast<float*>(v + 3 * size);
+  a.part = part;
   a.side[0] = {static_cast<const uint16_t*>(l.x), l.ldx, dv, l.K, nullptr, g.da, 0};
   a.side[1] = {static_cast<const uint16_t*>(g.dout), g.ld_dout, v, l.N, l.scale, g.db,
                (int64_t)adapter_grad_slots(l.T) * l.R * l.K};
@@ -1017,15 +1001,38 @@ int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipSt
     a.slabs0 = g.da ? (l.K + kGradCols - 1) / kGradCols : 0;
     a.slabs = a.slabs0 + (g.db ? (l.N + kGradCols - 1) / kGradCols : 0);
     const int rp = l.R <= 16 ? 16 : l.R <= 32 ? 32 : 64;
-    const dim3 grid((unsigned)(a.slabs * grad_chunks(l.T, l.n)), (l.R + rp - 1) / rp);
-    if (rp == 16) hipLaunchKernelGGL(adapter_grad_kernel<1>, grid, dim3(64 * kGradWaves), 0, stream, a);
-    else if (rp == 32) hipLaunchKernelGGL(adapter_grad_kernel<2>, grid, dim3(64 * kGradWaves), 0, stream, a);
-    else hipLaunchKernelGGL(adapter_grad_kernel<4>, grid, dim3(64 * kGradWaves), 0, stream, a);
+    const dim3 grid((unsigned)(a.slabs * grad_chunks(l.T, l.n)), (l.R + rp - 1) / rp), block(64 * kGradWaves);
+    if (rp == 16) hipLaunchKernelGGL(adapter_grad_kernel<1>, grid, block, 0, stream, a);
+    else if (rp == 32) hipLaunchKernelGGL(adapter_grad_kernel<2>, grid, block, 0, stream, a);
+    else hipLaunchKernelGGL(adapter_grad_kernel<4>, grid, block, 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_HIP;
   }
   const int64_t most = (int64_t)l.R * std::max(g.da ? l.K : 0, g.db ? l.N : 0);
   hipLaunchKernelGGL(adapter_join_kernel, dim3((unsigned)((most + kJoinValues - 1) / kJoinValues), l.n), dim3(256), 0, stream, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream) {
+  if (!fits(l, l.N, l.K, true)) return MOE_ERR_UNSUPPORTED;
+  // dv's partial results, dv and v in three bf16 numbers each, partial results of dA and dB
+  const int splits = l.T > 0 ? splits_of(l.T, l.N, l.n, block_rows_of(l)) : 1;
+  const int64_t size = (int64_t)l.T * l.R;
+  float* const part = static_cast<float*>(l.ws);
+  uint16_t* const dv = reinterpret_cast<uint16_t*>(part + splits * size);
+  uint16_t* const v = dv + 3 * size;
+  const bool rows = g.dx || g.da;
+  int rc = MOE_OK;
+  if (l.T > 0) {
+    if (rows) rc = down<true>(l, g.dout, g.ld_dout, l.b, l.scale, l.N, part, stream);
+    if (rc != MOE_OK) return rc;
+    rc = make_parts(l, {{part, l.v}, {splits, 1}, {rows ? dv : nullptr, g.db ? v : nullptr}, size, nullptr},
+                    {static_cast<const uint16_t*>(g.dx_base), g.ld_base, static_cast<uint16_t*>(g.dx), g.ld_dx, l.K}, stream);
+  }
+  // the factors' gradients first: dout is in the Infinity Cache yet
+  if (rc == MOE_OK && (g.da || g.db)) rc = factor_grads(l, g, dv, v, reinterpret_cast<float*>(v + 3 * size), stream);
+  if (rc == MOE_OK && l.T > 0 && g.dx)
+    rc = up<true>(l, nullptr, 0, dv, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
+  return rc;
 }
 
 }  // namespace moe
