@@ -588,6 +588,8 @@ struct GradArgs {
   const int32_t* ranks;
   int32_t n, T, R;
   int32_t rows;          // rows of a chunk
+  int32_t slots;         // places of `part`, for each side
+  int32_t rows_cap;      // of src
   GradSide side[2];      // 0: dA (x, dv), 1: dB (dout, v)
   int32_t slabs0, slabs; // column slabs of side 0, and of both
   float* part;
@@ -648,14 +650,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void adapter_grad_kernel(GradArgs 
   const int n0 = (slab - (db ? a.slabs0 : 0)) * kGradCols;
   const int r0 = blockIdx.y * RP;
   int e, at, slot;
-  if (!find_chunk(a.counts, a.n, a.rows, blockIdx.x / (uint32_t)a.slabs, e, at, slot)) return;
+  if (!find_chunk(a.counts, a.n, a.rows, blockIdx.x / (uint32_t)a.slabs, e, at, slot) || slot >= a.slots) return;
   e = __builtin_amdgcn_readfirstlane(e);
   const int cnt = min(a.rows, a.counts[e] - at * a.rows);
   const int rank = adapter_rank(a.ranks, e, a.R) - r0;
   const int steps = (cnt + kGradStep - 1) / kGradStep;
-  const int32_t* src = a.src + a.offsets[e] + (int64_t)at * a.rows;
+  const int64_t first = a.offsets[e] + (int64_t)at * a.rows;
   for (int i = tid; i < (steps + 8) * kGradStep; i += 64 * kGradWaves) {      // steps past the last: no rows
-    const int t = i < cnt ? src[i] : -1;
+    const int t = i < cnt && (uint64_t)(first + i) < (uint64_t)a.rows_cap ? a.src[first + i] : -1;
     s_src[i] = (uint32_t)t < (uint32_t)a.T ? t : -1;
   }
   __syncthreads();
@@ -771,7 +773,7 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(GradArgs a) {
       slot += readlane(wave_inclusive_scan(k > 1 ? k : 0), 63);
     }
   const int k = a.counts ? (a.counts[e] + a.rows - 1) / a.rows : 0;
-  if (k == 1) return;
+  if (k == 1 || (k > 1 && slot + k > a.slots)) return;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const GradSide& g = a.side[q];
@@ -794,6 +796,7 @@ struct PartsArgs {
   uint16_t* out[2];
   int64_t n;
   float* sum;            // the first array's sums themselves, or null
+  int32_t R;
   int32_t blocks;        // workgroups of that; those behind them copy rows without an adapter
   RowArgs rows;
   CopyArgs io;
@@ -811,7 +814,7 @@ __global__ __launch_bounds__(256) void adapter_parts_kernel(PartsArgs a) {
   f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
 #pragma unroll 8
   for (int s = 1; s < a.splits[k]; ++s) v += *reinterpret_cast<const f32x4*>(part + s * a.n + i);
-  if (a.sum && k == 0) *reinterpret_cast<f32x4*>(a.sum + i) = v;
+  if (a.sum && k == 0 && a.rows.pos[i / a.R] >= 0) *reinterpret_cast<f32x4*>(a.sum + i) = v;   // R % 4 == 0: one row's
   bf16x4 o[3];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -954,6 +957,7 @@ static int up(const AdapterLaunch& l, const float* part, int32_t splits, const u
 
 // u (and another array) in parts, and the rows without an adapter copied (unless nothing is written, or in place)
 static int make_parts(const AdapterLaunch& l, PartsArgs p, const CopyArgs& io, hipStream_t stream) {
+  p.R = l.R;
   p.blocks = (int)((p.n / 4 + 255) / 256);
   p.rows = row_args(l);
   p.io = io;
@@ -990,12 +994,14 @@ static int factor_grads(const AdapterLaunch& l, const AdapterGrads& g, const uin
   a.T = l.T;
   a.R = l.R;
   a.rows = adapter_grad_rows(l.T);
+  a.slots = adapter_grad_slots(l.T);
   a.part = part;
   a.side[0] = {static_cast<const uint16_t*>(l.x), l.ldx, dv, l.K, nullptr, g.da, 0};
   a.side[1] = {static_cast<const uint16_t*>(g.dout), g.ld_dout, v, l.N, l.scale, g.db,
-               (int64_t)adapter_grad_slots(l.T) * l.R * l.K};
+               (int64_t)a.slots * l.R * l.K};
   if (l.T > 0) {
     a.src = l.plan->src;
+    a.rows_cap = (int32_t)l.plan->rows_cap;
     a.offsets = l.plan->offsets;
     a.counts = l.plan->counts;
     a.slabs0 = g.da ? (l.K + kGradCols - 1) / kGradCols : 0;

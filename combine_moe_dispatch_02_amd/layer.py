@@ -423,15 +423,18 @@ class StreamMoE:
         """(w1t, w2t): the transposed, tiled weights the backward data GEMMs read (load time)."""
         return moe_pack_weights_transposed(w1), moe_pack_weights_transposed(w2)
 
-    def backward(self, dout, topk_weights, w1t, w2t, streams=None):
+    def backward(self, dout, topk_weights, w1t, w2t, streams=None, adapters=None):
         """Gradients of the last forward (train=True) for the output gradient dout [T, H]:
         returns (dx [T, H] bf16, d_topk_weights [T, K] fp32, dw1 [E_local, 2I, H], dw2 [E_local, H, I]).
+        With the ``adapters`` of that forward (made with train=True) dx has their share, and their da and db are made.
         y_pool is overwritten by dy. ``streams=(compute, comm)`` mirrors forward(): combine
         backward on comm raises each pool tile's flag as its dy rows land, and the backward GEMMs
         on compute start on flagged tiles (backward Y's grid leaves CUs for combine backward);
         dispatch backward follows on comm. None runs everything on the current stream."""
         if not self.train:
             raise RuntimeError("StreamMoE was built without train=True")
+        if adapters is not None:
+            adapters.check_backward()
         epoch = self.next_epoch()
         dw1 = torch.empty(self.E_local, 2 * self.I, self.H, dtype=torch.bfloat16, device=dout.device)
         dw2 = torch.empty(self.E_local, self.H, self.I, dtype=torch.bfloat16, device=dout.device)
@@ -441,6 +444,8 @@ class StreamMoE:
             moe_expert_ffn_backward(self.plan, self.pool, self.y_pool, self.g_pool, w1t, w2t, epoch, self.ws,
                                     self.dx_pool, dw1, dw2, self.cfg, s)
             moe_dispatch_backward(self.dx_pool, self.plan, self.dx, s)
+            if adapters is not None:
+                adapters.backward(dout, self.dx, stream=s)
             return self.dx, self.dw, dw1, dw2
         compute, comm = streams
         cur = torch.cuda.current_stream()
@@ -453,6 +458,8 @@ class StreamMoE:
         done.record(compute)
         comm.wait_event(done)
         moe_dispatch_backward(self.dx_pool, self.plan, self.dx, comm)
+        if adapters is not None:
+            adapters.backward(dout, self.dx, stream=comm)
         cur.wait_stream(comm)
         return self.dx, self.dw, dw1, dw2
 
@@ -491,17 +498,29 @@ class StreamMoE:
         else:
             moe_dispatch(x, self.plan, self.pool, self.pool_s, epoch, self.ws, self.dtype, stream)
 
-    def decode(self, x, topk_idx, topk_weights, w1, w2, w1_scale, w2_scale) -> torch.Tensor:
+    def _check_adapters(self, adapters, x, adapter_x) -> None:
+        if adapters is None:
+            return
+        rows = x if adapter_x is None else adapter_x
+        if isinstance(rows, tuple) or rows.dtype != torch.bfloat16:
+            raise ValueError("adapters take bf16 rows: adapter_x beside quantised ones")
+        if rows.shape != (adapters.rows.T, self.H) or adapters.a.shape[2] != self.H or adapters.b.shape[1] != self.H:
+            raise ValueError(f"adapters of {adapters.rows.T} rows, {adapters.a.shape[2]} to {adapters.b.shape[1]}, do not match "
+                             f"rows {tuple(rows.shape)} and H = {self.H}")
+
+    def decode(self, x, topk_idx, topk_weights, w1, w2, w1_scale, w2_scale, *, adapters=None,
+               adapter_x=None) -> torch.Tensor:
         """forward() of a few tokens (mxfp4): any number of rows up to min(T, 64), bf16 or (codes,
         scales) as moe_rmsnorm quantises them, through the same prepared weights but without plan and
         pool (moe_expert_ffn_decode), on the current stream. y is not rounded to bf16 before
         combine, so the results differ from forward()'s by that rounding. Returns the first rows
         of the layer's ``out``, which x may not overlap. Calls on one layer share its buffers, as
-        forward()'s do: one at a time, in graphs too."""
+        forward()'s do: one at a time, in graphs too. adapters and adapter_x: as in forward()."""
         from .block import moe_expert_ffn_decode
 
         if self.dtype != "mxfp4":
             raise MoeError("StreamMoE.decode", _abi.MOE_ERR_UNSUPPORTED)
+        rows = x
         x, x_s = x if isinstance(x, tuple) else (x, None)
         if x.shape[0] > self.T:
             raise ValueError(f"{x.shape[0]} rows, the layer was built for {self.T}")
@@ -510,21 +529,27 @@ class StreamMoE:
         if topk_idx.shape[1:] != (self.K,) or w1.shape[0] != self.E_local:
             raise ValueError("topk_idx [rows, K] / w1 [E_local, 2I, H/2] do not match the layer")
         out = self.out[:x.shape[0]]
+        self._check_adapters(adapters, rows, adapter_x)
         moe_expert_ffn_decode(x, x_s, topk_idx, topk_weights, w1, w1_scale, w2, w2_scale, self.decode_ws, out,
                               self.expert_begin)
+        if adapters is not None:
+            adapters.add(rows if adapter_x is None else adapter_x, out)
         return out
 
     def forward(self, x, topk_idx, topk_weights, w1, w2, w1_scale=None, w2_scale=None,
-                streams=None) -> torch.Tensor:
+                streams=None, *, adapters=None, adapter_x=None) -> torch.Tensor:
         """One layer. x is bf16 [T, H] or, in fp8 and mxfp4 mode, rows that are quantised already:
         (codes [T, H], scales) as moe_rmsnorm writes them. Weights and scales come from
         prepare_weights(). ``streams=(compute, comm)`` runs
         plan/dispatch/combine on comm and the FFN on compute, ordered by events, with GEMM A
         claiming pool tiles as dispatch raises their flags (its grid then leaves CUs free for
         dispatch); None runs everything on the current stream. Asynchronous: device errors are
-        reported by check_errors()."""
+        reported by check_errors(). ``adapters`` (an Adapters with K = N = H, its rows set): each row's
+        low-rank adapter of x is added to out, of ``adapter_x`` (bf16 [T, H]) where x is quantised."""
         if topk_idx.dtype != torch.int32:
             topk_idx = topk_idx.to(torch.int32)
+        self._check_adapters(adapters, x, adapter_x)
+        rows = x if adapter_x is None else adapter_x
         epoch = self.next_epoch()
         if streams is None:
             s = torch.cuda.current_stream()
@@ -533,6 +558,8 @@ class StreamMoE:
             if self.combine_on_completion:
                 moe_expert_ffn_combine(self.plan, self.pool, self.pool_s, w1, w1_scale, w2, w2_scale, epoch,
                                        self.ws, self.y_pool, topk_weights, self.out, self.dtype, self.cfg, s)
+                if adapters is not None:
+                    adapters.add(rows, self.out, stream=s)
                 return self.out
             if self.train:
                 moe_expert_ffn_train(self.plan, self.pool, w1, w2, epoch, self.ws, self.y_pool, self.g_pool,
@@ -541,6 +568,8 @@ class StreamMoE:
                 moe_expert_ffn(self.plan, self.pool, self.pool_s, w1, w1_scale, w2, w2_scale, epoch,
                                self.ws, self.y_pool, self.dtype, self.cfg, s)
             moe_combine(self.y_pool, topk_weights, self.plan, self.out, s)
+            if adapters is not None:
+                adapters.add(rows, self.out, stream=s)
             return self.out
         compute, comm = streams
         cur = torch.cuda.current_stream()
@@ -555,6 +584,8 @@ class StreamMoE:
             compute.wait_stream(cur)       # topk_weights and out belong to the caller's stream
             moe_expert_ffn_combine(self.plan, self.pool, self.pool_s, w1, w1_scale, w2, w2_scale, epoch,
                                    self.ws, self.y_pool, topk_weights, self.out, self.dtype, ccfg, compute)
+            if adapters is not None:
+                adapters.add(rows, self.out, stream=compute)
             cur.wait_stream(compute)
             cur.wait_stream(comm)
             return self.out
@@ -568,6 +599,8 @@ class StreamMoE:
         done.record(compute)
         comm.wait_event(done)
         moe_combine(self.y_pool, topk_weights, self.plan, self.out, comm)
+        if adapters is not None:
+            adapters.add(rows, self.out, stream=comm)
         cur.wait_stream(comm)
         return self.out
 
