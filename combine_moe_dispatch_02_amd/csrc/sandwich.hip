@@ -312,23 +312,21 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     float r1, r2, z;
   };
   const auto load = [&](int64_t t, int c) {
-    const auto row = [&](const uint16_t* p) { return make_rsrc(p ? p + t * H : nullptr, p && t < a.T ? row_bytes : 0u); };
+    const auto row = [&](const uint16_t* p) { return make_rsrc(p ? p + t * H : nullptr, p ? row_bytes : 0u); };
     const uint32_t o = (uint32_t)c * 16u;
     Chunk k;
     k.d = load_row<HELD>(row(a.dy), o);
     k.e = load_row<HELD>(row(a.d_s), o);
     k.x = load_row<HELD>(row(a.x), o);
     k.s = load_row<HELD>(row(a.s), o);
-    if constexpr (GK >= 2) k.z = load_raw(make_rsrc(static_cast<const char*>(a.gate) + t * gb, t < a.T ? gb : 0u), GK == 3, c);
+    if constexpr (GK >= 2) k.z = load_raw(make_rsrc(static_cast<const char*>(a.gate) + t * gb, gb), GK == 3, c);
     return k;
   };
   const auto stats = [&](int64_t t) {
     Stats r = {0.f, 0.f, 1.f};
-    if (t < a.T) {
-      if (pre) r.r2 = a.r2[t];
-      if (POST) r.r1 = a.r1[t];
-      if (GK == 0 && a.gate_kind == MOE_GATE_ROW) r.z = load_scalar(a.gate, a.gate_f32, t);
-    }
+    if (pre) r.r2 = a.r2[t];
+    if (POST) r.r1 = a.r1[t];
+    if (GK == 0 && a.gate_kind == MOE_GATE_ROW) r.z = load_scalar(a.gate, a.gate_f32, t);
     return r;
   };
   // the gate of a chunk's values
@@ -353,9 +351,12 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     Stats now;
     if constexpr (AHEAD) {
       cur = next;
-      ahead = load(t + stride, c0);
+      // Behind the last row the last once more. (With a range of no bytes chosen there, t < T ? gb : 0, the compiler took
+      // the choice from the carry of the address's addition, and gates were read from past their end.)
+      const int64_t tn = min(t + stride, (int64_t)a.T - 1);
+      ahead = load(tn, c0);
       now = st;
-      st = stats(t + stride);
+      st = stats(tn);
     } else {
       if constexpr (HELD) cur = load(t, c0);
       now = stats(t);
