@@ -159,16 +159,21 @@ _GATE_ACTS = {"none": _abi.MOE_GATE_IDENTITY, "sigmoid": _abi.MOE_GATE_SIGMOID, 
 
 def _gate(gate: Optional[torch.Tensor], act: str, dev: int, T: int, H: int):
     """(kind, activation, type, shape, address) of a block's gate: [T, 1] a row, [H] a channel, [T, H] a value."""
-    if act not in _GATE_ACTS:
+    code = _GATE_ACTS.get(act)
+    if code is None:
         raise ValueError(f"gate_act {act!r}")
     if gate is None:
-        return _abi.MOE_GATE_NONE, _GATE_ACTS[act], MOE_BF16, None, None
-    dt = _real_dtype(gate, "gate")
-    shape = tuple(gate.shape)
-    kind = {(T, 1): _abi.MOE_GATE_ROW, (H,): _abi.MOE_GATE_CHANNEL, (T, H): _abi.MOE_GATE_FULL}.get(shape)
-    if kind is None:
-        raise ValueError(f"gate has shape {shape}, expected [T, 1], [H] or [T, H]")
-    return kind, _GATE_ACTS[act], dt, shape, _ptr(gate, "gate", dev, shape, gate.dtype)
+        return _abi.MOE_GATE_NONE, code, MOE_BF16, None, None
+    shape = gate.shape
+    if shape == (T, 1):
+        kind = _abi.MOE_GATE_ROW
+    elif shape == (H,):
+        kind = _abi.MOE_GATE_CHANNEL
+    elif shape == (T, H):
+        kind = _abi.MOE_GATE_FULL
+    else:
+        raise ValueError(f"gate has shape {tuple(shape)}, expected [T, 1], [H] or [T, H]")
+    return kind, code, _real_dtype(gate, "gate"), shape, _ptr(gate, "gate", dev, shape, gate.dtype)
 
 
 def _both_weights(post_weight, weight, dev: int, H: int):
@@ -308,6 +313,8 @@ def _rows(t: Optional[torch.Tensor], name: str, dev: int, T: int, width: int):
     """(address, row pitch) of a checked bf16 tensor [T, width] whose rows may be columns of wider ones."""
     if t is None:
         return None, 0
+    if t.dtype is _BF16 and t.get_device() == dev and t.is_contiguous() and t.shape == (T, width):
+        return t.data_ptr(), width
     if t.dtype is not _BF16:
         raise ValueError(f"{name} has dtype {t.dtype}, expected bf16")
     if t.get_device() != dev:

@@ -134,10 +134,12 @@ __device__ u32x4 adapter_zeros[1];              // never written: what is loaded
 typedef const __attribute__((address_space(1))) void* global_ptr;
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// 16 bytes a lane from anywhere to LDS, lane after lane from `to` on. (The host's pass, which has no use for it, refuses 16.)
+// 16 bytes a lane from anywhere to LDS, lane after lane from `to` on; NT: to be read once. (The host's pass, which has no
+// use for it, refuses 16.)
+template <bool NT = false>
 __device__ inline void load_to_lds(const void* from, void* to) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
+  __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, NT ? 2 : 0);
 #endif
 }
 __device__ inline void load_to_lds(__amdgpu_buffer_rsrc_t from, uint32_t at, void* to) {
@@ -181,6 +183,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(DownArgs 
   constexpr int ZB = MB * KC * 2 / 1024, MBK = RP * KC * 2 / 1024;   // DMA blocks of 1 KiB
   constexpr int ZN = (ZB + kDownWaves - 1) / kDownWaves, MN = (MBK + kDownWaves - 1) / kDownWaves;
   constexpr int STAGE = (MB + RP) * KC * 2;
+  constexpr bool NT = MB == 128 && !TRANS;       // many rows of x pass the caches by: 20.7 us without, 16.7 so (8192 x 4096, rank 64);
+                                                 // of dout they are read once more soon, by the gradients
   constexpr int JG = RW < 4 ? RW : 4;            // fragments that are summed over the waves at a time
   // every wave has the same number of loads; with fewer blocks than waves some load the same
   static_assert((ZB % kDownWaves == 0 || kDownWaves % ZB == 0) && (MBK % kDownWaves == 0 || kDownWaves % MBK == 0));
@@ -235,7 +239,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(DownArgs 
 #pragma unroll
     for (int i = 0; i < ZN; ++i) {
       const uint64_t there = reinterpret_cast<uint64_t>(zrow[i] + k0 + zcol[i]), none = reinterpret_cast<uint64_t>(adapter_zeros);
-      load_to_lds(reinterpret_cast<const void*>(k0 < zend[i] ? there : none), stage + (wave + i * kDownWaves) % ZB * 1024);
+      load_to_lds<NT>(reinterpret_cast<const void*>(k0 < zend[i] ? there : none), stage + (wave + i * kDownWaves) % ZB * 1024);
     }
     const uint32_t step = (uint32_t)k0 * (TRANS ? (uint32_t)a.R : 1u) * 2u;
 #pragma unroll
@@ -558,7 +562,13 @@ __global__ __launch_bounds__(64 * kUpWaves, RS <= 2 ? 4 : 2) void adapter_up_ker
     const int ts[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (ts[q] >= 0 && lc < n1) *reinterpret_cast<words*>(a.io.out + ts[q] * a.io.ld_out + lc) = o[q];
+      if (ts[q] >= 0 && lc < n1) {
+        words* to = reinterpret_cast<words*>(a.io.out + ts[q] * a.io.ld_out + lc);
+        // many rows are written past the caches, whose lines the next kernel would have to wait for: 20.5 us
+        // instead of 24.2 for the down kernel behind it, and as long here
+        if constexpr (MB == 128) __builtin_nontemporal_store(o[q], to);
+        else *to = o[q];
+      }
   };
 #pragma unroll
   for (int i = 0; i < MB / 16; ++i) {
