@@ -2,9 +2,10 @@
 
 The residual's addition with the RMS norm and its 8-bit output, the router's choice of
 experts, the dispatch of rows that are quantised already, the expert FFN of a few
-tokens; the norms around a block's gate and residual, and low-rank adapters. Argument marshalling only, as in ``layer``: the caller owns every tensor and the
-calls are asynchronous. All tensors of a call are on one device, which need not be the
-current one; ``stream`` defaults to that device's current stream.
+tokens; the norms around a block's gate and residual, and low-rank adapters. Argument
+marshalling only, as in ``layer``: the caller owns every tensor and the calls are
+asynchronous. All tensors of a call are on one device, which need not be the current one;
+``stream`` defaults to that device's current stream.
 """
 from __future__ import annotations
 

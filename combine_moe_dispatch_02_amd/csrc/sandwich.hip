@@ -10,7 +10,8 @@
 //   the gate is broadcast to, dw = sum over rows of dy xs, dwp = sum over rows of dp xh.
 //
 // Both passes move a few bytes for every value and compute some tens of operations on it: the memory's
-// rate bounds them, and for one row the launch. As in the single norm a row lives in the registers
+// rate bounds them (16384 x 4096 with a channel gate: forward 99 us, 5.4 TB/s, backward 147 + 7, 5.5 TB/s; 1021 x 7168
+// with a gate a value: 20, 32 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
 // of the W waves that share it, and only sums cross lanes. The two sums of squares are in 64
 // bits, so that both statistics are the same fp32 numbers in whatever order they are summed, and
 // products and sums are rounded one by one (no contraction), so that the stream, y and the codes do
@@ -31,8 +32,8 @@ __device__ inline float exp_of(float c) {
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e * d, 0x1.62e430p-1f, e);
 }
-// 1 / (1 + e^-z) within 4 units in the last place, 0 below 2^-125. expf and a division take 13 instructions more a value:
-// 43 us instead of 34 (1021 x 7168 backward, a gate for each value).
+// 1 / (1 + e^-z) within 4 units in the last place, 0 below 2^-125. expf and a division take 13 instructions more a value,
+// 9 us of 43 (1021 x 7168 backward, a gate for each value, before its rows were loaded ahead).
 __device__ inline float sigmoid(float z) {
   const float f = __builtin_amdgcn_rcpf(1.0f + exp_of(-__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f)));
   return z != z ? z : z < -87.0f ? 0.0f : f;

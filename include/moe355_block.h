@@ -2,8 +2,9 @@
  * moe355_block.h -- C ABI of the operators that stand around the MoE layer of moe355.h in a
  * transformer block, in the same library (libmoe355.so): the residual's addition with the
  * RMS norm and its 8-bit output, the router's choice of experts, the dispatch of rows that
- * are 8-bit codes already, and the expert FFN of a few tokens with MXFP4 weights; behind the layer the norm of a
- * block's output with its gate and residual scales, and low-rank adapters of many requests.
+ * are 8-bit codes already, and the expert FFN of a few tokens with MXFP4 weights; behind
+ * the layer the norm of a block's output with its gate and residual scales, and low-rank
+ * adapters of many requests.
  *
  *   serving, one token:  moe_rmsnorm -> (router logits) -> moe_router_topk -> moe_expert_ffn_decode
  *   serving, a prompt:   moe_rmsnorm -> (router logits) -> moe_router_topk -> moe_plan ->
