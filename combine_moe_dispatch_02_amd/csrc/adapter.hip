@@ -130,7 +130,9 @@ struct DownArgs {
 // each. In a stage, 16-byte pieces are permuted within their rows so that fragments are read without bank conflicts;
 // the DMA writes lane after lane, so the permutation is in the source addresses.
 constexpr int kDownWaves = 8;
-constexpr int down_kc(int mb, int rf) { return mb > 32 || rf > 4 ? 128 : 256; }
+// columns of a stage: three of them have to fit, and with more than 32 ranks two workgroups on a CU are worth more than
+// longer stages (300 rows of 16 adapters, 4096 to 4096, rank 64: 17.9 us with 256, 14.3 with 128)
+constexpr int down_kc(int mb, int rf) { return mb > 32 || rf > 2 ? 128 : 256; }
 
 __device__ u32x4 adapter_zeros[1];              // never written: what is loaded for columns and rows that are not there
 
@@ -186,7 +188,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapter_down_kernel(DownArgs 
   constexpr int ZB = MB * KC * 2 / 1024, MBK = RP * KC * 2 / 1024;   // DMA blocks of 1 KiB
   constexpr int ZN = (ZB + kDownWaves - 1) / kDownWaves, MN = (MBK + kDownWaves - 1) / kDownWaves;
   constexpr int STAGE = (MB + RP) * KC * 2;
-  constexpr bool NT = MB == 128 && !TRANS;       // many rows of x pass the caches by: 20.7 us without, 16.7 so (8192 x 4096, rank 64);
+  constexpr bool NT = MB >= 64 && !TRANS;        // many rows of x pass the caches by: 20.7 us without, 16.7 so (8192 x 4096, rank 64);
                                                  // of dout they are read once more soon, by the gradients
   constexpr int JG = RW < 4 ? RW : 4;            // fragments that are summed over the waves at a time
   // every wave has the same number of loads; with fewer blocks than waves some load the same
@@ -569,7 +571,7 @@ __global__ __launch_bounds__(64 * kUpWaves, RS <= 2 ? 4 : 2) void adapter_up_ker
         words* to = reinterpret_cast<words*>(a.io.out + ts[q] * a.io.ld_out + lc);
         // many rows are written past the caches, whose lines the next kernel would have to wait for: 20.5 us
         // instead of 24.2 for the down kernel behind it, and as long here
-        if constexpr (MB == 128) __builtin_nontemporal_store(o[q], to);
+        if constexpr (MB >= 64) __builtin_nontemporal_store(o[q], to);
         else *to = o[q];
       }
   };
@@ -847,9 +849,10 @@ __global__ __launch_bounds__(256) void adapter_parts_kernel(PartsArgs a) {
 // ---------------------------------------------------------------------------------------
 constexpr int64_t kMaxGrid = (1 << 23) - 8;      // workgroups of up to 512 threads: fewer than 2^32 threads
 
-// rows of a block: 128 for many rows in tiles of 128 (with at most 64 ranks), so that an adapter's factors are read for
-// more rows at once
-static int block_rows_of(int32_t T, int32_t tile, int32_t R) { return tile == 16 ? 16 : tile == 128 && R <= 64 && T >= 256 ? 128 : 32; }
+// rows of a block: 128 for many rows in tiles of 128, so that an adapter's factors are read for more rows at once; 64 with
+// more than 64 ranks, of which three stages would not fit (8192 rows of one adapter, 4096 to 4096: rank 128 85 us in blocks of
+// 32, 63 of 64; rank 256 194 and 144)
+static int block_rows_of(int32_t T, int32_t tile, int32_t R) { return tile == 16 ? 16 : tile < 128 || T < 256 ? 32 : R <= 64 ? 128 : 64; }
 // Slices of the long dimension: so many that there are about as many workgroups as CUs, all in one round (64 rows of
 // nearly as many adapters: 8 slices 12.5 us, 4 slices 8.4; 1021 rows in tiles of 16: 11 and 8.5; 8192 rows of 16
 // adapters: 4 slices 31, 2 slices 27).
@@ -908,10 +911,13 @@ static void launch_down(const DownArgs& a, hipStream_t s) {
   const int rp = a.R <= 16 ? 16 : a.R <= 32 ? 32 : a.R <= 64 ? 64 : 128;
   const int x = a.splits > 1 ? a.splits * a.blocks : (a.blocks + 7) / 8 * 8;
   const dim3 grid((unsigned)x, (a.R + rp - 1) / rp), block(64 * kDownWaves);
-  if (rp == 16) hipLaunchKernelGGL((adapter_down_kernel<MB, 1, TRANS>), grid, block, 0, s, a);
-  else if (rp == 32) hipLaunchKernelGGL((adapter_down_kernel<MB, 2, TRANS>), grid, block, 0, s, a);
-  else if (rp == 64) hipLaunchKernelGGL((adapter_down_kernel<MB, 4, TRANS>), grid, block, 0, s, a);
-  else if constexpr (MB <= 32) hipLaunchKernelGGL((adapter_down_kernel<MB, 8, TRANS>), grid, block, 0, s, a);
+  if constexpr (MB != 64) {
+    if (rp == 16) hipLaunchKernelGGL((adapter_down_kernel<MB, 1, TRANS>), grid, block, 0, s, a);
+    else if (rp == 32) hipLaunchKernelGGL((adapter_down_kernel<MB, 2, TRANS>), grid, block, 0, s, a);
+    else if (rp == 64) hipLaunchKernelGGL((adapter_down_kernel<MB, 4, TRANS>), grid, block, 0, s, a);
+  }
+  if constexpr (MB <= 64)
+    if (rp == 128) hipLaunchKernelGGL((adapter_down_kernel<MB, 8, TRANS>), grid, block, 0, s, a);
 }
 
 template <int MB, bool TRANS>
@@ -943,6 +949,7 @@ static int down(const AdapterLaunch& l, const void* z, int64_t ldz, const void* 
   a.splits = splits_of(l.T, K, l.n, mb);
   if (mb == 16) launch_down<16, TRANS>(a, stream);
   else if (mb == 128) launch_down<128, TRANS>(a, stream);
+  else if (mb == 64) launch_down<64, TRANS>(a, stream);
   else launch_down<32, TRANS>(a, stream);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
@@ -992,7 +999,7 @@ int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
   if (rc != MOE_OK) return rc;
   // many rows: v once, in parts, rather than the partial results by every workgroup
   uint16_t* parts = nullptr;
-  if (block_rows_of(l) == 128) {
+  if (block_rows_of(l) >= 64) {
     parts = reinterpret_cast<uint16_t*>(static_cast<float*>(l.ws) + splits * size);
     const int rc = make_parts(l, {{part, nullptr}, {splits, 0}, {parts, nullptr}, size, splits > 1 ? l.v : nullptr},
                               {static_cast<const uint16_t*>(l.base), l.ld_base, static_cast<uint16_t*>(l.out), l.ld_out, l.N}, stream);

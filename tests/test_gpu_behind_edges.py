@@ -39,6 +39,18 @@ def test_widest_and_narrowest(size):
         ad.check_backward(d, o, ad.backward(d, o, plan))
 
 
+@pytest.mark.parametrize("size", [(256, 1, 264, 136, 72), (1021, 3, 520, 264, 128), (2600, 2, 136, 1032, 136), (700, 5, 72, 72, 256)], ids=str)
+def test_many_rows_of_high_ranks(size):
+    """Tiles of 128 with more than 64 ranks: blocks of 64 rows, v in parts."""
+    say("high ranks", size)
+    for ids in ("mixed", "runs"):
+        d = ad.make(*size, ids=ids, ranks=ids == "mixed")
+        plan = ad.make_plan(d, 128)
+        o = ad.forward(d, plan)
+        ad.check_forward(d, o)
+        ad.check_backward(d, o, ad.backward(d, o, plan))
+
+
 def test_ranks_out_of_range():
     d = ad.make(400, 4, 136, 72, 24)
     plan = ad.make_plan(d, 32)
