@@ -332,8 +332,11 @@ def _rows(t: Optional[torch.Tensor], name: str, dev: int, T: int, width: int):
 
 
 def adapter_tile(T: int, n: int) -> int:
-    """The tile of a plan that groups T rows by n adapters: 16, 32 or 128 by how many rows they have each."""
-    return 16 if T < 32 * n else 32 if T < 256 * n else 128
+    """The tile of a plan that groups T rows by n adapters: 16, 32 or 128. Few rows need small tiles for as many workgroups as
+    there are CUs, many share an adapter's factors in large ones (4096 to 4096, ranks 16 and 64, in us: 512 rows of one adapter
+    11 and 13 with 16, 19 and 22 with 128; 3500 of 40 adapters 28 and 46, 29 and 44 with 32, 26 and 33 with 128; 8192 of
+    256: 64 and 126, 65 and 112, 82 and 116)."""
+    return 128 if T >= max(3000, 64 * n) else 32 if T >= 2048 else 16
 
 
 def adapter_workspace_bytes(T: int, K: int, R: int) -> int:

@@ -27,6 +27,11 @@ def test_rows():
     assert moe.AdapterRows(1, 2, train=True, device="cpu").plan is not None
 
 
+def test_tiles():
+    assert [moe.adapter_tile(T, n) for T, n in ((1, 1), (2047, 1), (2048, 1), (2999, 1), (3000, 1), (6399, 100), (6400, 100))] == [
+        16, 16, 32, 32, 128, 32, 128]
+
+
 def test_no_rows():
     rows = moe.AdapterRows(0, 2, train=True, device="cpu")
     assert rows.plan is None
