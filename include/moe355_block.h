@@ -231,8 +231,8 @@ MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R);
  * The rows' adapters: either ids, int32 [T], e = ids[t] - id_begin, for up to 64 rows; or plan,
  * made by moe_plan with K = 1 from such ids ([T][1]), E_local = n and expert_begin in
  * id_begin's place, for any number: one plan serves all projections of a batch. Of
- * its tile only the speed depends: 16 where adapters have few rows each, else 32 or more. Ids
- * outside [0, n) are rows without an adapter.
+ * its tile only the speed depends: 16 for fewer than 2048 rows, 128 for 3000 and 64 an
+ * adapter, else 32. Ids outside [0, n) are rows without an adapter.
  * v: fp32 [T][R] or null: receives v of rows with an adapter (0 past its rank), for
  * moe_adapter_backward. ws: the workspace.
  * Products are exact and summed in fp32, in an order that sizes, and the plan or the ids, fix; v
