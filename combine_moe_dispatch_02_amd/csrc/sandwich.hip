@@ -10,8 +10,8 @@
 //   the gate is broadcast to, dw = sum over rows of dy xs, dwp = sum over rows of dp xh.
 //
 // Both passes move a few bytes for every value and compute some tens of operations on it: the memory's
-// rate bounds them (16384 x 4096 with a channel gate: forward 99 us, 5.4 TB/s, backward 147 + 7, 5.5 TB/s; 1021 x 7168
-// with a gate a value: 20, 32 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
+// rate bounds them (16384 x 4096 with a channel gate: forward 98 us, 5.5 TB/s, backward 143 + 7, 5.6 TB/s; 1021 x 7168
+// with a gate a value: 20, 31 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
 // of the W waves that share it, and only sums cross lanes. The two sums of squares are in 64
 // bits, so that both statistics are the same fp32 numbers in whatever order they are summed, and
 // products and sums are rounded one by one (no contraction), so that the stream, y and the codes do
