@@ -11,7 +11,7 @@
 //
 // Both passes move a few bytes for every value and compute some tens of operations on it: the memory's
 // rate bounds them (16384 x 4096 with a channel gate: forward 98 us, 5.5 TB/s, backward 143 + 7, 5.6 TB/s; 1021 x 7168
-// with a gate a value: 20, 31 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
+// with a gate a value: 21, 31 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
 // of the W waves that share it, and only sums cross lanes. The two sums of squares are in 64
 // bits, so that both statistics are the same fp32 numbers in whatever order they are summed, and
 // products and sums are rounded one by one (no contraction), so that the stream, y and the codes do
@@ -48,7 +48,15 @@ __device__ inline float tanh_of(float z) {
   const float f = num * __builtin_amdgcn_rcpf(den);
   return z != z ? z : f;
 }
-// the gate's factor without branch_scale, and its slope
+// The forward's gate: by the math library's functions and a full division, a unit or two off. What the stream is rounded to hangs on
+// it: with the functions above 40 of 7 million values (1021 x 7168) are rounded to their other neighbour, which
+// the norm weight's gradient shows (3e-6 of it instead of 1e-7). They cost 1.5 of 21 us there.
+__device__ inline float gate_value(int act, float z) {
+  if (act == MOE_GATE_SIGMOID) return 1.0f / (1.0f + expf(-z));
+  if (act == MOE_GATE_TANH) return tanhf(z);
+  return z;
+}
+// the gate's factor without branch_scale in the backward pass, and its slope
 __device__ inline float gate_act(int act, float z) {
   if (act == MOE_GATE_SIGMOID) return sigmoid(z);
   if (act == MOE_GATE_TANH) return tanh_of(z);
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
 #pragma unroll
     for (int i = 0; i < CPL; ++i) r[i] = load_row<NT>(rr, (uint32_t)(c0 + i * kWave) * 16u);
     float row_f = a.branch_scale;
-    if (a.gate_kind == MOE_GATE_ROW) row_f = gate_act(a.act, load_scalar(a.gate, a.gate_f32, t)) * a.branch_scale;
+    if (a.gate_kind == MOE_GATE_ROW) row_f = gate_value(a.act, load_scalar(a.gate, a.gate_f32, t)) * a.branch_scale;
     const uint32_t gb = val_bytes(a.gate_f32, H);
     const __amdgpu_buffer_rsrc_t gr =
         make_rsrc(COLS ? static_cast<const char*>(a.gate) + (a.gate_kind == MOE_GATE_FULL ? t * gb : 0) : nullptr, COLS ? gb : 0u);
@@ -160,7 +168,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
         float zf[8];
         unpack_raw(z[i], a.gate_f32, zf);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = p[j] * (gate_act(a.act, zf[j]) * a.branch_scale);
+        for (int j = 0; j < 8; ++j) p[j] = p[j] * (gate_value(a.act, zf[j]) * a.branch_scale);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] = p[j] * row_f;
