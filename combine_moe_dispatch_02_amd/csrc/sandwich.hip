@@ -24,29 +24,41 @@
 
 namespace moe {
 
-// e^c for |c| <= 87, within 2 units in the last place: 2^t (1 + ln 2 d) with t = c log2 e as fp32 rounds it and d what that
-// leaves out; the hardware's exp2 is good to a unit.
+// 2^S e^c within 2 units in the last place, where that is no denormal and S is 0 or t + S exact: 2^t (1 + ln 2 d) with t = c log2 e
+// as fp32 rounds it and d what that leaves out; the hardware's exp2 is good to a unit.
+template <int S = 0>
 __device__ inline float exp_of(float c) {
+#pragma clang fp contract(off)      // t is to be the rounded one in both places
   const float t = c * 0x1.715476p+0f;
   const float d = __builtin_fmaf(c, 0x1.4ae0bep-26f, __builtin_fmaf(c, 0x1.715476p+0f, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
+  const float e = __builtin_amdgcn_exp2f(t + (float)S);
   return __builtin_fmaf(e * d, 0x1.62e430p-1f, e);
 }
-// 1 / (1 + e^-z) within 4 units in the last place, 0 below 2^-125. expf and a division take 13 instructions more a value,
-// 9 us of 43 (1021 x 7168 backward, a gate for each value, before its rows were loaded ahead).
-__device__ inline float sigmoid(float z) {
-  const float f = __builtin_amdgcn_rcpf(1.0f + exp_of(-__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f)));
-  return z != z ? z : z < -87.0f ? 0.0f : f;
+// A gate's factor f in the backward pass, without branch_scale, and its slope, each within 6 units in the last place. Both are made
+// of one exponential: f (1 - f) of a sigmoid and 1 - f^2 of a tanh would have few or no digits left where the gate is
+// saturated. expf and a division take 13 instructions more a value, 9 us of 43 (1021 x 7168 backward, a
+// gate for each value, before its rows were loaded ahead).
+struct Gate {
+  float f, slope;
+};
+// e = e^-|z|: f = 1 / (1 + e), below zero e / (1 + e), the slope e / (1 + e)^2; e below e^-87 is taken as 0
+__device__ inline Gate sigmoid(float z) {
+  const float x = __builtin_fabsf(z);
+  float e = exp_of(-__builtin_fminf(x, 87.0f));
+  e = z != z ? z : x > 87.0f ? 0.0f : e;
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  return {z < 0.0f ? er : r, er * r};
 }
-// tanh z within 4 units: (1 - e^-2|z|) / (1 + e^-2|z|), and below 0.6, where that cancels, five terms of its continued
-// fraction z / (1 + z^2 / (3 + z^2 / (5 + ...))), which leave out 1e-9 of it.
-__device__ inline float tanh_of(float z) {
-  const float u = exp_of(-2.0f * __builtin_fminf(__builtin_fabsf(z), 43.0f)), s = z * z;
-  const bool small = __builtin_fabsf(z) < 0.6f;
+// u = e^-2|z|: f = (1 - u) / (1 + u), the slope 4 u / (1 + u)^2, taken as 0 below e^-87. Below 0.6, where 1 - u cancels, f is
+// five terms of the continued fraction z / (1 + z^2 / (3 + z^2 / (5 + ...))), which leave out 1e-9 of it, and 1 - f^2 is above 0.7.
+__device__ inline Gate tanh_of(float z) {
+  const float x = __builtin_fabsf(z), s = z * z;
+  const float u4 = x > 44.19f ? 0.0f : exp_of<2>(-2.0f * __builtin_fminf(x, 44.19f)), u = 0.25f * u4;   // t <= -1 (else small): t + 2 is exact
+  const bool small = x < 0.6f;
   const float num = small ? z * __builtin_fmaf(s, s + 105.0f, 945.0f) : __builtin_copysignf(1.0f - u, z);
-  const float den = small ? __builtin_fmaf(s, __builtin_fmaf(15.0f, s, 420.0f), 945.0f) : 1.0f + u;
-  const float f = num * __builtin_amdgcn_rcpf(den);
-  return z != z ? z : f;
+  const float den = small ? __builtin_fmaf(s, __builtin_fmaf(15.0f, s, 420.0f), 945.0f) : z != z ? z : 1.0f + u;
+  const float r = __builtin_amdgcn_rcpf(den), f = num * r;
+  return {f, small ? __builtin_fmaf(-f, f, 1.0f) : (u4 * r) * r};
 }
 // The forward's gate: by the math library's functions and a full division, a unit or two off. What the stream is rounded to hangs on
 // it: with the functions above 40 of 7 million values (1021 x 7168) are rounded to their other neighbour, which
@@ -56,16 +68,10 @@ __device__ inline float gate_value(int act, float z) {
   if (act == MOE_GATE_TANH) return tanhf(z);
   return z;
 }
-// the gate's factor without branch_scale in the backward pass, and its slope
-__device__ inline float gate_act(int act, float z) {
+__device__ inline Gate gate_act(int act, float z) {
   if (act == MOE_GATE_SIGMOID) return sigmoid(z);
   if (act == MOE_GATE_TANH) return tanh_of(z);
-  return z;
-}
-__device__ inline float gate_slope(int act, float f) {
-  if (act == MOE_GATE_SIGMOID) return f * (1.0f - f);
-  if (act == MOE_GATE_TANH) return 1.0f - f * f;
-  return 1.0f;
+  return {z, 1.0f};
 }
 __device__ inline float load_scalar(const void* p, bool f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i] : bf16_lo(static_cast<const uint16_t*>(p)[i]);
@@ -296,7 +302,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     for (int i = 0; i < CPL; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) acc[k][i][j] = 0.f;
-  float w[8], wp[8], z[8];
+  float w[8], wp[8], z[8], slope[8];
   const __amdgpu_buffer_rsrc_t gcr = make_rsrc(GK == 1 ? a.gate : nullptr, GK == 1 ? gb : 0u);
   const auto weights = [&](int c) {
     load_weight(wr, a.w_f32, c, w);
@@ -306,7 +312,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     if constexpr (GK == 1) {
       load_weight(gcr, a.gate_f32, c, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = gate_act(a.act, z[j]);
+      for (int j = 0; j < 8; ++j) z[j] = gate_act(a.act, z[j]).f;
     }
   };
   if constexpr (HELD) {
@@ -338,12 +344,16 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     if (GK == 0 && a.gate_kind == MOE_GATE_ROW) r.z = load_scalar(a.gate, a.gate_f32, t);
     return r;
   };
-  // the gate of a chunk's values
+  // the gate of a chunk's values, and its slopes
   const auto gates = [&](const Chunk& k) {
     if constexpr (GK >= 2) {
       unpack_raw(k.z, GK == 3, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) z[j] = gate_act(a.act, z[j]);
+      for (int j = 0; j < 8; ++j) {
+        const Gate g = gate_act(a.act, z[j]);
+        z[j] = g.f;
+        slope[j] = g.slope;
+      }
     }
   };
   int odd = 0;
@@ -371,7 +381,9 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       now = stats(t);
     }
     const float r1 = now.r1, r2 = now.r2;
-    const float zr = GK == 0 && a.gate_kind == MOE_GATE_ROW ? gate_act(a.act, now.z) : 1.f;
+    Gate row = {1.f, 0.f};
+    if (GK == 0 && a.gate_kind == MOE_GATE_ROW) row = gate_act(a.act, now.z);
+    const float zr = row.f;
     float sum[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < CPL; ++i) {
@@ -405,7 +417,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
     const float kds = sum[1] - (r2 * c2) * sum[2];       // of ds with p, times the gate where that is not one a row
     const float c1 = a.branch_scale * (GK == 0 ? zr : 1.f) * kds / (float)H;
     if (GK == 0 && a.gate_kind == MOE_GATE_ROW && a.d_gate && sub == 0 && lane == 0) {
-      const float dg = a.branch_scale * gate_slope(a.act, zr) * kds;
+      const float dg = a.branch_scale * row.slope * kds;
       if (a.gate_f32) static_cast<float*>(a.d_gate)[t] = dg;
       else static_cast<uint16_t*>(a.d_gate)[t] = (uint16_t)pack_bf16x2(dg, 0.f);
     }
@@ -439,8 +451,9 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
         const float xh = POST ? x * r1 : x;
         float g = 0.f, v = dp;
         if constexpr (GK != 0) {
-          g = a.branch_scale * gate_slope(a.act, z[j]) * ds * (POST ? xh * wp[j] : xh);
-          if constexpr (GK == 1) acc[AG][i][j] += g;
+          const float p = POST ? xh * wp[j] : xh;
+          if constexpr (GK == 1) acc[AG][i][j] += ds * p;
+          else g = a.branch_scale * slope[j] * ds * p;
         }
         if constexpr (POST) {
           acc[AP][i][j] += dp * xh;
@@ -465,6 +478,15 @@ __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwi
       if constexpr (GK == 2) store_row<true>(dg, dgr, (uint32_t)c * 16u);
     }
     if constexpr (AHEAD) next = ahead;
+  }
+  // a channel's slope is the same for all rows
+  if constexpr (GK == 1) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      load_weight(gcr, a.gate_f32, c0 + i * kWave, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[AG][i][j] *= a.branch_scale * gate_act(a.act, z[j]).slope;
+    }
   }
   float* const parts[3] = {a.part_w, POST ? a.part_wp : a.part_gate, a.part_gate};
 #pragma unroll
