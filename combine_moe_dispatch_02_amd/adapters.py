@@ -25,6 +25,7 @@ class AdapterRows:
     def __init__(self, T: int, n: int, *, begin: int = 0, train: bool = False, device="cuda", tile: Optional[int] = None):
         self.T, self.n, self.begin = T, n, begin
         self.ids: Optional[torch.Tensor] = None
+        self.batch = 0                # how often set() has grouped rows
         self.plan: Optional[Plan] = None
         if T > 64 or (train and T > 0):
             tile = adapter_tile(T, n) if tile is None else tile
@@ -34,9 +35,10 @@ class AdapterRows:
     def set(self, ids: torch.Tensor, stream=None) -> "AdapterRows":
         if ids.shape != (self.T,) or ids.dtype != torch.int32:
             raise ValueError(f"ids must be int32 [{self.T}]")
-        self.ids = ids
         if self.plan is not None:
             moe_plan(ids.view(self.T, 1), self.plan, self._ws, stream)
+        self.ids = ids
+        self.batch += 1
         return self
 
     def by(self) -> dict:
@@ -69,23 +71,27 @@ class Adapters:
             self.da = torch.empty(n, R, K, dtype=torch.float32, device=a.device)
             self.db = torch.empty(n, N, R, dtype=torch.float32, device=a.device)
             self._x: Optional[torch.Tensor] = None
+            self._batch = 0           # that of the rows which v is of
 
     def add(self, x: torch.Tensor, base: Optional[torch.Tensor], out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """out = base + each row's adapter of x; out None: in place, into base."""
         out = base if out is None else out
-        if self.train:
-            self._x = x
         moe_adapter(x, self.a, self.b, out, self._ws, base=base, scale=self.scale, ranks=self.ranks,
                     v=self.v if self.train else None, stream=stream, **self.rows.by())
+        if self.train:
+            self._x, self._batch = x, self.rows.batch
         return out
 
     def check_backward(self) -> None:
         if not self.train or self._x is None:
             raise RuntimeError("no add() with train=True to take the gradients of")
+        if self._batch != self.rows.batch:
+            raise RuntimeError("AdapterRows.set() has grouped other rows since the add() whose gradients these would be")
 
     def backward(self, dout: torch.Tensor, dx_base: Optional[torch.Tensor], dx: Optional[torch.Tensor] = None, stream=None) -> None:
         """da, db and dx = dx_base + the adapters' share (dx None: in place, into dx_base; both None: no dx) for the last
-        ``add``, whose x must hold what it held."""
+        ``add``, whose x must hold what it held and whose rows must not have been set again since (with graphs:
+        both captured, or neither)."""
         self.check_backward()
         dx = dx_base if dx is None else dx
         moe_adapter_backward(dout, self._x, self.v, self.a, self.b, self.rows.plan, self._bws, self.da, self.db, dx,
