@@ -458,9 +458,11 @@ class StreamMoE:
         done.record(compute)
         comm.wait_event(done)
         moe_dispatch_backward(self.dx_pool, self.plan, self.dx, comm)
-        if adapters is not None:
-            adapters.backward(dout, self.dx, stream=comm)
-        cur.wait_stream(comm)
+        try:
+            if adapters is not None:
+                adapters.backward(dout, self.dx, stream=comm)
+        finally:
+            cur.wait_stream(comm)
         return self.dx, self.dw, dw1, dw2
 
     def check_errors(self, stream=None) -> None:
@@ -508,6 +510,16 @@ class StreamMoE:
             raise ValueError(f"adapters of {adapters.rows.T} rows, {adapters.a.shape[2]} to {adapters.b.shape[1]}, do not match "
                              f"rows {tuple(rows.shape)} and H = {self.H}")
 
+    def _adapter_rows(self, adapters, x, adapter_x, T):
+        """What adapters are added of in a call of T rows (None without adapters), checked before anything is enqueued."""
+        if adapters is None:
+            return None
+        self._check_adapters(adapters, x, adapter_x)
+        if adapters.rows.T != T:
+            raise ValueError(f"adapters of {adapters.rows.T} rows do not match the call's {T}")
+        adapters.rows.by()
+        return x if adapter_x is None else adapter_x
+
     def decode(self, x, topk_idx, topk_weights, w1, w2, w1_scale, w2_scale, *, adapters=None,
                adapter_x=None) -> torch.Tensor:
         """forward() of a few tokens (mxfp4): any number of rows up to min(T, 64), bf16 or (codes,
@@ -520,7 +532,7 @@ class StreamMoE:
 
         if self.dtype != "mxfp4":
             raise MoeError("StreamMoE.decode", _abi.MOE_ERR_UNSUPPORTED)
-        rows = x
+        rows = self._adapter_rows(adapters, x, adapter_x, (x[0] if isinstance(x, tuple) else x).shape[0])
         x, x_s = x if isinstance(x, tuple) else (x, None)
         if x.shape[0] > self.T:
             raise ValueError(f"{x.shape[0]} rows, the layer was built for {self.T}")
@@ -529,11 +541,10 @@ class StreamMoE:
         if topk_idx.shape[1:] != (self.K,) or w1.shape[0] != self.E_local:
             raise ValueError("topk_idx [rows, K] / w1 [E_local, 2I, H/2] do not match the layer")
         out = self.out[:x.shape[0]]
-        self._check_adapters(adapters, rows, adapter_x)
         moe_expert_ffn_decode(x, x_s, topk_idx, topk_weights, w1, w1_scale, w2, w2_scale, self.decode_ws, out,
                               self.expert_begin)
         if adapters is not None:
-            adapters.add(rows if adapter_x is None else adapter_x, out)
+            adapters.add(rows, out)
         return out
 
     def forward(self, x, topk_idx, topk_weights, w1, w2, w1_scale=None, w2_scale=None,
@@ -548,8 +559,7 @@ class StreamMoE:
         low-rank adapter of x is added to out, of ``adapter_x`` (bf16 [T, H]) where x is quantised."""
         if topk_idx.dtype != torch.int32:
             topk_idx = topk_idx.to(torch.int32)
-        self._check_adapters(adapters, x, adapter_x)
-        rows = x if adapter_x is None else adapter_x
+        rows = self._adapter_rows(adapters, x, adapter_x, self.T)
         epoch = self.next_epoch()
         if streams is None:
             s = torch.cuda.current_stream()
@@ -584,10 +594,12 @@ class StreamMoE:
             compute.wait_stream(cur)       # topk_weights and out belong to the caller's stream
             moe_expert_ffn_combine(self.plan, self.pool, self.pool_s, w1, w1_scale, w2, w2_scale, epoch,
                                    self.ws, self.y_pool, topk_weights, self.out, self.dtype, ccfg, compute)
-            if adapters is not None:
-                adapters.add(rows, self.out, stream=compute)
-            cur.wait_stream(compute)
-            cur.wait_stream(comm)
+            try:
+                if adapters is not None:
+                    adapters.add(rows, self.out, stream=compute)
+            finally:                       # where that raises, the layer is enqueued already
+                cur.wait_stream(compute)
+                cur.wait_stream(comm)
             return self.out
         if self.train:
             moe_expert_ffn_train(self.plan, self.pool, w1, w2, epoch, self.ws, self.y_pool, self.g_pool,
@@ -599,9 +611,11 @@ class StreamMoE:
         done.record(compute)
         comm.wait_event(done)
         moe_combine(self.y_pool, topk_weights, self.plan, self.out, comm)
-        if adapters is not None:
-            adapters.add(rows, self.out, stream=comm)
-        cur.wait_stream(comm)
+        try:
+            if adapters is not None:
+                adapters.add(rows, self.out, stream=comm)
+        finally:
+            cur.wait_stream(comm)
         return self.out
 
     __call__ = forward
