@@ -62,6 +62,7 @@ class Adapters:
         if train and rows.T > 0 and rows.plan is None:
             raise ValueError("gradients need AdapterRows(train=True)")
         self.a, self.b, self.rows, self.scale, self.ranks, self.train = a, b, rows, scale, ranks, train
+        self.added = 0                # calls of add()
         (n, R, K), N = a.shape, b.shape[1]
         u8 = dict(dtype=torch.uint8, device=a.device)
         self._ws = torch.empty(adapter_workspace_bytes(rows.T, K, R), **u8)
@@ -78,6 +79,7 @@ class Adapters:
         out = base if out is None else out
         moe_adapter(x, self.a, self.b, out, self._ws, base=base, scale=self.scale, ranks=self.ranks,
                     v=self.v if self.train else None, stream=stream, **self.rows.by())
+        self.added += 1
         if self.train:
             self._x, self._batch = x, self.rows.batch
         return out

@@ -401,6 +401,7 @@ class StreamMoE:
         self.epoch = 0
         # training: G kept by the forward (replaced by dG in backward), and the backward's buffers
         self.train = train
+        self._added = None       # the adapters of the last forward, how often they were added by then, and whether of x itself
         if train:
             if self.dtype != "bf16" or not self.tiled:
                 raise MoeError("StreamMoE(train=True)", _abi.MOE_ERR_UNSUPPORTED)
@@ -426,7 +427,8 @@ class StreamMoE:
     def backward(self, dout, topk_weights, w1t, w2t, streams=None, adapters=None):
         """Gradients of the last forward (train=True) for the output gradient dout [T, H]:
         returns (dx [T, H] bf16, d_topk_weights [T, K] fp32, dw1 [E_local, 2I, H], dw2 [E_local, H, I]).
-        With the ``adapters`` of that forward (made with train=True) dx has their share, and their da and db are made.
+        With the ``adapters`` of that forward (made with train=True, added of x itself) dx has their share, and their da
+        and db are made; without, they are left out of dx.
         y_pool is overwritten by dy. ``streams=(compute, comm)`` mirrors forward(): combine
         backward on comm raises each pool tile's flag as its dy rows land, and the backward GEMMs
         on compute start on flagged tiles (backward Y's grid leaves CUs for combine backward);
@@ -435,6 +437,10 @@ class StreamMoE:
             raise RuntimeError("StreamMoE was built without train=True")
         if adapters is not None:
             adapters.check_backward()
+            if self._added is None or self._added[0] is not adapters or self._added[1] != adapters.added:
+                raise RuntimeError("not the adapters of the last forward, or they were added elsewhere since")
+            if not self._added[2]:
+                raise RuntimeError("the adapters were added of adapter_x: their share is not one of x's gradient")
         epoch = self.next_epoch()
         dw1 = torch.empty(self.E_local, 2 * self.I, self.H, dtype=torch.bfloat16, device=dout.device)
         dw2 = torch.empty(self.E_local, self.H, self.I, dtype=torch.bfloat16, device=dout.device)
@@ -520,6 +526,11 @@ class StreamMoE:
         adapters.rows.by()
         return x if adapter_x is None else adapter_x
 
+    def _add(self, adapters, rows, x, stream) -> None:
+        adapters.add(rows, self.out, stream=stream)
+        if self.train:                     # x is bf16 then
+            self._added = adapters, adapters.added, rows.data_ptr() == x.data_ptr() and rows.stride() == x.stride()
+
     def decode(self, x, topk_idx, topk_weights, w1, w2, w1_scale, w2_scale, *, adapters=None,
                adapter_x=None) -> torch.Tensor:
         """forward() of a few tokens (mxfp4): any number of rows up to min(T, 64), bf16 or (codes,
@@ -560,6 +571,7 @@ class StreamMoE:
         if topk_idx.dtype != torch.int32:
             topk_idx = topk_idx.to(torch.int32)
         rows = self._adapter_rows(adapters, x, adapter_x, self.T)
+        self._added = None
         epoch = self.next_epoch()
         if streams is None:
             s = torch.cuda.current_stream()
@@ -569,7 +581,7 @@ class StreamMoE:
                 moe_expert_ffn_combine(self.plan, self.pool, self.pool_s, w1, w1_scale, w2, w2_scale, epoch,
                                        self.ws, self.y_pool, topk_weights, self.out, self.dtype, self.cfg, s)
                 if adapters is not None:
-                    adapters.add(rows, self.out, stream=s)
+                    self._add(adapters, rows, x, s)
                 return self.out
             if self.train:
                 moe_expert_ffn_train(self.plan, self.pool, w1, w2, epoch, self.ws, self.y_pool, self.g_pool,
@@ -579,7 +591,7 @@ class StreamMoE:
                                self.ws, self.y_pool, self.dtype, self.cfg, s)
             moe_combine(self.y_pool, topk_weights, self.plan, self.out, s)
             if adapters is not None:
-                adapters.add(rows, self.out, stream=s)
+                self._add(adapters, rows, x, s)
             return self.out
         compute, comm = streams
         cur = torch.cuda.current_stream()
@@ -596,7 +608,7 @@ class StreamMoE:
                                    self.ws, self.y_pool, topk_weights, self.out, self.dtype, ccfg, compute)
             try:
                 if adapters is not None:
-                    adapters.add(rows, self.out, stream=compute)
+                    self._add(adapters, rows, x, compute)
             finally:                       # where that raises, the layer is enqueued already
                 cur.wait_stream(compute)
                 cur.wait_stream(comm)
@@ -613,7 +625,7 @@ class StreamMoE:
         moe_combine(self.y_pool, topk_weights, self.plan, self.out, comm)
         try:
             if adapters is not None:
-                adapters.add(rows, self.out, stream=comm)
+                self._add(adapters, rows, x, comm)
         finally:
             cur.wait_stream(comm)
         return self.out

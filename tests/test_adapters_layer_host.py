@@ -45,7 +45,7 @@ def make_layer(T=4, train=False, on_completion=False, dtype="bf16"):
     e = torch.empty(T, H, dtype=BF16)
     vars(layer).update(T=T, H=H, I=64, K=K, E_local=2, expert_begin=0, dtype=dtype, train=train, combine_on_completion=on_completion,
                        plan=None, ws=None, pool=None, pool_s=None, y_pool=None, g_pool=None, dx_pool=None, dw=None, cfg=None, epoch=0,
-                       decode_ws=None, out=e, dx=e.clone())
+                       decode_ws=None, out=e, dx=e.clone(), _added=None)
     return layer
 
 
@@ -109,3 +109,55 @@ def test_streams_are_joined_where_adapters_fail(log, monkeypatch, train, on_comp
     with pytest.raises(ValueError, match="another device"):
         layer.forward(*inputs(), streams=streams(log), adapters=ad)
     assert log[-1] == "cur waits for comm" and (not on_completion or "cur waits for compute" in log)
+
+
+def backward(layer, ad=None, st=None):
+    return layer.backward(inputs()[0], *inputs()[2:], streams=st, adapters=ad)
+
+
+@pytest.mark.parametrize("two", [False, True])
+def test_backward_takes_the_adapters_of_the_last_forward(log, two):
+    layer, ad, other = make_layer(train=True), make_adapters(train=True), make_adapters(train=True)
+    st = streams(log) if two else None
+    for a in (ad, other):
+        a.add(*2 * [inputs()[0]])                 # each has a batch of its own
+    with pytest.raises(RuntimeError, match="last forward"):
+        backward(layer, ad, st)                   # no forward at all
+    layer.forward(*inputs(), streams=st, adapters=ad)
+    del log[:]
+    with pytest.raises(RuntimeError, match="last forward"):
+        backward(layer, other, st)
+    assert not log
+    backward(layer, ad, st)
+    backward(layer, None, st)                     # their share left out, to be taken by hand
+    ad.add(*2 * [inputs()[0]])                    # something else since: v is of that
+    with pytest.raises(RuntimeError, match="last forward"):
+        backward(layer, ad, st)
+    layer.forward(*inputs(), streams=st, adapters=ad)
+    layer.forward(*inputs(), streams=st)          # without
+    with pytest.raises(RuntimeError, match="last forward"):
+        backward(layer, ad, st)
+
+
+def test_backward_refuses_the_gradient_of_other_rows_than_the_layers(log):
+    layer, ad = make_layer(train=True), make_adapters(train=True)
+    layer.forward(*inputs(), adapters=ad, adapter_x=inputs()[0])
+    with pytest.raises(RuntimeError, match="adapter_x"):
+        backward(layer, ad)                       # one dx cannot be that of two inputs
+    backward(layer)
+    x, *more = inputs()
+    layer.forward(x, *more, adapters=ad, adapter_x=x[:])
+    backward(layer, ad)
+
+
+def test_backward_refuses_where_the_adapters_of_the_last_forward_failed(log, monkeypatch):
+    layer, ad = make_layer(train=True), make_adapters(train=True)
+    layer.forward(*inputs(), adapters=ad)
+
+    def fail(*a, **k):
+        raise ValueError("refused")
+    monkeypatch.setattr(adapters_module, "moe_adapter", fail)
+    with pytest.raises(ValueError):
+        layer.forward(*inputs(), adapters=ad)
+    with pytest.raises(RuntimeError, match="last forward"):
+        backward(layer, ad)
