@@ -46,15 +46,28 @@ __device__ inline bf16x8 read_transposed(const uint8_t* tile, uint32_t at, uint3
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// v as a sum of P bf16 numbers; what rounds to an infinity stays one
-template <int P>
-__device__ inline void split(float v, __bf16 (&o)[P]) {
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    o[p] = (__bf16)v;
-    const float r = (float)o[p];
-    v = __builtin_isinf(r) ? 0.f : v - r;
-  }
+__device__ inline float cut_bf16(float v) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u); }
+
+// v as a sum of two bf16 numbers, each rounded: off by 2^-17 of v at most (the first leaves 2^-8 of v's power of two, 8 bits of which
+// the second has). The first is infinite where v is and not else, and the second 0 there.
+__device__ inline void split(float v, __bf16 (&o)[2]) {
+  o[0] = (__bf16)v;
+  if (__builtin_isinf((float)o[0])) o[0] = (__bf16)cut_bf16(v);
+  const float r = (float)o[0];
+  o[1] = (__bf16)(__builtin_isinf(r) ? 0.f : v - r);
+}
+
+// v as a sum of three, all of its 24 bits: cut off and not rounded, so that the three are of one sign, none of them 0 unless v is,
+// and all infinite where it is. So their products with an infinity or 0 add up to what v's would be, which no sum with parts
+// of 0 or of both signs does. (In a part that v has no bits for stands 2^-32 of v, which is 0 below 2^-101.)
+__device__ inline void split(float v, __bf16 (&o)[3]) {
+  const bool finite = __builtin_fabsf(v) < __builtin_inff();
+  const float none = cut_bf16(v * 0x1p-32f);
+  const float p0 = cut_bf16(v), r = v - p0;
+  const float p1 = cut_bf16(r), q = r - p1;
+  o[0] = (__bf16)(finite ? p0 : v);
+  o[1] = (__bf16)(!finite ? v : r == 0.f ? none : p1);
+  o[2] = (__bf16)(!finite ? v : q == 0.f ? none : q);
 }
 
 struct RowArgs {
@@ -503,6 +516,18 @@ __global__ __launch_bounds__(64 * kUpWaves, RS <= 2 ? 4 : 2) void adapter_up_ker
     wave_sync();
   }
 
+  // Whether m holds an infinity or NaN: a product with zeros shows it. Where u's second part is 0 or of the other sign, an
+  // infinity times both parts is NaN, so what is not finite of such a wave's results is made of the first part alone.
+  bool odd;
+  {
+    f32x4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < RS; ++s)
+#pragma unroll
+      for (int j = 0; j < CF; ++j) z = mfma(bf16x8{}, mf[s][j], z);
+    odd = ballot(z[0] != 0.f) != 0;
+  }
+
   // u as two bf16 numbers each: as they are, or of partial results added in order
   uint8_t* s_u = s_mem;
   __syncthreads();
@@ -529,7 +554,7 @@ __global__ __launch_bounds__(64 * kUpWaves, RS <= 2 ? 4 : 2) void adapter_up_ker
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         __bf16 o[2];
-        split<2>(v[q], o);
+        split(v[q], o);
         hi[q] = o[0];
         lo[q] = o[1];
       }
@@ -553,6 +578,17 @@ __global__ __launch_bounds__(64 * kUpWaves, RS <= 2 ? 4 : 2) void adapter_up_ker
         for (int j = 0; j < CF; ++j) acc[j] = mfma(lo, mf[s][j], acc[j]);
 #pragma unroll
         for (int j = 0; j < CF; ++j) acc[j] = mfma(hi, mf[s][j], acc[j]);
+      }
+    if (odd)
+#pragma unroll
+      for (int j = 0; j < CF; ++j) {
+        f32x4 one = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < RS; ++s)
+          if (s < steps) one = mfma(*reinterpret_cast<const bf16x8*>(&s_u[(i * 16 + l16) * UP + (s * 32 + lhi * 8) * 2]), mf[s][j], one);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (!(__builtin_fabsf(acc[j][q]) < __builtin_inff())) acc[j][q] = one[q];
       }
     words o[4];                                  // row 4 lhi + q
 #pragma unroll
@@ -806,11 +842,13 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(GradArgs a) {
   }
 }
 
-// u[i], the sum of `splits` partial results in order, as three bf16 numbers n apart; of two arrays
+// u[i], the sum of `splits` partial results in order, in bf16 numbers n apart: two for the up kernel and three for the
+// gradients (each null: not wanted); of two arrays
 struct PartsArgs {
   const float* part[2];
   int32_t splits[2];
-  uint16_t* out[2];
+  uint16_t* two[2];
+  uint16_t* three[2];
   int64_t n;
   float* sum;            // the first array's sums themselves, or null
   int32_t R;
@@ -826,22 +864,26 @@ __global__ __launch_bounds__(256) void adapter_parts_kernel(PartsArgs a) {
   }
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int k = blockIdx.y;
-  if (i >= a.n || !a.out[k]) return;
+  if (i >= a.n || !(a.two[k] || a.three[k])) return;
   const float* part = a.part[k];
   f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
 #pragma unroll 8
   for (int s = 1; s < a.splits[k]; ++s) v += *reinterpret_cast<const f32x4*>(part + s * a.n + i);
   if (a.sum && k == 0 && a.rows.pos[i / a.R] >= 0) *reinterpret_cast<f32x4*>(a.sum + i) = v;   // R % 4 == 0: one row's
-  bf16x4 o[3];
+  const auto write = [&]<int P>(uint16_t* out, std::integral_constant<int, P>) {
+    bf16x4 o[P];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    __bf16 b[3];
-    split<3>(v[q], b);
+    for (int q = 0; q < 4; ++q) {
+      __bf16 b[P];
+      split(v[q], b);
 #pragma unroll
-    for (int p = 0; p < 3; ++p) o[p][q] = b[p];
-  }
+      for (int p = 0; p < P; ++p) o[p][q] = b[p];
+    }
 #pragma unroll
-  for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x4*>(a.out[k] + p * a.n + i) = o[p];
+    for (int p = 0; p < P; ++p) *reinterpret_cast<bf16x4*>(out + p * a.n + i) = o[p];
+  };
+  if (a.two[k]) write(a.two[k], std::integral_constant<int, 2>{});
+  if (a.three[k]) write(a.three[k], std::integral_constant<int, 3>{});
 }
 
 // ---------------------------------------------------------------------------------------
@@ -986,7 +1028,7 @@ static int make_parts(const AdapterLaunch& l, PartsArgs p, const CopyArgs& io, h
   p.rows = row_args(l);
   p.io = io;
   const int copies = io.out && io.out != io.base ? copy_blocks(l.T) : 0;
-  hipLaunchKernelGGL(adapter_parts_kernel, dim3((unsigned)(p.blocks + copies), p.out[1] ? 2 : 1), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL(adapter_parts_kernel, dim3((unsigned)(p.blocks + copies), p.three[1] ? 2 : 1), dim3(256), 0, stream, p);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -1001,7 +1043,7 @@ int launch_adapter(const AdapterLaunch& l, hipStream_t stream) {
   uint16_t* parts = nullptr;
   if (block_rows_of(l) >= 64) {
     parts = reinterpret_cast<uint16_t*>(static_cast<float*>(l.ws) + splits * size);
-    const int rc = make_parts(l, {{part, nullptr}, {splits, 0}, {parts, nullptr}, size, splits > 1 ? l.v : nullptr},
+    const int rc = make_parts(l, {{part, nullptr}, {splits, 0}, {parts, nullptr}, {}, size, splits > 1 ? l.v : nullptr},
                               {static_cast<const uint16_t*>(l.base), l.ld_base, static_cast<uint16_t*>(l.out), l.ld_out, l.N}, stream);
     if (rc != MOE_OK) return rc;
   }
@@ -1044,24 +1086,25 @@ static int factor_grads(const AdapterLaunch& l, const AdapterGrads& g, const uin
 
 int launch_adapter_backward(const AdapterLaunch& l, const AdapterGrads& g, hipStream_t stream) {
   if (!fits(l, l.N, l.K, true)) return MOE_ERR_UNSUPPORTED;
-  // dv's partial results, dv and v in three bf16 numbers each, partial results of dA and dB
+  // dv's partial results, dv in two bf16 numbers, dv and v in three each, partial results of dA and dB
   const int splits = l.T > 0 ? splits_of(l.T, l.N, l.n, block_rows_of(l)) : 1;
   const int64_t size = (int64_t)l.T * l.R;
   float* const part = static_cast<float*>(l.ws);
-  uint16_t* const dv = reinterpret_cast<uint16_t*>(part + splits * size);
+  uint16_t* const dv2 = reinterpret_cast<uint16_t*>(part + splits * size);
+  uint16_t* const dv = dv2 + 2 * size;
   uint16_t* const v = dv + 3 * size;
   const bool rows = g.dx || g.da;
   int rc = MOE_OK;
   if (l.T > 0) {
     if (rows) rc = down<true>(l, g.dout, g.ld_dout, l.b, l.scale, l.N, part, stream);
     if (rc != MOE_OK) return rc;
-    rc = make_parts(l, {{part, l.v}, {splits, 1}, {rows ? dv : nullptr, g.db ? v : nullptr}, size, nullptr},
+    rc = make_parts(l, {{part, l.v}, {splits, 1}, {g.dx ? dv2 : nullptr, nullptr}, {g.da ? dv : nullptr, g.db ? v : nullptr}, size, nullptr},
                     {static_cast<const uint16_t*>(g.dx_base), g.ld_base, static_cast<uint16_t*>(g.dx), g.ld_dx, l.K}, stream);
   }
   // the factors' gradients first: dout is in the Infinity Cache yet
   if (rc == MOE_OK && (g.da || g.db)) rc = factor_grads(l, g, dv, v, reinterpret_cast<float*>(v + 3 * size), stream);
   if (rc == MOE_OK && l.T > 0 && g.dx)
-    rc = up<true>(l, nullptr, 0, dv, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
+    rc = up<true>(l, nullptr, 0, dv2, l.a, nullptr, l.K, g.dx_base, g.ld_base, g.dx, g.ld_dx, nullptr, stream);
   return rc;
 }
 

@@ -247,7 +247,7 @@ MOE355_API int moe_adapter(const void* x, int32_t ldx, const void* a, const void
 
 MOE355_API size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t n, int32_t K, int32_t N, int32_t R) {
   if (n < 1 || n > 1024 || N < 8 || N % 8 != 0 || N > kMaxWidth || moe_adapter_workspace_bytes(T, K, R) == 0) return 0;
-  // dv's partial results, dv and v in three 2-byte parts each, partial results of da and db
+  // dv's partial results, dv in two 2-byte parts, dv and v in three each, partial results of da and db
   return moe_adapter_workspace_bytes(T, N, R) + (size_t)T * R * 12 + (size_t)adapter_grad_slots(T) * R * (K + N) * sizeof(float);
 }
 
