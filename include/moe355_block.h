@@ -236,7 +236,8 @@ MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R);
  * v: fp32 [T][R] or null: receives v of rows with an adapter (0 past its rank), for
  * moe_adapter_backward. ws: the workspace.
  * Products are exact and summed in fp32, in an order that sizes, and the plan or the ids, fix; v
- * enters the second product as a sum of two bf16 numbers (off by 2^-18 at most).
+ * enters the second product as a sum of two bf16 numbers (off by 2^-17 at most). Infinities and
+ * NaN give what they give in fp32 products, in their rows and columns alone.
  * Errors: MOE_ERR_INVALID (null or misaligned pointers, n not in [1,1024], T < 0, K, N or R <
  * 8, pitches below the width or no multiples of 8, both or neither of ids and plan, id_begin <
  * 0, a plan of other sizes, small workspace), MOE_ERR_UNSUPPORTED (K, N or R no multiple of 8,
