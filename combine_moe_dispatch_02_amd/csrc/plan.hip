@@ -80,24 +80,31 @@ struct WavePairs {
       e[i] = begin + i * kWave + lane < end && id >= a.expert_begin && x < a.E ? x : -1;
     }
   }
+  // whether all lanes have the same local expert
+  __device__ static bool all_one(int x) {
+    const int first = __builtin_amdgcn_readfirstlane(x);
+    return first >= 0 && ballot(x != first) == 0;
+  }
   // run[e] = the wave's pairs of e. RUNS: neighbouring pairs may well be of one expert (K = 1: rows of adapters, one request
-  // behind another), and 64 additions to one word are 64 steps: 8192 rows in 16 runs 13.4 us so, 8.1 by one addition.
-  // (Looked for where it does not occur, it costs 0.4 us.)
+  // behind another), and 64 additions to one word are 64 steps: 8192 rows in 16 runs 13.0 us so, 7.8 by one addition. A wave looks
+  // for runs at its first and last pairs; a top-1 router's mixed ids pay for that (1024 of 128 experts 6.31 us without, 6.44 with, 7.01 with
+  // every 64 pairs looked at; 8192 of 16 7.35, 7.48 and 7.76).
   template <bool RUNS>
   __device__ void count(const PlanArgs& a, int* run) const {
     for (int x = lane_id(); x < a.E; x += kWave) run[x] = 0;
     wave_sync();
+    if (RUNS && __builtin_expect(all_one(e[0]) || all_one(e[kWaveIters - 1]), 0)) {
 #pragma unroll
-    for (int i = 0; i < kWaveIters; ++i) {
-      if constexpr (RUNS) {
+      for (int i = 0; i < kWaveIters; ++i) {
         const int first = __builtin_amdgcn_readfirstlane(e[i]);
-        if (ballot(e[i] != first) == 0) {
-          if (first >= 0 && lane_id() == 0) atomicAdd(&run[first], kWave);
-          continue;
-        }
+        const bool one = ballot(e[i] != first) == 0;
+        if (one ? (lane_id() == 0 && first >= 0) : e[i] >= 0) atomicAdd(&run[e[i]], one ? kWave : 1);
       }
-      if (e[i] >= 0) atomicAdd(&run[e[i]], 1);
+      return;
     }
+#pragma unroll
+    for (int i = 0; i < kWaveIters; ++i)
+      if (e[i] >= 0) atomicAdd(&run[e[i]], 1);
   }
   // run[e] = the row of the wave's first pair of e
   __device__ void place(const PlanArgs& a, int* run) const {
