@@ -82,6 +82,12 @@ struct RowArgs {
   int32_t key_bits;
 };
 
+// the adapter of row t, told by its id: -1 for none (id - begin itself may leave 32 bits)
+__device__ inline int id_of(const RowArgs& r, int t) {
+  const int id = r.ids[t], x = (int)((uint32_t)id - (uint32_t)r.begin);
+  return id >= r.begin && (uint32_t)x < (uint32_t)r.n ? x : -1;
+}
+
 // The adapter and the rows of block mb (by the whole workgroup): false if there is no such block. rows[i] is -1
 // where the block has fewer than MB.
 template <int MB>
@@ -99,8 +105,8 @@ __device__ inline bool block_rows(const RowArgs& r, int mb, int& e, int* rows) {
   }
   // every wave for itself: a lane a row, the rows of one adapter one group, groups in order of their first rows
   const int lane = lane_id();
-  const int id = lane < r.T ? r.ids[lane] - r.begin : -1;
-  const bool valid = (uint32_t)id < (uint32_t)r.n;
+  const int id = lane < r.T ? id_of(r, lane) : -1;
+  const bool valid = id >= 0;
   const uint64_t peers = match_key((uint32_t)id, valid, r.key_bits);
   const int rank = mask_rank(peers);
   const bool first = valid && rank == 0;
@@ -371,7 +377,7 @@ struct CopyArgs {
   int32_t N;
 };
 __device__ inline void copy_row(const CopyArgs& a, const RowArgs& rows, int t) {
-  if (rows.ids ? (uint32_t)(rows.ids[t] - rows.begin) < (uint32_t)rows.n : rows.pos[t] >= 0) return;
+  if ((rows.ids ? id_of(rows, t) : rows.pos[t]) >= 0) return;
   const uint16_t* from = a.base + t * a.ld_base;
   uint16_t* to = a.out + t * a.ld_out;
   for (int c = lane_id() * 8; c < a.N; c += 8 * 512) {
