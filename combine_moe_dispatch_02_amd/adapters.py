@@ -36,7 +36,10 @@ class AdapterRows:
         if ids.shape != (self.T,) or ids.dtype != torch.int32:
             raise ValueError(f"ids must be int32 [{self.T}]")
         if self.plan is not None:
-            moe_plan(ids.view(self.T, 1), self.plan, self._ws, stream)
+            if ids.device != self.plan.pos.device:
+                raise ValueError(f"ids are on device {ids.device}, the rows on {self.plan.pos.device}")
+            with torch.cuda.device_of(ids):          # need not be the current one
+                moe_plan(ids.view(self.T, 1), self.plan, self._ws, stream)
         self.ids = ids
         self.batch += 1
         return self

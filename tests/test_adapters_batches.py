@@ -93,3 +93,28 @@ def test_a_set_that_failed_leaves_the_grouping(calls, monkeypatch):
     assert rows.ids is first
     ad.backward(out, None)
     assert calls[-1] is x
+
+
+def test_rows_are_grouped_on_their_own_device(calls, monkeypatch):
+    """Not on the current one: moe_plan launches on whatever device is current, on its current stream."""
+    rows, _ = make()
+    inside = []
+
+    class DeviceOf:
+        def __init__(self, t):
+            self.t = t
+
+        def __enter__(self):
+            inside.append(self.t)
+
+        def __exit__(self, *a):
+            inside.append(None)
+
+    monkeypatch.setattr(torch.cuda, "device_of", DeviceOf)
+    monkeypatch.setattr(module, "moe_plan", lambda t, *a: calls.append(inside[-1] if inside else None))
+    mine = ids()
+    rows.set(mine)
+    assert calls[-1] is not None and calls[-1].data_ptr() == mine.data_ptr() and inside[-1] is None
+    with pytest.raises(ValueError, match="device"):
+        rows.set(torch.empty(4, dtype=torch.int32, device="meta"))
+    assert len(calls) == 1
