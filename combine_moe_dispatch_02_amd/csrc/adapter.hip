@@ -12,12 +12,12 @@
 //   up    (v -> out, dv -> dx): contraction over R, v in LDS, the addition in the epilogue;
 //   grad  (dA, dB): contraction over an adapter's rows, in chunks whose partial sums are added in order.
 // All three are a few products for each byte of x, out or their gradients: memory bounds them. 8192 x 4096 in bf16,
-// rank 64, one adapter (a copy of 1 GiB runs at 5.06 TB/s): down 17 us (x at 3.9 TB/s), v into parts 5, up 35 (base and
-// out, 134 MB, and v's parts: 4.3 TB/s), dv 19, the factors' gradients 35 + 7 (134 MB: 3.8 TB/s), dx 35. One row, rank
-// 16: 4.1 + 4.9 us, two launches.
+// rank 64, one adapter (a copy of 1 GiB runs at 5.06 TB/s): down 17 us (x at 3.9 TB/s), v into parts 5.5, up 35 (base and
+// out, 134 MB, and v's parts: 4.3 TB/s), dv 19, parts of both 6, the factors' gradients 35 + 7 (134 MB: 3.8 TB/s), dx 35. One
+// row, rank 16: 4.1 + 4.9 us, two launches.
 //
 // All products run on bf16 MFMA with fp32 sums. v and dv are fp32 and enter the next product as sums of bf16
-// numbers: of two (off by 2^-17 at most, far below the result's rounding to bf16, 2^-9; a third in out and dx costs 8 % of the
+// numbers: of two (off by 2^-17 at most, far below the result's rounding to bf16, 2^-8; a third in out and dx costs 8 % of the
 // forward pass with 64 ranks, 8192 rows, and 60 % with 256), or of three (all of fp32's bits) in the gradients of the
 // factors, whose results stay in fp32.
 #include <algorithm>
@@ -902,9 +902,9 @@ constexpr int64_t kMaxGrid = (1 << 23) - 8;      // workgroups of up to 512 thre
 // more than 64 ranks, of which three stages would not fit (8192 rows of one adapter, 4096 to 4096: rank 128 85 us in blocks of
 // 32, 63 of 64; rank 256 194 and 144)
 static int block_rows_of(int32_t T, int32_t tile, int32_t R) { return tile == 16 ? 16 : tile < 128 || T < 256 ? 32 : R <= 64 ? 128 : 64; }
-// Slices of the long dimension: so many that there are about as many workgroups as CUs, all in one round (64 rows of
-// nearly as many adapters: 8 slices 12.5 us, 4 slices 8.4; 1021 rows in tiles of 16: 11 and 8.5; 8192 rows of 16
-// adapters: 4 slices 31, 2 slices 27).
+// Slices of the long dimension: so many that there are about as many workgroups as CUs, all in one round. Down alone in us, with
+// 2, 3, 4 and 8 slices: 64 rows of nearly as many adapters (rule: 4) 10.3, 8.1, 7.5, 7.6; 1021 rows in tiles of 16 (3) 9.1,
+// 8.6, 8.2, 10.9; 8192 rows of 16 adapters (3) 21.5, 20.0, 25.0, 26.3; of one (4) 21.8, 17.8, 16.7, 22.3.
 static int32_t splits_of(int32_t T, int32_t K, int32_t n, int mb) {
   const int blocks = std::max(1, T <= 64 ? T : (T + mb - 1) / mb + std::min(n, T) / 2);    // half a block more for each adapter
   return std::max(1, std::min((K + 255) / 256, 256 / blocks));

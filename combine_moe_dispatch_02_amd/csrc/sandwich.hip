@@ -10,8 +10,8 @@
 //   the gate is broadcast to, dw = sum over rows of dy xs, dwp = sum over rows of dp xh.
 //
 // Both passes move a few bytes for every value and compute some tens of operations on it: the memory's
-// rate bounds them (16384 x 4096 with a channel gate: forward 98 us, 5.5 TB/s, backward 143 + 7, 5.6 TB/s; 1021 x 7168
-// with a gate a value: 21, 31 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
+// rate bounds them (16384 x 4096 with a channel gate: forward 97 us, 5.6 TB/s, backward 137 + 7, 5.9 TB/s; 1021 x 7168
+// with a gate a value: 21, 30 + 5), and for one row the launch (4.0 us). As in the single norm a row lives in the registers
 // of the W waves that share it, and only sums cross lanes. The two sums of squares are in 64
 // bits, so that both statistics are the same fp32 numbers in whatever order they are summed, and
 // products and sums are rounded one by one (no contraction), so that the stream, y and the codes do
@@ -278,8 +278,9 @@ template <int W, int CPL, bool POST, int GK>
 __global__ __launch_bounds__(W == 16 ? 1024 : 64 * (W == 1 ? 4 : W)) void sandwich_backward_kernel(SandwichBwdArgs a) {
   constexpr int ROWS = W == 1 ? 4 : 1;
   constexpr bool HELD = CPL == 1;         // weights, a channel gate and rows stay in registers
-  // The next row is loaded while one is worked on where a CU has but one workgroup (1021 x 7168, a gate a value: 30.4 us
-  // with, 31.7 without; workgroups of 8 waves, 16384 x 4096: 149 and 140)
+  // The next row is loaded while one is worked on where a CU has but one workgroup (8192 x 7168, a gate a value, both
+  // launches: 188 us with, 191 without; 1021 rows, four a workgroup with the last loaded once more, 36.1 and 35.0). With workgroups of 8
+  // waves it costs (16384 x 4096: 154 with, 149 without).
   constexpr bool AHEAD = HELD && W == 16;
   constexpr int NACC = 1 + (POST ? 1 : 0) + (GK == 1 ? 1 : 0);
   __shared__ float red[2 * 3 * W];
