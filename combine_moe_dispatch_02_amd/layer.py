@@ -428,7 +428,7 @@ class StreamMoE:
         """Gradients of the last forward (train=True) for the output gradient dout [T, H]:
         returns (dx [T, H] bf16, d_topk_weights [T, K] fp32, dw1 [E_local, 2I, H], dw2 [E_local, H, I]).
         With the ``adapters`` of that forward (made with train=True, added of x itself) dx has their share, and their da
-        and db are made; without, they are left out of dx.
+        and db are made; without, they are left out of dx. On one rank of several, as in forward().
         y_pool is overwritten by dy. ``streams=(compute, comm)`` mirrors forward(): combine
         backward on comm raises each pool tile's flag as its dy rows land, and the backward GEMMs
         on compute start on flagged tiles (backward Y's grid leaves CUs for combine backward);
@@ -538,7 +538,7 @@ class StreamMoE:
         pool (moe_expert_ffn_decode), on the current stream. y is not rounded to bf16 before
         combine, so the results differ from forward()'s by that rounding. Returns the first rows
         of the layer's ``out``, which x may not overlap. Calls on one layer share its buffers, as
-        forward()'s do: one at a time, in graphs too. adapters and adapter_x: as in forward()."""
+        forward()'s do: one at a time, in graphs too. adapters and adapter_x: as in forward(), on one rank of several."""
         from .block import moe_expert_ffn_decode
 
         if self.dtype != "mxfp4":
@@ -567,7 +567,9 @@ class StreamMoE:
         claiming pool tiles as dispatch raises their flags (its grid then leaves CUs free for
         dispatch); None runs everything on the current stream. Asynchronous: device errors are
         reported by check_errors(). ``adapters`` (an Adapters with K = N = H, its rows set): each row's
-        low-rank adapter of x is added to out, of ``adapter_x`` (bf16 [T, H]) where x is quantised."""
+        low-rank adapter of x is added to out, of ``adapter_x`` (bf16 [T, H]) where x is quantised. That is their
+        whole share: where the experts are spread over ranks and the ranks' outs are summed, one of the ranks passes them (in
+        backward too), or Adapters.add adds them to the sum."""
         if topk_idx.dtype != torch.int32:
             topk_idx = topk_idx.to(torch.int32)
         rows = self._adapter_rows(adapters, x, adapter_x, self.T)
