@@ -20,7 +20,8 @@ __all__ = ["AdapterRows", "Adapters"]
 class AdapterRows:
     """Which adapter each of a batch's rows has: ``ids`` int32 [T], -1 (or any id outside
     [begin, begin + n)) for none. ``set`` is called once for a batch, before its projections; without
-    gradients up to 64 rows need no more than the ids, others are grouped by moe_plan."""
+    gradients up to 64 rows need no more than the ids, others are grouped by moe_plan. ``ids`` is read by set() in the second case
+    and by every later call in the first: it is left unchanged until the batch is done. One batch at a time, in graphs too."""
 
     def __init__(self, T: int, n: int, *, begin: int = 0, train: bool = False, device="cuda", tile: Optional[int] = None):
         self.T, self.n, self.begin = T, n, begin
@@ -54,7 +55,9 @@ class AdapterRows:
 class Adapters:
     """a bf16 [n, R, K], b bf16 [n, N, R], scale fp32 [n], ranks int32 [n] (both optional) of one projection,
     for batches of ``rows`` (an AdapterRows). With train=True, ``add`` keeps what ``backward`` takes, and ``da`` and
-    ``db`` (fp32) receive the gradients."""
+    ``db`` (fp32) receive the gradients. All calls share the workspaces, v, da and db: one at a time, in graphs too, and of
+    several ``add`` calls the last has its gradients; layers that run at once, or whose backward passes come after both forward
+    passes, have an Adapters each."""
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, rows: AdapterRows, *, scale: Optional[torch.Tensor] = None,
                  ranks: Optional[torch.Tensor] = None, train: bool = False):
