@@ -345,6 +345,17 @@ def make_streams(device=None) -> Tuple[torch.cuda.Stream, torch.cuda.Stream]:
     return torch.cuda.Stream(device=device), torch.cuda.Stream(device=device)
 
 
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the bytes from the first to the last element of two tensors meet."""
+    ends = []
+    for t in (a, b):
+        if t.numel() == 0:
+            return False
+        last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+        ends.append((t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()))
+    return a.device == b.device and ends[0][0] < ends[1][1] and ends[1][0] < ends[0][1]
+
+
 class StreamMoE:
     """Buffers of one layer shape, and the four calls in order.
 
@@ -441,6 +452,8 @@ class StreamMoE:
                 raise RuntimeError("not the adapters of the last forward, or they were added elsewhere since")
             if not self._added[2]:
                 raise RuntimeError("the adapters were added of adapter_x: their share is not one of x's gradient")
+            if _overlap(dout, self.dx):
+                raise ValueError("dout overlaps the layer's dx, which is written before the adapters read dout")
         epoch = self.next_epoch()
         dw1 = torch.empty(self.E_local, 2 * self.I, self.H, dtype=torch.bfloat16, device=dout.device)
         dw2 = torch.empty(self.E_local, self.H, self.I, dtype=torch.bfloat16, device=dout.device)
@@ -524,7 +537,10 @@ class StreamMoE:
         if adapters.rows.T != T:
             raise ValueError(f"adapters of {adapters.rows.T} rows do not match the call's {T}")
         adapters.rows.by()
-        return x if adapter_x is None else adapter_x
+        rows = x if adapter_x is None else adapter_x
+        if _overlap(rows, self.out[:T]):
+            raise ValueError("the adapters' rows overlap the layer's out, which is written before they are read")
+        return rows
 
     def _add(self, adapters, rows, x, stream) -> None:
         adapters.add(rows, self.out, stream=stream)
@@ -567,7 +583,8 @@ class StreamMoE:
         claiming pool tiles as dispatch raises their flags (its grid then leaves CUs free for
         dispatch); None runs everything on the current stream. Asynchronous: device errors are
         reported by check_errors(). ``adapters`` (an Adapters with K = N = H, its rows set): each row's
-        low-rank adapter of x is added to out, of ``adapter_x`` (bf16 [T, H]) where x is quantised. That is their
+        low-rank adapter of x is added to out, of ``adapter_x`` (bf16 [T, H]) where x is quantised;
+        these rows may not overlap the layer's out. That is their
         whole share: where the experts are spread over ranks and the ranks' outs are summed, one of the ranks passes them (in
         backward too), or Adapters.add adds them to the sum."""
         if topk_idx.dtype != torch.int32:

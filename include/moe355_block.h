@@ -227,7 +227,7 @@ MOE355_API size_t moe_adapter_workspace_bytes(int32_t T, int32_t K, int32_t R);
  * of b[e] (taken into [0, R]), the others are not looked at and may hold anything.
  * x: bf16 [T][K], base and out: bf16 [T][N], with row pitches ldx, ld_base, ld_out in elements
  * (multiples of 8), so that they may be columns of wider arrays. out may be base (same
- * pitch): rows without an adapter then stay as they are.
+ * pitch): rows without an adapter then stay as they are. Apart from that out and v overlap no input.
  * The rows' adapters: either ids, int32 [T], e = ids[t] - id_begin, for up to 64 rows; or plan,
  * made by moe_plan with K = 1 from such ids ([T][1]), E_local = n and expert_begin in
  * id_begin's place, for any number: one plan serves all projections of a batch. Of
@@ -259,7 +259,7 @@ MOE355_API size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t n, int
  *   db[e] = scale[e] * sum over its rows of dout[t] v[t]^T       fp32 [n][N][R]
  * dout: bf16 [T][N], the gradient of out (and, as it is, of base); v as moe_adapter wrote it;
  * dx_base: the shared projection's own dx, or null (zeros); dx may be dx_base (same pitch; rows
- * without an adapter then stay as they are). dx, da and db may each be null, not all; x is needed
+ * without an adapter then stay as they are), and overlaps nothing else. dx, da and db may each be null, not all; x is needed
  * for da, v for db. da and db are written, not added to, zeros past an adapter's rank and for
  * adapters without rows; with T = 0 (plan null) they are zero-filled. Sums run in orders that sizes and
  * plan fix. ids, ranks, scale and pitches as in moe_adapter.

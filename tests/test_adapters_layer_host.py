@@ -161,3 +161,28 @@ def test_backward_refuses_where_the_adapters_of_the_last_forward_failed(log, mon
         layer.forward(*inputs(), adapters=ad)
     with pytest.raises(RuntimeError, match="last forward"):
         backward(layer, ad)
+
+
+@pytest.mark.parametrize("two", [False, True])
+def test_rows_that_the_layer_overwrites_before_the_adapters_read_them(log, two):
+    """forward() without adapters takes the layer's own out as x; adapters would read what it has become."""
+    layer, ad = make_layer(train=True), make_adapters(train=True)
+    st = streams(log) if two else None
+    x, *more = inputs()
+    wide = torch.empty(4, 2 * H, dtype=BF16)
+    layer.out = wide[:, :H]
+    layer.forward(layer.out, *more, streams=st)
+    del log[:]
+    for rows, other in ((layer.out, None), (x, layer.out), (x, wide[:, 8:8 + H])):
+        with pytest.raises(ValueError, match="overlap"):
+            layer.forward(rows, *more, streams=st, adapters=ad, adapter_x=other)
+    assert not log
+    layer.forward(x, *more, streams=st, adapters=ad)
+    with pytest.raises(ValueError, match="overlap"):
+        layer.backward(layer.dx, *inputs()[2:], streams=st, adapters=ad)
+    layer.backward(layer.dx, *inputs()[2:], streams=st)
+    decoder = make_layer(dtype="mxfp4")
+    with pytest.raises(ValueError, match="overlap"):
+        decoder.decode(x, *more, None, None, adapters=make_adapters(), adapter_x=decoder.out)
+    few = [t[:2] for t in (x, *more[:2])]
+    decoder.decode(*few, *more[2:], None, None, adapters=make_adapters(2), adapter_x=decoder.out[2:])
