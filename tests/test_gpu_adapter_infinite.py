@@ -4,7 +4,6 @@ import numpy as np
 import pytest
 import torch
 
-import combine_moe_dispatch_02_amd as moe
 import test_gpu_adapter as ad
 
 from _gpu import say
@@ -27,12 +26,6 @@ def make(T, n, K, N, R, seed=0):
 
 def plan_of(d, tile):
     return None if tile is None else ad.make_plan(d, tile)
-
-
-def same_where_finite(got, ref, cells):
-    keep = torch.ones(got.shape, dtype=torch.bool, device="cuda")
-    keep[cells] = False
-    assert torch.equal(got[keep], ref[keep])
 
 
 SIZES = [(40, 3, 64, 136, 24, None), (64, 2, 264, 520, 64, None), (300, 3, 136, 264, 16, 16), (400, 2, 136, 264, 40, 128), (600, 2, 264, 136, 64, 128),
@@ -138,7 +131,7 @@ def test_infinite_values_in_the_backward_pass(size, sign):
 @pytest.mark.parametrize("tile", [None, 128])
 def test_largest_finite_v(tile):
     """v that a bf16 rounding would make infinite: x 2^127 times 1 + 255/256 and more."""
-    T, n, K, N, R = (8, 1, 16, 64, 8, ) if tile is None else (300, 1, 16, 64, 8)
+    T, n, K, N, R = (8, 1, 16, 64, 8) if tile is None else (300, 1, 16, 64, 8)
     d = ad.make(T, n, K, N, R, ids=[0] * T)
     d["x"].zero_(), d["a"].zero_(), d["b"].fill_(0), d["base"].zero_()
     d["scale"] = torch.ones(1, device="cuda")
